@@ -14,7 +14,9 @@ from ._binding import (  # noqa: F401
     zs_shard_load_resharded, ZS_EIO, zs_adamw_step_host, zs_offload_step, zs_stream_ceiling,
     zs_hbm_probe, ZS_PROBE_READ, ZS_PROBE_WRITE, ZS_PROBE_COPY, ZS_PROBE_TRIAD, PackTable,
     zs_step_pipelined_static, ZS_W_STREAM, ZS_W_KEEP, zs_adamw_step_timed,
-    zs_stream_ceiling_timed,
+    zs_stream_ceiling_timed, MultiTable, zs_adamw_multi, zs_grad_norm, zs_clip_coef,
+    zs_state8_layout, zs_state8_encode, zs_state8_decode, zs_quantize_mx4, zs_gather_unit_mx4,
+    ZS_STATE_NONE, ZS_STATE_F32, ZS_STATE_8BIT, ZS_STATE8_M, ZS_STATE8_V, ZS_NORM_WORKSPACE,
 )
 
 __all__ = [
@@ -25,4 +27,8 @@ __all__ = [
     "ZS_PROBE_READ", "ZS_PROBE_WRITE", "ZS_PROBE_COPY", "ZS_PROBE_TRIAD",
     "zs_gather_unit", "zs_step_pipelined", "zs_last_error", "zs_abi_version", "AdamWHP", "ZsError",
     "ZS_BF16", "ZS_F32", "ZS_MAX_D", "load", "PackTable", "zs_step_pipelined_static",
+    "MultiTable", "zs_adamw_multi", "zs_grad_norm", "zs_clip_coef", "zs_state8_layout",
+    "zs_state8_encode", "zs_state8_decode", "zs_quantize_mx4", "zs_gather_unit_mx4",
+    "ZS_STATE_NONE", "ZS_STATE_F32", "ZS_STATE_8BIT", "ZS_STATE8_M", "ZS_STATE8_V",
+    "ZS_NORM_WORKSPACE",
 ]

@@ -41,12 +41,26 @@ class zs_bucket(ctypes.Structure):
 
 
 ZS_W_STREAM, ZS_W_KEEP = 0, 1
+ZS_STATE_NONE, ZS_STATE_F32, ZS_STATE_8BIT = 0, 1, 2
+ZS_STATE8_M, ZS_STATE8_V = 0, 1
+ZS_NORM_WORKSPACE = 32768
 
 
 class zs_reduce_opts(ctypes.Structure):
     _fields_ = [("replicas", ctypes.c_int32), ("round_to_reduce_dtype", ctypes.c_int32),
                 ("scale", ctypes.c_double), ("working_shard_hint", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class zs_multi_tensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("w_out", ctypes.c_void_p), ("g", ctypes.c_void_p), ("numel", ctypes.c_int64)]
+
+
+class zs_round_opts(ctypes.Structure):
+    _fields_ = [("stochastic", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("seed", ctypes.c_uint64)]
 
 
 class zs_shard_info(ctypes.Structure):
@@ -120,6 +134,17 @@ def load() -> ctypes.CDLL:
                                             P(zs_adamw_hp), vp, vp]),
                 "zs_step_pipelined_static": (i32, [P(zs_bucket), i32, i32, i32,
                                                    P(zs_adamw_hp), vp, vp]),
+                "zs_multi_create": (i32, [P(zs_multi_tensor), i32, i32, i32, P(vp)]),
+                "zs_multi_image": (i32, [vp, P(vp), P(i64)]),
+                "zs_multi_destroy": (i32, [vp]),
+                "zs_adamw_multi": (i32, [vp, vp, P(zs_adamw_hp), vp, P(zs_round_opts), vp]),
+                "zs_state8_layout": (i32, [P(i64), i32, P(i64)]),
+                "zs_state8_encode": (i32, [vp, i64, i32, vp, vp, vp]),
+                "zs_state8_decode": (i32, [vp, vp, i64, i32, i32, vp, vp]),
+                "zs_grad_norm": (i32, [vp, vp, ctypes.c_double, vp, vp, vp, vp]),
+                "zs_clip_coef": (i32, [P(vp), i32, ctypes.c_double, vp, vp]),
+                "zs_quantize_mx4": (i32, [vp, i32, i64, vp, vp, vp]),
+                "zs_gather_unit_mx4": (i32, [P(vp), P(vp), i32, i64, i32, vp, vp]),
                 "zs_last_error": (ctypes.c_char_p, []),
                 "zs_abi_version": (i32, []),
             }
@@ -642,6 +667,255 @@ def zs_stream_ceiling_timed(p, m, v, w, contribs: Sequence, start, stop, stream=
     ptrs, S, arr, n, code = _ceiling_args(p, m, v, w, contribs)
     _check(load().zs_stream_ceiling_timed(*ptrs, S, arr, n, code, _event_handle(start, "start"),
                                           _event_handle(stop, "stop"), _stream(p, stream)))
+
+
+# ------------------------------------------------------- many tensors at once
+def _same_device(ts: Sequence, what: str):
+    if len({t.device for t in ts}) > 1:
+        raise ValueError(f"{what}: every tensor must be on one device")
+
+
+def _on(t):
+    """The tensor's device as the current one: kernels go to its streams."""
+    return _torch().cuda.device(t.device)
+
+
+def _typed(t, what: str, dtype, numel=None):
+    _dev(t, what)
+    if t.dtype != dtype or (numel is not None and t.numel() != numel):
+        size = "" if numel is None else f" with {numel} elements"
+        raise ValueError(f"{what} must be {str(dtype).replace('torch.', '')}{size}")
+    return t
+
+
+class MultiTable:
+    """The tensors of zs_adamw_multi and zs_grad_norm, checked once by the
+    library: gradients (all bf16 or all fp32) and, for the step, parameters p
+    (float32), moments m and v and optionally working copies w (bf16), one
+    each per gradient and contiguous. Moments are float32, or uint8 codes with
+    m_scale and v_scale (uint8, ceil(numel / 256) each: zs_state8_layout). It
+    holds the tensors, whose addresses it has given to the device: new tensors
+    (gradients that were reallocated, too) need a new table."""
+
+    def __init__(self, p: Sequence = None, m: Sequence = None, v: Sequence = None,
+                 grads: Sequence = (), w: Sequence = None, m_scale: Sequence = None,
+                 v_scale: Sequence = None, device=None):
+        import numpy as np
+        torch = _torch()
+        self._multi = None
+        grads = list(grads)
+        T = len(grads)
+        lists = dict(p=p, m=m, v=v, m_scale=m_scale, v_scale=v_scale, w_out=w)
+        lists = {k: list(x) for k, x in lists.items() if x is not None}
+        for k, x in lists.items():
+            if len(x) != T:
+                raise ValueError(f"{k} must hold one tensor per gradient ({T})")
+        numels = [g.numel() for g in grads]
+        self.numels = numels
+        if not lists:
+            self.state = ZS_STATE_NONE
+        elif not {"p", "m", "v"} <= set(lists):
+            raise ValueError("a step's table needs p, m and v")
+        elif ("m_scale" in lists) != ("v_scale" in lists):
+            raise ValueError("8-bit moments need both m_scale and v_scale")
+        else:
+            self.state = ZS_STATE_8BIT if "m_scale" in lists else ZS_STATE_F32
+        moment = torch.float32 if self.state == ZS_STATE_F32 else torch.uint8
+        code = _dtype_code(grads[0]) if grads else ZS_F32
+        for i, g in enumerate(grads):
+            _dev(g, f"grads[{i}]")
+            if _dtype_code(g) != code:
+                raise TypeError("gradients must share one dtype")
+            for k, x in lists.items():
+                if k == "w_out":
+                    _dev(x[i], f"w[{i}]")
+                    if _dtype_code(x[i]) != ZS_BF16 or x[i].numel() != numels[i]:
+                        raise ValueError(f"w[{i}] must be bf16 bits with {numels[i]} elements")
+                elif k in ("m_scale", "v_scale"):
+                    _typed(x[i], f"{k}[{i}]", torch.uint8, -(-numels[i] // 256))
+                else:
+                    _typed(x[i], f"{k}[{i}]", torch.float32 if k == "p" else moment, numels[i])
+        every = grads + [t for x in lists.values() for t in x]
+        _same_device(every, "MultiTable")
+        self.tensors = every
+        # rows are zs_multi_tensor: 7 pointers and numel, 8 bytes each
+        rows = np.zeros((max(1, T), 8), dtype=np.int64)
+        for j, k in enumerate(("p", "m", "v", "m_scale", "v_scale", "w_out", "g")):
+            x = grads if k == "g" else lists.get(k)
+            if x and T:
+                rows[:T, j] = np.array([t.data_ptr() for t in x], dtype=np.uint64).view(np.int64)
+        rows[:T, 7] = numels
+        multi = ctypes.c_void_p()
+        lib = load()
+        _check(lib.zs_multi_create(rows.ctypes.data_as(ctypes.POINTER(zs_multi_tensor)), T,
+                                   self.state, code, ctypes.byref(multi)))
+        self._multi = multi
+        host, nbytes = ctypes.c_void_p(), ctypes.c_int64()
+        _check(lib.zs_multi_image(multi, ctypes.byref(host), ctypes.byref(nbytes)))
+        device = every[0].device if every else device
+        self.image = None
+        if nbytes.value:
+            view = (ctypes.c_uint8 * nbytes.value).from_address(host.value)
+            # a synchronous copy: the image is whole for every stream when this returns
+            self.image = torch.from_numpy(np.frombuffer(view, dtype=np.uint8).copy()).to(device)
+        self._ref = every[0] if every else None
+
+    def __del__(self):
+        if getattr(self, "_multi", None) is not None and _lib is not None:
+            _lib.zs_multi_destroy(self._multi)
+            self._multi = None
+
+    def _args(self, stream, ref):
+        """(handle, device image, stream); the image stays allocated until the
+        work on `stream` is done."""
+        torch = _torch()
+        if self.image is None:
+            return self._multi, None, _stream(ref, stream)
+        if isinstance(stream, torch.cuda.Stream):
+            self.image.record_stream(stream)
+        return self._multi, self.image.data_ptr(), _stream(self.image, stream)
+
+
+def _norm_coef(t):
+    return _typed(t, "norm_coef", _torch().float32, 2)
+
+
+def zs_adamw_multi(table: MultiTable, hp, grad_scale=None, seed: int = None,
+                   stream=None) -> None:
+    """One AdamW step of every tensor of the table. grad_scale: a float32
+    device tensor of one element that multiplies every gradient (the clip
+    factor norm_coef[1:] of zs_grad_norm), read when the kernel runs. seed:
+    8-bit moments are rounded stochastically with random numbers of this seed
+    (a new one each step) instead of to nearest."""
+    h = _hp(hp)
+    scale = None
+    if grad_scale is not None:
+        _typed(grad_scale, "grad_scale", _torch().float32, 1)
+        if table.image is not None and grad_scale.device != table.image.device:
+            raise ValueError("grad_scale must be on the table's device")
+        scale = grad_scale.data_ptr()
+    opts = None
+    if seed is not None:
+        opts = ctypes.byref(zs_round_opts(1, 0, int(seed) & (2**64 - 1)))
+    if table._ref is None:
+        _check(load().zs_adamw_multi(table._multi, None, ctypes.byref(h), scale, opts, None))
+        return
+    with _on(table._ref):
+        multi, image, s = table._args(stream, table._ref)
+        _check(load().zs_adamw_multi(multi, image, ctypes.byref(h), scale, opts, s))
+
+
+def zs_grad_norm(table: MultiTable, max_norm: float, sumsq, norm_coef, workspace,
+                 stream=None) -> None:
+    """sumsq (float64, 1 element) = sum of the squares of every gradient;
+    norm_coef (float32, 2) = its root and the factor that clips it to max_norm.
+    workspace: uint8 device tensor of ZS_NORM_WORKSPACE bytes."""
+    torch = _torch()
+    _typed(sumsq, "sumsq", torch.float64, 1)
+    _norm_coef(norm_coef)
+    _typed(workspace, "workspace", torch.uint8)
+    if workspace.numel() < ZS_NORM_WORKSPACE:
+        raise ValueError(f"workspace must hold {ZS_NORM_WORKSPACE} bytes")
+    _same_device([sumsq, norm_coef, workspace] + ([table._ref] if table._ref is not None else []),
+                 "zs_grad_norm")
+    with _on(sumsq):
+        multi, image, s = table._args(stream, sumsq)
+        _check(load().zs_grad_norm(multi, image, float(max_norm), sumsq.data_ptr(),
+                                   norm_coef.data_ptr(), workspace.data_ptr(), s))
+
+
+def zs_clip_coef(sumsq: Sequence, max_norm: float, norm_coef, stream=None) -> None:
+    """norm_coef of zs_grad_norm for the sum over D ranks' sumsq (D tensors of
+    one float64 each), added in rank order."""
+    torch = _torch()
+    sumsq = list(sumsq)
+    for r, t in enumerate(sumsq):
+        _typed(t, f"sumsq[{r}]", torch.float64, 1)
+    _norm_coef(norm_coef)
+    _same_device(sumsq + [norm_coef], "zs_clip_coef")
+    with _on(norm_coef):
+        _check(load().zs_clip_coef(_ptr_array(sumsq), len(sumsq), float(max_norm),
+                                   norm_coef.data_ptr(), _stream(norm_coef, stream)))
+
+
+# ------------------------------------------------------------- 8-bit moments
+def zs_state8_layout(numels: Sequence[int]) -> List[int]:
+    """offsets[T + 1] of T tensors' 8-bit moments in one buffer of codes; their
+    scale bytes start at offsets[t] // 256 of a buffer of offsets[T] // 256."""
+    T = len(numels)
+    arr = (ctypes.c_int64 * max(1, T))(*[int(n) for n in numels])
+    off = (ctypes.c_int64 * (T + 1))()
+    _check(load().zs_state8_layout(arr, T, off))
+    return list(off)
+
+
+def _state8(codes, scales, S):
+    torch = _torch()
+    _typed(codes, "codes", torch.uint8, S)
+    _typed(scales, "scales", torch.uint8, -(-S // 256))
+
+
+def zs_state8_encode(x, kind: int, codes, scales, stream=None) -> None:
+    """codes (uint8, S) and scales (uint8, ceil(S / 256)) of the moments x
+    (float32, S), rounded to nearest; kind ZS_STATE8_M or ZS_STATE8_V."""
+    S = x.numel()
+    _typed(x, "x", _torch().float32)
+    _state8(codes, scales, S)
+    _same_device([x, codes, scales], "zs_state8_encode")
+    with _on(x):
+        _check(load().zs_state8_encode(x.data_ptr(), S, int(kind), codes.data_ptr(),
+                                       scales.data_ptr(), _stream(x, stream)))
+
+
+def zs_state8_decode(codes, scales, kind: int, out, stream=None) -> None:
+    """out (float32 or bf16, S) = the values of S 8-bit moments."""
+    S = codes.numel()
+    _state8(codes, scales, S)
+    _dev(out, "out")
+    code = _dtype_code(out)
+    if out.numel() != S:
+        raise ValueError(f"out must hold {S} elements")
+    _same_device([out, codes, scales], "zs_state8_decode")
+    with _on(out):
+        _check(load().zs_state8_decode(codes.data_ptr(), scales.data_ptr(), S, int(kind), code,
+                                       out.data_ptr(), _stream(out, stream)))
+
+
+# ------------------------------------------------------------- 4-bit shards
+def _mx4(codes, scales, S, what=""):
+    torch = _torch()
+    _typed(codes, f"codes{what}", torch.uint8, -(-S // 2))
+    _typed(scales, f"scales{what}", torch.uint8, -(-S // 32))
+
+
+def zs_quantize_mx4(src, codes, scales, stream=None) -> None:
+    """codes (uint8, ceil(S / 2)) and scales (uint8, ceil(S / 32)) of a bf16 or
+    fp32 shard of S elements in microscaled 4-bit floating point."""
+    S = src.numel()
+    _dev(src, "src")
+    code = _dtype_code(src)
+    _mx4(codes, scales, S)
+    _same_device([src, codes, scales], "zs_quantize_mx4")
+    with _on(src):
+        _check(load().zs_quantize_mx4(src.data_ptr(), code, S, codes.data_ptr(),
+                                      scales.data_ptr(), _stream(src, stream)))
+
+
+def zs_gather_unit_mx4(codes: Sequence, scales: Sequence, flat_out, stream=None) -> None:
+    """flat_out[r*S + i] (bf16 or fp32) = value of element i of 4-bit shard r."""
+    codes, scales = list(codes), list(scales)
+    D = len(codes)
+    _dev(flat_out, "flat_out")
+    code = _dtype_code(flat_out)
+    if D < 1 or len(scales) != D or flat_out.numel() % D:
+        raise ValueError("need D codes, D scales and a flat_out of D * S elements")
+    S = flat_out.numel() // D
+    for r in range(D):
+        _mx4(codes[r], scales[r], S, f"[{r}]")
+    _same_device(codes + scales + [flat_out], "zs_gather_unit_mx4")
+    with _on(flat_out):
+        _check(load().zs_gather_unit_mx4(_ptr_array(codes), _ptr_array(scales), D, S, code,
+                                         flat_out.data_ptr(), _stream(flat_out, stream)))
 
 
 ZS_PROBE_READ, ZS_PROBE_WRITE, ZS_PROBE_COPY, ZS_PROBE_TRIAD = 0, 1, 2, 3

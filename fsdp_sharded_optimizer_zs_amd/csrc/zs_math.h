@@ -1,0 +1,40 @@
+// Device arithmetic of the kernels over many tensors: bf16 conversions and one AdamW
+// element, in the operation order of the single-shard step. Files that include it are
+// compiled with -ffp-contract=off (and say so here as well).
+#pragma once
+
+#include "zs_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace zs {
+namespace {
+
+// bf16 bits -> fp32: exact, the 16 bits become the high half of the word.
+__device__ __forceinline__ float bf16_lo(uint32_t word) { return __uint_as_float(word << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t word) { return __uint_as_float(word & 0xffff0000u); }
+
+// fp32 -> bf16 bits, IEEE round to nearest, ties to even. Adding 0x7fff plus
+// the kept low bit carries into the kept half exactly when the dropped half
+// is above one half, or equal to it with an odd kept half. NaNs keep sign
+// and high payload and are made quiet.
+__device__ __forceinline__ uint32_t f32_to_bf16(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const uint32_t rounded = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    return ((u & 0x7fffffffu) > 0x7f800000u) ? ((u >> 16) | 0x40u) : rounded;
+}
+
+// One AdamW element, in the fixed order, every operation rounded on its own.
+__device__ __forceinline__ void adamw1(float& p, float& m, float& v, float g,
+                                       const AdamConsts& k) {
+    const float p1 = p * k.dec;
+    const float m1 = (k.b1 * m) + (k.b1c * g);
+    const float v1 = (k.b2 * v) + (k.b2c * (g * g));
+    const float den = (__builtin_sqrtf(v1) / k.bc2s) + k.eps;
+    p = p1 - (k.ss * (m1 / den));
+    m = m1;
+    v = v1;
+}
+
+}  // namespace
+}  // namespace zs

@@ -1,0 +1,374 @@
+// Entry points over many tensors (zs_multi_*, zs_adamw_multi, zs_grad_norm), of the
+// 8-bit moments and of the 4-bit shards: host-side checks, then one launch (the norm:
+// two). Nothing here allocates device memory or synchronizes.
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "zs_multi.h"
+
+#define ZS_EXPORT extern "C" __attribute__((visibility("default")))
+
+using namespace zs;
+
+// A checked table: the descriptors, then the chunks, in one block of bytes.
+struct zs_multi {
+    uint64_t magic;
+    int32_t state;
+    int32_t dtype;
+    int64_t T;
+    int64_t n_chunks;
+    std::vector<uint8_t> image;
+};
+
+namespace {
+
+constexpr uint64_t kMagic = 0x7a736d756c746931ull;
+constexpr int kBlock8 = 256;  // elements to a scale byte of the 8-bit moments
+constexpr int kBlock4 = 32;   // elements to a scale byte of the 4-bit format
+
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0 ? 1 : 0); }
+
+struct Owned {  // a range that the step writes, and whose it is
+    Range r;
+    int32_t tensor;
+    const char* name;
+};
+
+zs_status check_multi(const char* who, const zs_multi* multi, const void* image) {
+    if (multi == nullptr || multi->magic != kMagic)
+        return fail(ZS_EINVAL, "%s: multi is NULL or not a live zs_multi", who);
+    if (multi->n_chunks > 0 && (image == nullptr || !aligned(image, 16)))
+        return fail(ZS_EINVAL, "%s: image is NULL or not 16-byte aligned", who);
+    return ZS_OK;
+}
+
+MultiImage image_of(const zs_multi& m, const void* image) {
+    MultiImage im;
+    im.table = static_cast<const zs_multi_tensor*>(image);
+    im.chunks = reinterpret_cast<const MultiChunk*>(static_cast<const uint8_t*>(image) +
+                                                    size_t(m.T) * sizeof(zs_multi_tensor));
+    im.n_chunks = m.n_chunks;
+    return im;
+}
+
+zs_status check_max_norm(const char* who, double max_norm) {
+    if (!(max_norm > 0.0)) return fail(ZS_EINVAL, "%s: max_norm must be > 0", who);
+    return ZS_OK;
+}
+
+zs_status check_tensors(const zs_multi_tensor* ts, int32_t T, int32_t state, int es) {
+    const char* who = "zs_multi_create";
+    for (int32_t t = 0; t < T; ++t) {
+        const zs_multi_tensor& x = ts[t];
+        if (!size_ok(x.numel, 4))
+            return fail(ZS_EINVAL, "%s: tensor %d has numel %lld", who, t, (long long)x.numel);
+        if (ceil_div(x.numel, ZS_MULTI_CHUNK) > INT32_MAX)
+            return fail(ZS_EUNSUPPORTED, "%s: tensor %d has too many chunks", who, t);
+        if (x.numel == 0) continue;
+        if (x.g == nullptr) return fail(ZS_EINVAL, "%s: tensor %d: g is NULL", who, t);
+        if (!aligned(x.g, uintptr_t(es)))
+            return fail(ZS_EINVAL, "%s: tensor %d: g not aligned to %d bytes", who, t, es);
+        if (state == ZS_STATE_NONE) continue;
+        if (!x.p || !x.m || !x.v)
+            return fail(ZS_EINVAL, "%s: tensor %d: p, m or v is NULL", who, t);
+        const bool f32 = state == ZS_STATE_F32;
+        if (!aligned(x.p, 4) || (f32 && (!aligned(x.m, 4) || !aligned(x.v, 4))) ||
+            !aligned(x.w_out, 2))
+            return fail(ZS_EINVAL, "%s: tensor %d: p, m, v or w_out misaligned", who, t);
+        if (f32 && (x.m_scale || x.v_scale))
+            return fail(ZS_EINVAL, "%s: tensor %d: scales are for 8-bit moments only", who, t);
+        if (!f32 && (!x.m_scale || !x.v_scale))
+            return fail(ZS_EINVAL, "%s: tensor %d: m_scale or v_scale is NULL", who, t);
+    }
+    return ZS_OK;
+}
+
+// No written range may meet another one or a gradient. Sorted, two written ranges meet
+// only if two neighbours do, and a gradient can only meet the last one that starts
+// before its end.
+zs_status check_alias(const zs_multi_tensor* ts, int32_t T, int32_t state, int es) {
+    const char* who = "zs_multi_create";
+    if (state == ZS_STATE_NONE) return ZS_OK;
+    std::vector<Owned> own;
+    own.reserve(size_t(T) * 6);
+    for (int32_t t = 0; t < T; ++t) {
+        const zs_multi_tensor& x = ts[t];
+        if (x.numel == 0) continue;
+        const int ms = state == ZS_STATE_F32 ? 4 : 1;
+        own.push_back({range_of(x.p, x.numel, 4), t, "p"});
+        own.push_back({range_of(x.m, x.numel, ms), t, "m"});
+        own.push_back({range_of(x.v, x.numel, ms), t, "v"});
+        if (x.w_out) own.push_back({range_of(x.w_out, x.numel, 2), t, "w_out"});
+        if (state == ZS_STATE_8BIT) {
+            own.push_back({range_of(x.m_scale, ceil_div(x.numel, kBlock8), 1), t, "m_scale"});
+            own.push_back({range_of(x.v_scale, ceil_div(x.numel, kBlock8), 1), t, "v_scale"});
+        }
+    }
+    std::sort(own.begin(), own.end(),
+              [](const Owned& a, const Owned& b) { return a.r.lo < b.r.lo; });
+    for (size_t i = 1; i < own.size(); ++i)
+        if (own[i - 1].r.hi > own[i].r.lo)
+            return fail(ZS_EALIAS, "%s: %s of tensor %d overlaps %s of tensor %d", who, own[i].name,
+                        own[i].tensor, own[i - 1].name, own[i - 1].tensor);
+    for (int32_t t = 0; t < T; ++t) {
+        if (ts[t].numel == 0) continue;
+        const Range g = range_of(ts[t].g, ts[t].numel, es);
+        auto it = std::lower_bound(own.begin(), own.end(), g.hi,
+                                   [](const Owned& o, uintptr_t hi) { return o.r.lo < hi; });
+        if (it != own.begin() && (it - 1)->r.hi > g.lo)
+            return fail(ZS_EALIAS, "%s: g of tensor %d overlaps %s of tensor %d", who, t,
+                        (it - 1)->name, (it - 1)->tensor);
+    }
+    return ZS_OK;
+}
+
+// The checks that the moment conversions share; n_scales scale bytes.
+zs_status check_state8(const char* who, int64_t S, int32_t kind) {
+    if (kind != ZS_STATE8_M && kind != ZS_STATE8_V)
+        return fail(ZS_EUNSUPPORTED, "%s: unknown kind %d", who, kind);
+    if (!size_ok(S, 4)) return fail(ZS_EINVAL, "%s: S = %lld out of range", who, (long long)S);
+    return ZS_OK;
+}
+
+}  // namespace
+
+ZS_EXPORT zs_status zs_multi_create(const zs_multi_tensor* tensors, int32_t T, int32_t state,
+                                    int32_t dtype, zs_multi** out) {
+    const char* who = "zs_multi_create";
+    if (out == nullptr) return fail(ZS_EINVAL, "%s: out is NULL", who);
+    *out = nullptr;
+    const int es = elem_size(dtype);
+    if (es == 0) return fail(ZS_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
+    if (state != ZS_STATE_NONE && state != ZS_STATE_F32 && state != ZS_STATE_8BIT)
+        return fail(ZS_EUNSUPPORTED, "%s: unknown state %d", who, state);
+    if (T < 0) return fail(ZS_EINVAL, "%s: T = %d < 0", who, T);
+    if (T > 0 && tensors == nullptr) return fail(ZS_EINVAL, "%s: tensors is NULL", who);
+    try {
+        zs_status st = check_tensors(tensors, T, state, es);
+        if (st == ZS_OK) st = check_alias(tensors, T, state, es);
+        if (st != ZS_OK) return st;
+        int64_t n = 0;
+        for (int32_t t = 0; t < T; ++t) n += ceil_div(tensors[t].numel, ZS_MULTI_CHUNK);
+        zs_multi* m = new zs_multi{kMagic, state, dtype, T, n, {}};
+        try {
+            if (n > 0) {
+                const size_t head = size_t(T) * sizeof(zs_multi_tensor);
+                m->image.resize(head + size_t(n) * sizeof(MultiChunk));
+                std::memcpy(m->image.data(), tensors, head);
+                MultiChunk* c = reinterpret_cast<MultiChunk*>(m->image.data() + head);
+                for (int32_t t = 0; t < T; ++t) {
+                    const int64_t k = ceil_div(tensors[t].numel, ZS_MULTI_CHUNK);
+                    for (int64_t j = 0; j < k; ++j) *c++ = MultiChunk{t, int32_t(j)};
+                }
+            }
+        } catch (...) {
+            delete m;
+            throw;
+        }
+        *out = m;
+    } catch (const std::exception&) {
+        return fail(ZS_EINVAL, "%s: out of host memory", who);
+    }
+    return ok();
+}
+
+ZS_EXPORT zs_status zs_multi_image(const zs_multi* multi, const void** image, int64_t* bytes) {
+    if (multi == nullptr || multi->magic != kMagic)
+        return fail(ZS_EINVAL, "zs_multi_image: multi is NULL or not a live zs_multi");
+    if (!image || !bytes) return fail(ZS_EINVAL, "zs_multi_image: an output pointer is NULL");
+    *image = multi->image.data();
+    *bytes = int64_t(multi->image.size());
+    return ok();
+}
+
+ZS_EXPORT zs_status zs_multi_destroy(zs_multi* multi) {
+    if (multi == nullptr) return ok();
+    if (multi->magic != kMagic)
+        return fail(ZS_EINVAL, "zs_multi_destroy: not a live zs_multi");
+    multi->magic = 0;
+    delete multi;
+    return ok();
+}
+
+ZS_EXPORT zs_status zs_adamw_multi(const zs_multi* multi, const void* image, const zs_adamw_hp* hp,
+                                   const float* grad_scale, const zs_round_opts* round,
+                                   hipStream_t stream) {
+    const char* who = "zs_adamw_multi";
+    zs_status st = check_multi(who, multi, image);
+    if (st != ZS_OK) return st;
+    if (multi->state == ZS_STATE_NONE)
+        return fail(ZS_EINVAL, "%s: the table holds gradients only", who);
+    st = check_hp(hp, who);
+    if (st != ZS_OK) return st;
+    if (!aligned(grad_scale, 4)) return fail(ZS_EINVAL, "%s: grad_scale not 4-byte aligned", who);
+    MultiArgs a;
+    bool stoch = false;
+    a.seed_lo = a.seed_hi = 0;
+    if (round != nullptr) {
+        if (round->stochastic != 0 && round->stochastic != 1)
+            return fail(ZS_EINVAL, "%s: stochastic must be 0 or 1", who);
+        if (round->reserved != 0) return fail(ZS_EINVAL, "%s: reserved must be 0", who);
+        stoch = round->stochastic == 1;
+        a.seed_lo = uint32_t(round->seed);
+        a.seed_hi = uint32_t(round->seed >> 32);
+    }
+    if (multi->n_chunks == 0) return ok();
+    a.k = adam_consts(*hp, 1);
+    a.grad_scale = grad_scale;
+    return hip_status(
+        launch_multi(image_of(*multi, image), multi->state, multi->dtype, a, stoch, stream), who);
+}
+
+ZS_EXPORT zs_status zs_state8_layout(const int64_t* numels, int32_t T, int64_t* offsets_out) {
+    const char* who = "zs_state8_layout";
+    if (T < 0) return fail(ZS_EINVAL, "%s: T = %d < 0", who, T);
+    if (T > 0 && numels == nullptr) return fail(ZS_EINVAL, "%s: numels is NULL", who);
+    if (offsets_out == nullptr) return fail(ZS_EINVAL, "%s: offsets_out is NULL", who);
+    int64_t at = 0;
+    offsets_out[0] = 0;
+    for (int32_t t = 0; t < T; ++t) {
+        if (numels[t] < 0)
+            return fail(ZS_EINVAL, "%s: numels[%d] = %lld < 0", who, t, (long long)numels[t]);
+        if (numels[t] > INT64_MAX / 16 - at - 1024)
+            return fail(ZS_EUNSUPPORTED, "%s: the buffer's size overflows", who);
+        at += ceil_div(numels[t], 1024) * 1024;
+        offsets_out[t + 1] = at;
+    }
+    return ok();
+}
+
+ZS_EXPORT zs_status zs_state8_encode(const float* x, int64_t S, int32_t kind, uint8_t* codes,
+                                     uint8_t* scales, hipStream_t stream) {
+    const char* who = "zs_state8_encode";
+    zs_status st = check_state8(who, S, kind);
+    if (st != ZS_OK) return st;
+    if (S == 0) return ok();
+    if (!x || !codes || !scales)
+        return fail(ZS_EINVAL, "%s: x, codes or scales is NULL", who);
+    if (!aligned(x, 4)) return fail(ZS_EINVAL, "%s: x not 4-byte aligned", who);
+    const Range rx = range_of(x, S, 4), rc = range_of(codes, S, 1),
+                rs = range_of(scales, ceil_div(S, kBlock8), 1);
+    if (overlap(rx, rc) || overlap(rx, rs) || overlap(rc, rs))
+        return fail(ZS_EALIAS, "%s: x, codes and scales overlap", who);
+    return hip_status(launch_encode8(x, S, kind == ZS_STATE8_M, codes, scales, stream), who);
+}
+
+ZS_EXPORT zs_status zs_state8_decode(const uint8_t* codes, const uint8_t* scales, int64_t S,
+                                     int32_t kind, int32_t dtype, void* out, hipStream_t stream) {
+    const char* who = "zs_state8_decode";
+    const int es = elem_size(dtype);
+    if (es == 0) return fail(ZS_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
+    zs_status st = check_state8(who, S, kind);
+    if (st != ZS_OK) return st;
+    if (S == 0) return ok();
+    if (!out || !codes || !scales)
+        return fail(ZS_EINVAL, "%s: codes, scales or out is NULL", who);
+    if (!aligned(out, uintptr_t(es)))
+        return fail(ZS_EINVAL, "%s: out not aligned to %d bytes", who, es);
+    const Range ro = range_of(out, S, es);
+    if (overlap(ro, range_of(codes, S, 1)) || overlap(ro, range_of(scales, ceil_div(S, kBlock8), 1)))
+        return fail(ZS_EALIAS, "%s: out overlaps codes or scales", who);
+    return hip_status(launch_decode8(codes, scales, S, kind == ZS_STATE8_M, dtype, out, stream),
+                      who);
+}
+
+ZS_EXPORT zs_status zs_grad_norm(const zs_multi* multi, const void* image, double max_norm,
+                                 double* sumsq, float* norm_coef, void* workspace,
+                                 hipStream_t stream) {
+    const char* who = "zs_grad_norm";
+    static_assert(kNormGrid * sizeof(double) <= ZS_NORM_WORKSPACE, "the workspace holds a grid");
+    zs_status st = check_multi(who, multi, image);
+    if (st != ZS_OK) return st;
+    st = check_max_norm(who, max_norm);
+    if (st != ZS_OK) return st;
+    if (!sumsq || !norm_coef || !workspace)
+        return fail(ZS_EINVAL, "%s: sumsq, norm_coef or workspace is NULL", who);
+    if (!aligned(sumsq, 8) || !aligned(norm_coef, 4) || !aligned(workspace, 16))
+        return fail(ZS_EINVAL, "%s: sumsq, norm_coef or workspace misaligned", who);
+    const Range out[3] = {range_of(sumsq, 1, 8), range_of(norm_coef, 2, 4),
+                          range_of(workspace, ZS_NORM_WORKSPACE, 1)};
+    for (int a = 0; a < 3; ++a)
+        for (int b = a + 1; b < 3; ++b)
+            if (overlap(out[a], out[b]))
+                return fail(ZS_EALIAS, "%s: sumsq, norm_coef and workspace overlap", who);
+    if (multi->n_chunks > 0) {
+        const zs_multi_tensor* ts =
+            reinterpret_cast<const zs_multi_tensor*>(multi->image.data());
+        const int es = elem_size(multi->dtype);
+        for (int64_t t = 0; t < multi->T; ++t) {
+            const Range g = range_of(ts[t].g, ts[t].numel, es);
+            for (int a = 0; a < 3; ++a)
+                if (overlap(g, out[a]))
+                    return fail(ZS_EALIAS, "%s: an output or the workspace overlaps gradient %lld",
+                                who, (long long)t);
+        }
+    }
+    return hip_status(launch_norm(image_of(*multi, image), multi->dtype, max_norm, sumsq, norm_coef,
+                                  static_cast<double*>(workspace), stream),
+                      who);
+}
+
+ZS_EXPORT zs_status zs_clip_coef(const double* const* sumsq, int32_t D, double max_norm,
+                                 float* norm_coef, hipStream_t stream) {
+    const char* who = "zs_clip_coef";
+    if (D < 1 || D > ZS_MAX_D) return fail(ZS_EINVAL, "%s: D = %d outside 1..%d", who, D, ZS_MAX_D);
+    zs_status st = check_max_norm(who, max_norm);
+    if (st != ZS_OK) return st;
+    if (norm_coef == nullptr || !aligned(norm_coef, 4))
+        return fail(ZS_EINVAL, "%s: norm_coef is NULL or misaligned", who);
+    PtrPack sp;
+    st = take_ptrs(reinterpret_cast<const void* const*>(sumsq), D, 8, "zs_clip_coef: sumsq", &sp);
+    if (st != ZS_OK) return st;
+    for (int r = 0; r < D; ++r)
+        if (overlap(range_of(norm_coef, 2, 4), range_of(sp.p[r], 1, 8)))
+            return fail(ZS_EALIAS, "%s: norm_coef overlaps sumsq[%d]", who, r);
+    return hip_status(launch_clip(sp, D, max_norm, norm_coef, stream), who);
+}
+
+ZS_EXPORT zs_status zs_quantize_mx4(const void* src, int32_t dtype, int64_t S, uint8_t* codes,
+                                    uint8_t* scales, hipStream_t stream) {
+    const char* who = "zs_quantize_mx4";
+    const int es = elem_size(dtype);
+    if (es == 0) return fail(ZS_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
+    if (!size_ok(S, 4)) return fail(ZS_EINVAL, "%s: S = %lld out of range", who, (long long)S);
+    if (S == 0) return ok();
+    if (!src || !codes || !scales) return fail(ZS_EINVAL, "%s: src, codes or scales is NULL", who);
+    if (!aligned(src, uintptr_t(es)))
+        return fail(ZS_EINVAL, "%s: src not aligned to %d bytes", who, es);
+    const Range rx = range_of(src, S, es), rc = range_of(codes, ceil_div(S, 2), 1),
+                rs = range_of(scales, ceil_div(S, kBlock4), 1);
+    if (overlap(rx, rc) || overlap(rx, rs) || overlap(rc, rs))
+        return fail(ZS_EALIAS, "%s: src, codes and scales overlap", who);
+    return hip_status(launch_quantize_mx4(src, dtype, S, codes, scales, stream), who);
+}
+
+ZS_EXPORT zs_status zs_gather_unit_mx4(const uint8_t* const* codes, const uint8_t* const* scales,
+                                       int32_t D, int64_t S, int32_t dtype, void* flat_out,
+                                       hipStream_t stream) {
+    const char* who = "zs_gather_unit_mx4";
+    const int es = elem_size(dtype);
+    if (es == 0) return fail(ZS_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
+    if (D < 1 || D > ZS_MAX_D) return fail(ZS_EINVAL, "%s: D = %d outside 1..%d", who, D, ZS_MAX_D);
+    if (!size_ok(S, es) || S > INT64_MAX / 16 / es / D)
+        return fail(ZS_EINVAL, "%s: S = %lld out of range", who, (long long)S);
+    if (S == 0) return ok();
+    if (flat_out == nullptr || !aligned(flat_out, uintptr_t(es)))
+        return fail(ZS_EINVAL, "%s: flat_out is NULL or not aligned to %d bytes", who, es);
+    PtrPack cp, sp;
+    zs_status st = take_ptrs(reinterpret_cast<const void* const*>(codes), D, 1,
+                             "zs_gather_unit_mx4: codes", &cp);
+    if (st != ZS_OK) return st;
+    st = take_ptrs(reinterpret_cast<const void* const*>(scales), D, 1,
+                   "zs_gather_unit_mx4: scales", &sp);
+    if (st != ZS_OK) return st;
+    const Range out = range_of(flat_out, S * D, es);
+    for (int r = 0; r < D; ++r)
+        if (overlap(out, range_of(cp.p[r], ceil_div(S, 2), 1)) ||
+            overlap(out, range_of(sp.p[r], ceil_div(S, kBlock4), 1)))
+            return fail(ZS_EALIAS, "%s: flat_out overlaps codes or scales of shard %d", who, r);
+    return hip_status(launch_gather_mx4(cp, sp, D, S, dtype, flat_out, stream), who);
+}

@@ -1,0 +1,41 @@
+// Internal interface between the entry points of zs_multi.cpp and the kernels of
+// zs_multi.hip and zs_mx4.hip.
+#pragma once
+
+#include "zs_internal.h"
+#include "zs_multi_grid.h"
+
+namespace zs {
+
+// Many tensors at once (zs_multi.cpp, zs_multi.hip): the device image of a table
+// is the T descriptors followed by the chunks.
+struct MultiChunk {
+    int32_t tensor;  // index into the table
+    int32_t index;   // chunk of that tensor: elements [index, index + 1) * ZS_MULTI_CHUNK
+};
+struct MultiImage {
+    const zs_multi_tensor* table;  // device
+    const MultiChunk* chunks;      // device
+    int64_t n_chunks;
+};
+struct MultiArgs {
+    AdamConsts k;
+    const float* grad_scale;  // device, or nullptr
+    uint32_t seed_lo, seed_hi;
+};
+hipError_t launch_multi(const MultiImage& im, int state, int dtype, const MultiArgs& a, bool stoch,
+                        hipStream_t stream);
+hipError_t launch_encode8(const float* x, int64_t S, bool is_signed, uint8_t* codes,
+                          uint8_t* scales, hipStream_t stream);
+hipError_t launch_decode8(const uint8_t* codes, const uint8_t* scales, int64_t S, bool is_signed,
+                          int dtype, void* out, hipStream_t stream);
+hipError_t launch_norm(const MultiImage& im, int dtype, double max_norm, double* sumsq,
+                       float* norm_coef, double* partial, hipStream_t stream);
+hipError_t launch_clip(const PtrPack& sums, int D, double max_norm, float* norm_coef,
+                       hipStream_t stream);
+hipError_t launch_quantize_mx4(const void* src, int dtype, int64_t S, uint8_t* codes,
+                               uint8_t* scales, hipStream_t stream);
+hipError_t launch_gather_mx4(const PtrPack& codes, const PtrPack& scales, int D, int64_t S,
+                             int dtype, void* flat, hipStream_t stream);
+
+}  // namespace zs

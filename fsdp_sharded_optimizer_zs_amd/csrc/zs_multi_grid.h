@@ -1,0 +1,33 @@
+// Launch geometry of the kernels over many tensors, of the 8-bit moments and of the
+// 4-bit shards; like zs_grid.h plain C++, checked on the host alone.
+#pragma once
+
+#include "zs_grid.h"
+
+namespace zs {
+
+// Conversions of 8-bit moments: one wavefront per block of 256 elements.
+inline int64_t state8_grid(int64_t S) {
+    return grid_blocks(S / 256 + (S % 256 != 0), kBlockThreads / 64);
+}
+
+// Sums of squares over a table's chunks: as many workgroups as fill the chip (8 on
+// each of 256 CUs), whose partial sums fit zs_grad_norm's workspace; 0 chunks: 0.
+constexpr int64_t kNormGrid = 2048;
+inline int64_t norm_grid(int64_t n_chunks) {
+    return n_chunks < kNormGrid ? n_chunks : kNormGrid;
+}
+
+// 4-bit quantisation: 8 elements per lane.
+inline int64_t quantize_mx4_grid(int64_t S) {
+    return grid_blocks(S / 8 + (S % 8 != 0), kBlockThreads);
+}
+
+// Gather from 4-bit shards: 8 elements per lane, a row of the grid per shard (the
+// whole grid under the cap).
+inline int64_t gather_mx4_grid(int64_t S, int D) {
+    const int64_t b = quantize_mx4_grid(S), cap = kMaxGrid / D;
+    return b < cap ? b : cap;
+}
+
+}  // namespace zs

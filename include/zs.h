@@ -22,6 +22,16 @@
  *                    per-rank shard checkpoints, resumable at any D2
  *   zs_adamw_step_host, zs_offload_step
  *                    the step's AdamW on host cores (ZeRO-Offload)
+ *   zs_multi_create, zs_adamw_multi
+ *                    AdamW over many tensors in one launch, moments in 32 or
+ *                    in 8 bits; zs_state8_layout, zs_state8_encode and
+ *                    zs_state8_decode lay out and convert the 8-bit moments
+ *   zs_grad_norm, zs_clip_coef
+ *                    the L2 norm over many gradient tensors and the factor
+ *                    that clips it, left on the device for zs_adamw_multi
+ *   zs_quantize_mx4, zs_gather_unit_mx4
+ *                    a shard in microscaled 4-bit floating point, and the
+ *                    all-gather's rebuild of a unit from such shards
  *   zs_stream_ceiling, zs_stream_ceiling_timed, zs_hbm_probe
  *                    measurement aids: the step's memory streams without its
  *                    arithmetic, and HBM's rate for one direction alone
@@ -591,6 +601,219 @@ zs_status zs_stream_ceiling_timed(float* p, float* m, float* v, uint16_t* w, int
 enum { ZS_PROBE_READ = 0, ZS_PROBE_WRITE = 1, ZS_PROBE_COPY = 2, ZS_PROBE_TRIAD = 3 };
 zs_status zs_hbm_probe(int32_t kind, void* buf, void* buf2, int64_t bytes,
                        int32_t blocks_per_cu, hipStream_t stream);
+
+/*
+ * Many tensors at once. A zs_multi is a host object that describes T tensors
+ * (their gradients, and for the step their parameters and moments): it is
+ * checked once, when it is made, and every later call reads the checked
+ * description. Its image -- the tensors' pointers and a table of the chunks of
+ * at most ZS_MULTI_CHUNK elements that workgroups take -- is copied by the
+ * caller to device memory once and read there by the kernels.
+ */
+#define ZS_MULTI_CHUNK 4096
+
+#define ZS_STATE_NONE 0  /* gradients only (zs_grad_norm)                       */
+#define ZS_STATE_F32  1  /* m and v are fp32                                    */
+#define ZS_STATE_8BIT 2  /* m and v are 8-bit codes with one scale byte per 256 */
+
+typedef struct {
+    float* p;          /* device, numel floats: fp32 master, updated in place       */
+    void* m;           /* device, first moment: numel floats, or numel code bytes   */
+    void* v;           /* device, second moment, likewise                           */
+    uint8_t* m_scale;  /* device, ceil(numel / 256) scale bytes (ZS_STATE_8BIT),
+                          else NULL                                                 */
+    uint8_t* v_scale;  /* likewise                                                  */
+    uint16_t* w_out;   /* device, numel bf16, written; NULL: no working copy        */
+    const void* g;     /* device, numel gradient elements of the table's dtype      */
+    int64_t numel;     /* >= 0                                                      */
+} zs_multi_tensor;
+
+typedef struct zs_multi zs_multi;
+
+/*
+ * zs_multi_create -- check a table of T tensors and make its zs_multi (host
+ * memory of the library; no GPU work). The tensors may be of any sizes and
+ * start at any address that their element types allow (views into a flat unit,
+ * end to end). The table itself is copied.
+ *
+ *   tensors  host array of T descriptors (may be NULL when T == 0); with
+ *            ZS_STATE_NONE only g and numel are read
+ *   state    ZS_STATE_NONE, ZS_STATE_F32 or ZS_STATE_8BIT
+ *   dtype    ZS_BF16 or ZS_F32: element type of every gradient
+ *   out      receives the object
+ * Errors: ZS_EINVAL (NULLs, misalignment, sizes), ZS_EALIAS (a written array
+ * -- p, m, v, their scales, w_out -- overlaps another written array or a
+ * gradient, of the same tensor or another: so a tensor listed twice),
+ * ZS_EUNSUPPORTED (state, dtype, more than 2^31 - 1 chunks of one tensor).
+ */
+zs_status zs_multi_create(const zs_multi_tensor* tensors, int32_t T, int32_t state,
+                          int32_t dtype, zs_multi** out);
+
+/* zs_multi_image -- the host bytes that the caller copies, unchanged, to a
+ * 16-byte aligned device buffer of its own and passes as `image` below. *bytes
+ * is 0 when no tensor has an element. The pointer lives as long as the object. */
+zs_status zs_multi_image(const zs_multi* multi, const void** image, int64_t* bytes);
+
+/* zs_multi_destroy -- free the host object (NULL is allowed). Work already
+ * enqueued does not read it; that work reads the device image. */
+zs_status zs_multi_destroy(zs_multi* multi);
+
+/* How 8-bit moments are rounded (zs_adamw_multi; ignored for ZS_STATE_F32). */
+typedef struct {
+    int32_t stochastic;  /* 0: to nearest, ties to even; 1: stochastically  */
+    int32_t reserved;    /* must be 0                                       */
+    uint64_t seed;       /* of the random numbers; a new one for each step  */
+} zs_round_opts;
+
+/*
+ * zs_adamw_multi -- AdamW over every tensor of a table, in one launch.
+ *
+ * Per element, with g = widen(gradient) * *grad_scale (one fp32 product; no
+ * product when grad_scale is NULL), the update of zs_adamw_step, operation by
+ * operation: with ZS_STATE_F32 the results are the bits that zs_adamw_step gives
+ * for each tensor and the single fp32 contribution g.
+ *
+ * With ZS_STATE_8BIT the moments are held as codes, and the update reads their
+ * values, computes in fp32 and encodes m' and v' again (p' and w use m' and v'
+ * before they are encoded). Blocks of 256 elements, counted from the tensor's
+ * first element, share a scale byte s, and a code c stands for
+ *   m:  +-float_of_bits((c & 127) << 20) * 2^(s - 15)     (sign in bit 7)
+ *   v:    float_of_bits(c << 20)         * 2^(s - 31)
+ * -- a float with 3 bits of mantissa and 4 (m) or 5 (v) of exponent, whose
+ * smallest values are subnormal. s = 255 marks a block that holds an infinity
+ * or NaN: all its values are NaN. Zeroed codes and scales stand for 0. To
+ * encode a block, with u the fp32 bits of its largest magnitude:
+ *   s = 255 if u >= 0x7f800000 (all codes 0), else
+ *       min(254, (u + 0xfffff) >> 23), for v at least 11
+ * (the largest magnitude is at most the top code's value), and per element, with
+ * b the fp32 bits of |x| * 2^(15 - s) (v: 2^(31 - s)):
+ *   c = min(127 (v: 255), (b + a) >> 20), a = 0x7ffff + ((b >> 20) & 1) to nearest;
+ * for v at least 1 when x > 0, so that a positive v never becomes 0. Stochastic
+ * rounding takes a = (r16 << 4) | 8 with 16 random bits r16: it rounds up with
+ * the probability that keeps the mean, so that slow changes of v (1 - beta2 of
+ * it a step, less than half a code) are not lost. The random bits of element i of
+ * tensor t, the low 16 of r for m and the high 16 for v, are, in 32-bit
+ * arithmetic,
+ *   mix(x): x *= 0x6a09e667; x ^= x >> 15; x *= 0xbb67ae85; x ^= x >> 16
+ *   key = mix(mix(seed_lo + 0x9e3779b9 * (t + 1)) + seed_hi),  r = mix(i ^ key).
+ *
+ *   multi       a table with ZS_STATE_F32 or ZS_STATE_8BIT
+ *   image       device, 16-byte aligned: the copy of the table's image
+ *   hp          host pointer to the hyperparameters (parameter groups with
+ *               others are tables and calls of their own)
+ *   grad_scale  device pointer to one float, or NULL; read when the kernel runs
+ *               (zs_grad_norm's clip factor, a loss scale's inverse)
+ *   round       host pointer, or NULL: to nearest
+ * Errors: ZS_EINVAL. Tables without elements enqueue nothing.
+ */
+zs_status zs_adamw_multi(const zs_multi* multi, const void* image, const zs_adamw_hp* hp,
+                         const float* grad_scale, const zs_round_opts* round, hipStream_t stream);
+
+/*
+ * zs_state8_layout -- where T tensors' 8-bit moments start in one buffer (host
+ * only): offsets_out[t] is a multiple of 1024, tensor after tensor;
+ * offsets_out[T] is the buffer's length in codes. The scale bytes of tensor t
+ * start at offsets_out[t] / 256 of a buffer of offsets_out[T] / 256 bytes, so the
+ * whole buffer can be decoded in one call. A convenience: zs_multi_create takes
+ * any other placement too.
+ * Errors: ZS_EINVAL, ZS_EUNSUPPORTED as zs_unit_layout.
+ */
+zs_status zs_state8_layout(const int64_t* numels, int32_t T, int64_t* offsets_out);
+
+#define ZS_STATE8_M 0  /* signed codes   */
+#define ZS_STATE8_V 1  /* unsigned codes */
+
+/*
+ * zs_state8_encode, zs_state8_decode -- fp32 moments to 8-bit codes, rounded to
+ * nearest (starting 8-bit moments from a 32-bit run or a checkpoint), and codes to
+ * the values they stand for (checkpoints through zs_shard_save, re-sharding).
+ * Encoding what was decoded gives the same values (but for blocks whose largest
+ * magnitude is below 2^-126).
+ *
+ *   x       device, S floats; for ZS_STATE8_V a negative one counts as NaN
+ *   kind    ZS_STATE8_M or ZS_STATE8_V
+ *   codes   device, S bytes;  scales  device, ceil(S / 256) bytes
+ *   dtype   ZS_F32 (every value exact) or ZS_BF16 (exact down to 2^-133)
+ *   out     device, S elements of dtype
+ * Errors: ZS_EINVAL, ZS_EALIAS (any two arrays overlap), ZS_EUNSUPPORTED.
+ */
+zs_status zs_state8_encode(const float* x, int64_t S, int32_t kind, uint8_t* codes,
+                           uint8_t* scales, hipStream_t stream);
+zs_status zs_state8_decode(const uint8_t* codes, const uint8_t* scales, int64_t S, int32_t kind,
+                           int32_t dtype, void* out, hipStream_t stream);
+
+#define ZS_NORM_WORKSPACE 32768  /* bytes of workspace zs_grad_norm needs */
+
+/*
+ * zs_grad_norm -- the L2 norm over the gradients of a table, and the factor that
+ * brings it down to max_norm.
+ *
+ *   sumsq[0]     = sum of g * g over every element, in fp64 (exact products;
+ *                  the order of the sum depends on the table alone)
+ *   norm_coef[0] = float(sqrt(sumsq))
+ *   norm_coef[1] = float(c) for c = max_norm / (sqrt(sumsq) + 1e-6) < 1, else 1
+ *                  (NaN if the sum is NaN; 0 if it is infinite; always 1 when
+ *                  max_norm is infinite)
+ * norm_coef + 1 is what zs_adamw_multi takes as grad_scale. When the ranks of a
+ * data-parallel group hold parts of the gradients, zs_clip_coef joins their sums.
+ *
+ *   multi, image  as zs_adamw_multi, with any state
+ *   max_norm      > 0, or infinity: never clip
+ *   sumsq         device, one double, 8-byte aligned
+ *   norm_coef     device, two floats
+ *   workspace     device, ZS_NORM_WORKSPACE bytes, 16-byte aligned, of any
+ *                 contents; calls that may run at the same time (other streams,
+ *                 graphs) need one each
+ * A table without elements gives 0, 0 and 1.
+ * Errors: ZS_EINVAL, ZS_EALIAS (outputs and workspace overlap, or one of them a
+ * gradient).
+ */
+zs_status zs_grad_norm(const zs_multi* multi, const void* image, double max_norm, double* sumsq,
+                       float* norm_coef, void* workspace, hipStream_t stream);
+
+/*
+ * zs_clip_coef -- norm_coef of zs_grad_norm for the sum, in rank order and fp64,
+ * of D ranks' sums of squares.
+ *   sumsq     host array of D device pointers, each to one double
+ *   D         1..ZS_MAX_D
+ * Errors: ZS_EINVAL, ZS_EALIAS (norm_coef overlaps a sum).
+ */
+zs_status zs_clip_coef(const double* const* sumsq, int32_t D, double max_norm, float* norm_coef,
+                       hipStream_t stream);
+
+/*
+ * Microscaled 4-bit floating point: blocks of 32 elements share a power of two
+ * 2^(s - 127) with s one byte, and each element is +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}
+ * of it in 4 bits (sign in bit 3, the values in order in bits 0-2), element 2k in
+ * the low and 2k + 1 in the high half of byte k. s = 255 marks a block of NaN.
+ * A working shard takes 4.25 bits an element on the way to the gather.
+ *
+ * zs_quantize_mx4 -- a shard to that form. s = max(0, e - 2) with e the fp32
+ * exponent byte of the block's largest magnitude (255 with all codes 0 if that is
+ * not finite); |x| * 2^(127 - s) is rounded to the nearest value, ties to the even
+ * code, and what is over 6 becomes 6. Signs are kept, of zeros too. The last block
+ * may be short, and the last half byte of an odd shard is 0.
+ *
+ *   src     device, S elements of dtype (ZS_BF16 or ZS_F32)
+ *   codes   device, ceil(S / 2) bytes;  scales  device, ceil(S / 32) bytes
+ * Errors: ZS_EINVAL, ZS_EALIAS, ZS_EUNSUPPORTED.
+ */
+zs_status zs_quantize_mx4(const void* src, int32_t dtype, int64_t S, uint8_t* codes,
+                          uint8_t* scales, hipStream_t stream);
+
+/*
+ * zs_gather_unit_mx4 -- zs_gather_unit from shards in that form:
+ *   flat_out[r*S + i] = value of element i of shard r, for r < D, i < S,
+ * rounded to dtype (to nearest even; every value that zs_quantize_mx4 writes is
+ * exact in bf16 and fp32).
+ *
+ *   codes, scales  host arrays of D device pointers
+ *   dtype          ZS_BF16 or ZS_F32;  flat_out  device, D * S elements
+ * Errors: ZS_EINVAL, ZS_EALIAS (flat_out overlaps codes or scales),
+ * ZS_EUNSUPPORTED.
+ */
+zs_status zs_gather_unit_mx4(const uint8_t* const* codes, const uint8_t* const* scales, int32_t D,
+                             int64_t S, int32_t dtype, void* flat_out, hipStream_t stream);
 
 /* Text of the calling thread's most recent failure ("" if none). The pointer
  * stays valid until the thread's next call into the library. */
