@@ -24,6 +24,15 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float x) {
     return ((u & 0x7fffffffu) > 0x7f800000u) ? ((u >> 16) | 0x40u) : rounded;
 }
 
+// Two values' bf16 bits in one word, by gfx950's conversion instruction: the same
+// rounding in half an instruction a value, NaNs quiet.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 x{lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+}
+
 // One AdamW element, in the fixed order, every operation rounded on its own.
 __device__ __forceinline__ void adamw1(float& p, float& m, float& v, float g,
                                        const AdamConsts& k) {

@@ -207,6 +207,7 @@ ZS_EXPORT zs_status zs_adamw_multi(const zs_multi* multi, const void* image, con
     if (!aligned(grad_scale, 4)) return fail(ZS_EINVAL, "%s: grad_scale not 4-byte aligned", who);
     MultiArgs a;
     bool stoch = false;
+    a.rbc2s = 0.0f;
     a.seed_lo = a.seed_hi = 0;
     if (round != nullptr) {
         if (round->stochastic != 0 && round->stochastic != 1)

@@ -20,10 +20,11 @@ struct MultiImage {
 };
 struct MultiArgs {
     AdamConsts k;
+    float rbc2s;              // 1 / k.bc2s
     const float* grad_scale;  // device, or nullptr
     uint32_t seed_lo, seed_hi;
 };
-hipError_t launch_multi(const MultiImage& im, int state, int dtype, const MultiArgs& a, bool stoch,
+hipError_t launch_multi(const MultiImage& im, int state, int dtype, MultiArgs a, bool stoch,
                         hipStream_t stream);
 hipError_t launch_encode8(const float* x, int64_t S, bool is_signed, uint8_t* codes,
                           uint8_t* scales, hipStream_t stream);

@@ -100,8 +100,7 @@ __device__ __forceinline__ void store_f32_part(float* base, int64_t i, int live,
         if (e < live) global<g_f32>(base)[i + e] = x[e];
 }
 __device__ __forceinline__ void store_bf16(uint16_t* base, int64_t i, const float (&x)[4]) {
-    const u32x2 h{f32_to_bf16(x[0]) | (f32_to_bf16(x[1]) << 16),
-                  f32_to_bf16(x[2]) | (f32_to_bf16(x[3]) << 16)};
+    const u32x2 h{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
     __builtin_nontemporal_store(h, reinterpret_cast<g_u32x2*>(global<g_u16>(base) + i));
 }
 __device__ __forceinline__ void store_bf16_part(uint16_t* base, int64_t i, int live,
@@ -238,92 +237,228 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 
 // ------------------------------------------------------------- the step
 
-// fp32 moments: one quarter, whole or the first `live` elements of each lane.
-template <int DT, bool FULL>
-__device__ __forceinline__ void step32(const zs_multi_tensor& t, int64_t i, int live,
-                                       const MultiArgs& a, float mult) {
+// fp32 moments: the first `live` elements of each lane of one quarter.
+template <int DT>
+__device__ __forceinline__ void step32_part(const zs_multi_tensor& t, int64_t i, int live,
+                                            const MultiArgs& a, float mult) {
     float p[4], m[4], v[4], g[4];
-    if constexpr (FULL) {
-        load_f32(t.p, i, p);
-        load_f32(static_cast<const float*>(t.m), i, m);
-        load_f32(static_cast<const float*>(t.v), i, v);
-        load_grad<DT>(t.g, i, g);
-    } else {
-        load_f32_part(t.p, i, live, p);
-        load_f32_part(static_cast<const float*>(t.m), i, live, m);
-        load_f32_part(static_cast<const float*>(t.v), i, live, v);
-        load_grad_part<DT>(t.g, i, live, g);
-    }
+    load_f32_part(t.p, i, live, p);
+    load_f32_part(static_cast<const float*>(t.m), i, live, m);
+    load_f32_part(static_cast<const float*>(t.v), i, live, v);
+    load_grad_part<DT>(t.g, i, live, g);
 #pragma unroll
     for (int e = 0; e < 4; ++e) adamw1(p[e], m[e], v[e], g[e] * mult, a.k);
-    if constexpr (FULL) {
-        store_f32(t.p, i, p);
-        store_f32(static_cast<float*>(t.m), i, m);
-        store_f32(static_cast<float*>(t.v), i, v);
-        if (t.w_out) store_bf16(t.w_out, i, p);
-    } else {
-        store_f32_part(t.p, i, live, p);
-        store_f32_part(static_cast<float*>(t.m), i, live, m);
-        store_f32_part(static_cast<float*>(t.v), i, live, v);
-        if (t.w_out) store_bf16_part(t.w_out, i, live, p);
+    store_f32_part(t.p, i, live, p);
+    store_f32_part(static_cast<float*>(t.m), i, live, m);
+    store_f32_part(static_cast<float*>(t.v), i, live, v);
+    if (t.w_out) store_bf16_part(t.w_out, i, live, p);
+}
+
+// fp32 moments: a wavefront's 1024 elements, every load ahead of the arithmetic.
+template <int DT>
+__device__ __forceinline__ void step32_wave(const zs_multi_tensor& t, int64_t i,
+                                            const MultiArgs& a, float mult) {
+    float p[kQ][4], m[kQ][4], v[kQ][4], g[kQ][4];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        load_f32(t.p, i + q * kQuarter, p[q]);
+        load_f32(static_cast<const float*>(t.m), i + q * kQuarter, m[q]);
+        load_f32(static_cast<const float*>(t.v), i + q * kQuarter, v[q]);
+        load_grad<DT>(t.g, i + q * kQuarter, g[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) adamw1(p[q][e], m[q][e], v[q][e], g[q][e] * mult, a.k);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) store_f32(t.p, i + q * kQuarter, p[q]);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) store_f32(static_cast<float*>(t.m), i + q * kQuarter, m[q]);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) store_f32(static_cast<float*>(t.v), i + q * kQuarter, v[q]);
+    if (t.w_out) {
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) store_bf16(t.w_out, i + q * kQuarter, p[q]);
     }
 }
 
-// 8-bit moments: the same, the quarter's scale bytes sm and sv in and out.
-template <int DT, bool STOCH, bool FULL>
-__device__ __forceinline__ void step8(const zs_multi_tensor& t, int64_t i, int live,
-                                      const MultiArgs& a, float mult, uint32_t key, int* sm,
-                                      int* sv) {
+// The parameter's part of the update with 8-bit moments. EXACT: the fp32 step's
+// operations, each correctly rounded. Otherwise the root and the two quotients are
+// the hardware's one-step approximations and a product with 1 / BC2S: 10 issue slots
+// instead of about 50, of which HBM leaves about 100 an element. Their errors (root and
+// reciprocal 1 ulp, four roundings) stay within 2^-21 of the update. It needs
+// EPS >= 2^-39: then the roots that the hardware may flush (of subnormals) are below
+// half an ulp of EPS, and the divisor and its reciprocal are normal numbers.
+template <bool EXACT>
+__device__ __forceinline__ float new_p(float p, float m1, float v1, const MultiArgs& a) {
+    if constexpr (EXACT) {
+        const float den = (__builtin_sqrtf(v1) / a.k.bc2s) + a.k.eps;
+        return (p * a.k.dec) - (a.k.ss * (m1 / den));
+    } else {
+        const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v1), a.rbc2s, a.k.eps);
+        return __builtin_fmaf(-a.k.ss, m1 * __builtin_amdgcn_rcpf(den), p * a.k.dec);
+    }
+}
+
+__device__ __forceinline__ uint32_t tensor_key(const MultiArgs& a, int32_t tensor) {
+    return mix(mix(a.seed_lo + 0x9e3779b9u * uint32_t(tensor + 1)) + a.seed_hi);
+}
+
+// 8-bit moments, any case: the first `live` elements of each lane of one quarter, its
+// scale bytes sm and sv in and out.
+template <int DT, bool STOCH, bool EXACT>
+__device__ __forceinline__ void step8_part(const zs_multi_tensor& t, int64_t i, int live,
+                                           const MultiArgs& a, float mult, uint32_t key, int* sm,
+                                           int* sv) {
     float p[4], m[4], v[4], g[4];
     uint8_t* const mc = static_cast<uint8_t*>(t.m);
     uint8_t* const vc = static_cast<uint8_t*>(t.v);
-    uint32_t wm, wv;
-    if constexpr (FULL) {
-        load_f32(t.p, i, p);
-        wm = load_codes(mc, i);
-        wv = load_codes(vc, i);
-        load_grad<DT>(t.g, i, g);
-    } else {
-        load_f32_part(t.p, i, live, p);
-        wm = load_codes_part(mc, i, live);
-        wv = load_codes_part(vc, i, live);
-        load_grad_part<DT>(t.g, i, live, g);
-    }
-    decode4<true>(wm, *sm, m);
-    decode4<false>(wv, *sv, v);
+    load_f32_part(t.p, i, live, p);
+    load_grad_part<DT>(t.g, i, live, g);
+    decode4<true>(load_codes_part(mc, i, live), *sm, m);
+    decode4<false>(load_codes_part(vc, i, live), *sv, v);
+    uint32_t rm[4] = {}, rv[4] = {};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        adamw1(p[e], m[e], v[e], g[e] * mult, a.k);
-        if (!FULL && e >= live) m[e] = v[e] = 0.0f;  // no part of the block's largest
+        const float x = g[e] * mult;
+        m[e] = (a.k.b1 * m[e]) + (a.k.b1c * x);
+        v[e] = (a.k.b2 * v[e]) + (a.k.b2c * (x * x));
+        p[e] = new_p<EXACT>(p[e], m[e], v[e], a);
+        if (e >= live) m[e] = v[e] = 0.0f;  // no part of the block's largest
+        if constexpr (STOCH) {
+            rm[e] = mix(uint32_t(i + e) ^ key);
+            rv[e] = rm[e] >> 16;
+        }
     }
     *sm = scale_of<true>(wave_max(top_bits(m)));
     *sv = scale_of<false>(wave_max(top_bits(v)));
-    uint32_t rm[4] = {}, rv[4] = {};
-    if constexpr (STOCH) {
+    store_codes_part(mc, i, live, encode4<true, STOCH>(m, *sm, rm));
+    store_codes_part(vc, i, live, encode4<false, STOCH>(v, *sv, rv));
+    store_f32_part(t.p, i, live, p);
+    if (t.w_out) store_bf16_part(t.w_out, i, live, p);
+}
+
+// Codes as encode4 gives them, for a scale byte below 254: then the largest magnitude
+// is at most the top code's value and no code needs a limit. Signs ride along in bit
+// 31 (the sum never reaches it); the codes are packed from whole bytes.
+template <bool STOCH>
+__device__ __forceinline__ uint32_t pack_m(const float (&x)[4], int s, const uint32_t (&r)[4]) {
+    uint32_t c[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t r = mix(uint32_t(i + e) ^ key);
-            rm[e] = r;
-            rv[e] = r >> 16;
-        }
+    for (int e = 0; e < 4; ++e) {
+        uint32_t u = __float_as_uint(__builtin_ldexpf(x[e], Code<true>::K - s));
+        u += STOCH ? ((r[e] << 4) & 0xffff0u) | 8u : 0x7ffffu + ((u >> 20) & 1u);
+        c[e] = ((u << 4) & 0x7fffffffu) | (u & 0x80000000u);
     }
-    wm = encode4<true, STOCH>(m, *sm, rm);
-    wv = encode4<false, STOCH>(v, *sv, rv);
-    if constexpr (FULL) {
-        store_f32(t.p, i, p);
-        if (t.w_out) store_bf16(t.w_out, i, p);
-        store_codes(mc, i, wm);
-        store_codes(vc, i, wv);
-    } else {
-        store_f32_part(t.p, i, live, p);
-        if (t.w_out) store_bf16_part(t.w_out, i, live, p);
-        store_codes_part(mc, i, live, wm);
-        store_codes_part(vc, i, live, wv);
+    return __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0703u) |
+           __builtin_amdgcn_perm(c[3], c[2], 0x07030c0cu);
+}
+template <bool STOCH>
+__device__ __forceinline__ uint32_t pack_v(const float (&x)[4], int s, const uint32_t (&r)[4]) {
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t u = __float_as_uint(__builtin_ldexpf(x[e], Code<false>::K - s));
+        u += STOCH ? ((r[e] >> 12) & 0xffff0u) | 8u : 0x7ffffu + ((u >> 20) & 1u);
+        const uint32_t b = __float_as_uint(x[e]), one = b < 1u ? b : 1u;  // 1 for x > 0
+        const uint32_t k = u >> 20;
+        c[e] = k > one ? k : one;
+    }
+    return __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u) |
+           __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);
+}
+
+// Largest old scale bytes that step8_wave takes: B1 * 2^(s - 15) and B2 * 2^(s - 31)
+// have to be finite (moments below 2^16 and 2^32; others, and NaN blocks, go by quarters).
+constexpr int kMostM = 142, kMostV = 158;
+
+// 8-bit moments: what a wavefront's 1024 elements load.
+struct Loaded8 {
+    float p[kQ][4], g[kQ][4];
+    uint32_t wm[kQ], wv[kQ];
+};
+template <int DT>
+__device__ __forceinline__ void load8_wave(const zs_multi_tensor& t, int64_t i, Loaded8& d) {
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        d.wm[q] = load_codes(static_cast<const uint8_t*>(t.m), i + q * kQuarter);
+        d.wv[q] = load_codes(static_cast<const uint8_t*>(t.v), i + q * kQuarter);
+        load_grad<DT>(t.g, i + q * kQuarter, d.g[q]);
+        load_f32(t.p, i + q * kQuarter, d.p[q]);
     }
 }
 
-template <int DT, int STATE, bool STOCH>
-__global__ __launch_bounds__(kThreads) void multi_kernel(
+// 8-bit moments: a wavefront's 1024 elements; lane q < 4 holds the scale bytes of
+// quarter q, in and out. A code's value needs no scaling of its own: B1 * m is taken as
+// (B1 * 2^(s - 15)) * float_of_bits(c << 20), the same real product, rounded once.
+template <bool STOCH>
+__device__ __forceinline__ void step8_wave(const zs_multi_tensor& t, Loaded8& d, int64_t i,
+                                           int lane, const MultiArgs& a, float mult, uint32_t key,
+                                           int* lm, int* lv) {
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        const float b1 = __builtin_ldexpf(a.k.b1, __builtin_amdgcn_readlane(*lm, q) - 15);
+        const float b2 = __builtin_ldexpf(a.k.b2, __builtin_amdgcn_readlane(*lv, q) - 31);
+        float m[4], v[4];
+        uint32_t r[4] = {};
+        const uint32_t at = uint32_t(i + q * kQuarter) ^ key;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int cm = (int(d.wm[q] << (24 - 8 * e)) >> 4) & int(0x87f00000u);
+            const uint32_t cv =
+                (e == 3 ? d.wv[q] >> 4 : d.wv[q] << (20 - 8 * e)) & 0x0ff00000u;
+            const float x = d.g[q][e] * mult;
+            m[e] = (b1 * __uint_as_float(uint32_t(cm))) + (a.k.b1c * x);
+            v[e] = (b2 * __uint_as_float(cv)) + (a.k.b2c * (x * x));
+            d.p[q][e] = new_p<false>(d.p[q][e], m[e], v[e], a);
+            if constexpr (STOCH) r[e] = mix(at ^ uint32_t(e));
+        }
+        const int sm = scale_of<true>(wave_max(top_bits(m)));
+        const int sv = scale_of<false>(wave_max(top_bits(v)));
+        uint32_t wm, wv;
+        if (sm < 254 && sv < 254) {
+            wm = pack_m<STOCH>(m, sm, r);
+            wv = pack_v<STOCH>(v, sv, r);
+        } else {
+            const uint32_t rv[4] = {r[0] >> 16, r[1] >> 16, r[2] >> 16, r[3] >> 16};
+            wm = encode4<true, STOCH>(m, sm, r);
+            wv = encode4<false, STOCH>(v, sv, rv);
+        }
+        if (lane == q) {
+            *lm = sm;
+            *lv = sv;
+        }
+        store_f32(t.p, i + q * kQuarter, d.p[q]);
+        if (t.w_out) store_bf16(t.w_out, i + q * kQuarter, d.p[q]);
+        store_codes(static_cast<uint8_t*>(t.m), i + q * kQuarter, wm);
+        store_codes(static_cast<uint8_t*>(t.v), i + q * kQuarter, wv);
+    }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void multi32_kernel(
+    const zs_multi_tensor* __restrict__ table, const MultiChunk* __restrict__ chunks,
+    int64_t n_chunks, MultiArgs a) {
+    const int lane = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const float mult = a.grad_scale ? *a.grad_scale : 1.0f;
+    for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
+        const MultiChunk ch = chunks[c];
+        const zs_multi_tensor t = table[ch.tensor];
+        const int64_t n = t.numel;
+        const int64_t base = int64_t(ch.index) * ZS_MULTI_CHUNK + wave * kWaveElems;
+        if (base + kWaveElems <= n) {
+            step32_wave<DT>(t, base + 4 * lane, a, mult);
+        } else {
+#pragma unroll 1
+            for (int64_t b = base; b < n; b += kQuarter)
+                step32_part<DT>(t, b + 4 * lane, live_of(b + 4 * lane, n), a, mult);
+        }
+    }
+}
+
+template <int DT, bool STOCH, bool EXACT>
+__global__ __launch_bounds__(kThreads) void multi8_kernel(
     const zs_multi_tensor* __restrict__ table, const MultiChunk* __restrict__ chunks,
     int64_t n_chunks, MultiArgs a) {
     const int lane = int(threadIdx.x) & 63;
@@ -335,47 +470,42 @@ __global__ __launch_bounds__(kThreads) void multi_kernel(
         const int64_t n = t.numel;
         const int64_t base = int64_t(ch.index) * ZS_MULTI_CHUNK + wave * kWaveElems;
         if (base >= n) continue;
-        if constexpr (STATE == ZS_STATE_F32) {
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) {
-                const int64_t i = base + q * kQuarter + 4 * lane;
-                if (base + (q + 1) * kQuarter <= n) {
-                    step32<DT, true>(t, i, 4, a, mult);
-                } else if (base + q * kQuarter < n) {
-                    step32<DT, false>(t, i, live_of(i, n), a, mult);
-                }
-            }
+        const uint32_t key = STOCH ? tensor_key(a, ch.tensor) : 0u;
+        // lane q < 4 holds the scale bytes of quarter q
+        g_u8* const ms = global<g_u8>(t.m_scale) + base / kQuarter + lane;
+        g_u8* const vs = global<g_u8>(t.v_scale) + base / kQuarter + lane;
+        const bool mine = lane < kQ && base + lane * kQuarter < n;
+        int lm = 0, lv = 0;
+        if (mine) {
+            lm = *ms;
+            lv = *vs;
+        }
+        const bool whole = !EXACT && base + kWaveElems <= n;
+        Loaded8 d;
+        if (whole) {
+            load8_wave<DT>(t, base + 4 * lane, d);
+            // keeps the loads here, in flight beside the scale bytes, ahead of the branch
+            // that waits for those
+            asm volatile("" ::: "memory");
+        }
+        if (whole && __all(lm <= kMostM && lv <= kMostV)) {
+            step8_wave<STOCH>(t, d, base + 4 * lane, lane, a, mult, key, &lm, &lv);
         } else {
-            const uint32_t key = STOCH ? mix(mix(a.seed_lo + 0x9e3779b9u * uint32_t(ch.tensor + 1)) +
-                                             a.seed_hi)
-                                       : 0u;
-            // lane q holds the scale bytes of quarter q
-            const int64_t block0 = base / kQuarter;
-            const bool mine = lane < kQ && base + lane * kQuarter < n;
-            int lm = 0, lv = 0;
-            if (mine) {
-                lm = global<const g_u8>(t.m_scale)[block0 + lane];
-                lv = global<const g_u8>(t.v_scale)[block0 + lane];
-            }
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) {
+#pragma unroll 1
+            for (int q = 0; q < kQ && base + q * kQuarter < n; ++q) {
                 const int64_t i = base + q * kQuarter + 4 * lane;
-                if (base + q * kQuarter >= n) break;
                 int sm = __builtin_amdgcn_readlane(lm, q);
                 int sv = __builtin_amdgcn_readlane(lv, q);
-                if (base + (q + 1) * kQuarter <= n)
-                    step8<DT, STOCH, true>(t, i, 4, a, mult, key, &sm, &sv);
-                else
-                    step8<DT, STOCH, false>(t, i, live_of(i, n), a, mult, key, &sm, &sv);
+                step8_part<DT, STOCH, EXACT>(t, i, live_of(i, n), a, mult, key, &sm, &sv);
                 if (lane == q) {
                     lm = sm;
                     lv = sv;
                 }
             }
-            if (mine) {
-                global<g_u8>(t.m_scale)[block0 + lane] = uint8_t(lm);
-                global<g_u8>(t.v_scale)[block0 + lane] = uint8_t(lv);
-            }
+        }
+        if (mine) {
+            *ms = uint8_t(lm);
+            *vs = uint8_t(lv);
         }
     }
 }
@@ -521,28 +651,38 @@ __global__ __launch_bounds__(64) void clip_kernel(PtrPack sums, int D, double ma
     write_clip(s, max_norm, norm_coef);
 }
 
-template <int DT, int STATE, bool STOCH>
-hipError_t launch_kind(const MultiImage& im, const MultiArgs& a, hipStream_t stream) {
+template <int DT, bool STOCH, bool EXACT>
+void launch8(const MultiImage& im, const MultiArgs& a, hipStream_t stream) {
     const unsigned grid = unsigned(grid_blocks(im.n_chunks, 1));
-    hipLaunchKernelGGL((multi_kernel<DT, STATE, STOCH>), dim3(grid), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL((multi8_kernel<DT, STOCH, EXACT>), dim3(grid), dim3(kThreads), 0, stream,
                        im.table, im.chunks, im.n_chunks, a);
-    return hipGetLastError();
+}
+
+template <int DT>
+void launch_dtype(const MultiImage& im, int state, const MultiArgs& a, bool stoch, bool exact,
+                  hipStream_t stream) {
+    if (state == ZS_STATE_F32) {
+        const unsigned grid = unsigned(grid_blocks(im.n_chunks, 1));
+        hipLaunchKernelGGL((multi32_kernel<DT>), dim3(grid), dim3(kThreads), 0, stream, im.table,
+                           im.chunks, im.n_chunks, a);
+    } else if (stoch) {
+        exact ? launch8<DT, true, true>(im, a, stream) : launch8<DT, true, false>(im, a, stream);
+    } else {
+        exact ? launch8<DT, false, true>(im, a, stream) : launch8<DT, false, false>(im, a, stream);
+    }
 }
 
 }  // namespace
 
-hipError_t launch_multi(const MultiImage& im, int state, int dtype, const MultiArgs& a, bool stoch,
+hipError_t launch_multi(const MultiImage& im, int state, int dtype, MultiArgs a, bool stoch,
                         hipStream_t stream) {
-    if (state == ZS_STATE_F32) {
-        return dtype == ZS_BF16 ? launch_kind<ZS_BF16, ZS_STATE_F32, false>(im, a, stream)
-                                : launch_kind<ZS_F32, ZS_STATE_F32, false>(im, a, stream);
-    }
-    if (stoch) {
-        return dtype == ZS_BF16 ? launch_kind<ZS_BF16, ZS_STATE_8BIT, true>(im, a, stream)
-                                : launch_kind<ZS_F32, ZS_STATE_8BIT, true>(im, a, stream);
-    }
-    return dtype == ZS_BF16 ? launch_kind<ZS_BF16, ZS_STATE_8BIT, false>(im, a, stream)
-                            : launch_kind<ZS_F32, ZS_STATE_8BIT, false>(im, a, stream);
+    a.rbc2s = float(1.0 / double(a.k.bc2s));
+    // when the update's approximations hold (new_p), and B1 and B2 can be scaled exactly
+    const auto scales = [](float b) { return b == 0.0f || b >= 0x1p-60f; };
+    const bool exact = !(a.k.eps >= 0x1p-39f && scales(a.k.b1) && scales(a.k.b2));
+    if (dtype == ZS_BF16) launch_dtype<ZS_BF16>(im, state, a, stoch, exact, stream);
+    else launch_dtype<ZS_F32>(im, state, a, stoch, exact, stream);
+    return hipGetLastError();
 }
 
 hipError_t launch_encode8(const float* x, int64_t S, bool is_signed, uint8_t* codes,

@@ -18,13 +18,15 @@ inline int64_t norm_grid(int64_t n_chunks) {
     return n_chunks < kNormGrid ? n_chunks : kNormGrid;
 }
 
-// 4-bit quantisation: 8 elements per lane.
+// 4-bit quantisation: one workgroup per tile of kMx4Unroll groups of 8 elements a lane.
+constexpr int kMx4Unroll = 4;
 inline int64_t quantize_mx4_grid(int64_t S) {
-    return grid_blocks(S / 8 + (S % 8 != 0), kBlockThreads);
+    const int64_t tile = int64_t(kBlockThreads) * 8 * kMx4Unroll;
+    return grid_blocks(S / tile + (S % tile != 0), 1);
 }
 
-// Gather from 4-bit shards: 8 elements per lane, a row of the grid per shard (the
-// whole grid under the cap).
+// Gather from 4-bit shards: the same tiles, a row of the grid per shard (the whole grid
+// under the cap).
 inline int64_t gather_mx4_grid(int64_t S, int D) {
     const int64_t b = quantize_mx4_grid(S), cap = kMaxGrid / D;
     return b < cap ? b : cap;

@@ -674,8 +674,13 @@ typedef struct {
  * for each tensor and the single fp32 contribution g.
  *
  * With ZS_STATE_8BIT the moments are held as codes, and the update reads their
- * values, computes in fp32 and encodes m' and v' again (p' and w use m' and v'
- * before they are encoded). Blocks of 256 elements, counted from the tensor's
+ * values, computes m' and v' as above and encodes them again (p' and w use m' and
+ * v' before they are encoded). There p' = p * DEC - SS * (m' / den) is held to a bound
+ * instead of an operation order, since roots and divisions rounded to the last bit
+ * would cost more than the memory traffic: within 2^-21 |SS * (m' / den)| +
+ * 2^-24 (|p * DEC| + |p'|) of the formula's value for these m' and v', the same in every
+ * run (with eps < 2^-39 or a beta in (0, 2^-60), p' is the fp32 step's, bit for bit).
+ * Blocks of 256 elements, counted from the tensor's
  * first element, share a scale byte s, and a code c stands for
  *   m:  +-float_of_bits((c & 127) << 20) * 2^(s - 15)     (sign in bit 7)
  *   v:    float_of_bits(c << 20)         * 2^(s - 31)
