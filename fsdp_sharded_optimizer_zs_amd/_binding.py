@@ -671,21 +671,38 @@ def zs_stream_ceiling_timed(p, m, v, w, contribs: Sequence, start, stop, stream=
 
 # ------------------------------------------------------- many tensors at once
 def _same_device(ts: Sequence, what: str):
-    if len({t.device for t in ts}) > 1:
-        raise ValueError(f"{what}: every tensor must be on one device")
-
-
-def _on(t):
-    """The tensor's device as the current one: kernels go to its streams."""
-    return _torch().cuda.device(t.device)
+    d = ts[0].device if ts else None
+    for t in ts:
+        if t.device != d:
+            raise ValueError(f"{what}: every tensor must be on one device")
 
 
 def _typed(t, what: str, dtype, numel=None):
+    if (t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and (numel is None or t.numel() == numel)):
+        return
     _dev(t, what)
-    if t.dtype != dtype or (numel is not None and t.numel() != numel):
-        size = "" if numel is None else f" with {numel} elements"
-        raise ValueError(f"{what} must be {str(dtype).replace('torch.', '')}{size}")
-    return t
+    size = "" if numel is None else f" with {numel} elements"
+    raise ValueError(f"{what} must be {str(dtype).replace('torch.', '')}{size}")
+
+
+def _enqueue(f, ref, stream, *args) -> None:
+    """Call entry point f with args and the stream, by default the current one
+    of ref's device, with that device the current one."""
+    torch = _torch()
+    cuda, dev = torch.cuda, ref.get_device()
+    if stream is None:
+        # what current_stream(dev).cuda_stream is, without making a Stream (1 us of 6)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == cuda.current_device():
+        status = f(*args, stream)
+    else:
+        with cuda.device(dev):
+            status = f(*args, stream)
+    if status != ZS_OK:
+        _check(status)
 
 
 class MultiTable:
@@ -765,19 +782,14 @@ class MultiTable:
             _lib.zs_multi_destroy(self._multi)
             self._multi = None
 
-    def _args(self, stream, ref):
-        """(handle, device image, stream); the image stays allocated until the
-        work on `stream` is done."""
-        torch = _torch()
+    def _image(self, stream):
+        """Address of the device image, which stays allocated until the work on
+        `stream` is done."""
         if self.image is None:
-            return self._multi, None, _stream(ref, stream)
-        if isinstance(stream, torch.cuda.Stream):
+            return None
+        if stream is not None and isinstance(stream, _torch().cuda.Stream):
             self.image.record_stream(stream)
-        return self._multi, self.image.data_ptr(), _stream(self.image, stream)
-
-
-def _norm_coef(t):
-    return _typed(t, "norm_coef", _torch().float32, 2)
+        return self.image.data_ptr()
 
 
 def zs_adamw_multi(table: MultiTable, hp, grad_scale=None, seed: int = None,
@@ -787,41 +799,38 @@ def zs_adamw_multi(table: MultiTable, hp, grad_scale=None, seed: int = None,
     factor norm_coef[1:] of zs_grad_norm), read when the kernel runs. seed:
     8-bit moments are rounded stochastically with random numbers of this seed
     (a new one each step) instead of to nearest."""
-    h = _hp(hp)
-    scale = None
+    lib = load()
+    h = ctypes.byref(_hp(hp))
+    ref, scale, opts = table._ref, None, None
     if grad_scale is not None:
         _typed(grad_scale, "grad_scale", _torch().float32, 1)
-        if table.image is not None and grad_scale.device != table.image.device:
-            raise ValueError("grad_scale must be on the table's device")
+        if ref is not None:
+            _same_device((ref, grad_scale), "zs_adamw_multi")
         scale = grad_scale.data_ptr()
-    opts = None
     if seed is not None:
         opts = ctypes.byref(zs_round_opts(1, 0, int(seed) & (2**64 - 1)))
-    if table._ref is None:
-        _check(load().zs_adamw_multi(table._multi, None, ctypes.byref(h), scale, opts, None))
+    if ref is None:
+        _check(lib.zs_adamw_multi(table._multi, None, h, scale, opts, None))
         return
-    with _on(table._ref):
-        multi, image, s = table._args(stream, table._ref)
-        _check(load().zs_adamw_multi(multi, image, ctypes.byref(h), scale, opts, s))
+    _enqueue(lib.zs_adamw_multi, ref, stream, table._multi, table._image(stream), h, scale, opts)
 
 
 def zs_grad_norm(table: MultiTable, max_norm: float, sumsq, norm_coef, workspace,
                  stream=None) -> None:
     """sumsq (float64, 1 element) = sum of the squares of every gradient;
     norm_coef (float32, 2) = its root and the factor that clips it to max_norm.
-    workspace: uint8 device tensor of ZS_NORM_WORKSPACE bytes."""
+    workspace: uint8 device tensor of ZS_NORM_WORKSPACE bytes, zeroed once; one
+    for each of calls that may run at the same time."""
     torch = _torch()
     _typed(sumsq, "sumsq", torch.float64, 1)
-    _norm_coef(norm_coef)
+    _typed(norm_coef, "norm_coef", torch.float32, 2)
     _typed(workspace, "workspace", torch.uint8)
     if workspace.numel() < ZS_NORM_WORKSPACE:
         raise ValueError(f"workspace must hold {ZS_NORM_WORKSPACE} bytes")
-    _same_device([sumsq, norm_coef, workspace] + ([table._ref] if table._ref is not None else []),
-                 "zs_grad_norm")
-    with _on(sumsq):
-        multi, image, s = table._args(stream, sumsq)
-        _check(load().zs_grad_norm(multi, image, float(max_norm), sumsq.data_ptr(),
-                                   norm_coef.data_ptr(), workspace.data_ptr(), s))
+    _same_device((sumsq, norm_coef, workspace) if table._ref is None
+                 else (sumsq, norm_coef, workspace, table._ref), "zs_grad_norm")
+    _enqueue(load().zs_grad_norm, sumsq, stream, table._multi, table._image(stream),
+             float(max_norm), sumsq.data_ptr(), norm_coef.data_ptr(), workspace.data_ptr())
 
 
 def zs_clip_coef(sumsq: Sequence, max_norm: float, norm_coef, stream=None) -> None:
@@ -831,11 +840,10 @@ def zs_clip_coef(sumsq: Sequence, max_norm: float, norm_coef, stream=None) -> No
     sumsq = list(sumsq)
     for r, t in enumerate(sumsq):
         _typed(t, f"sumsq[{r}]", torch.float64, 1)
-    _norm_coef(norm_coef)
+    _typed(norm_coef, "norm_coef", torch.float32, 2)
     _same_device(sumsq + [norm_coef], "zs_clip_coef")
-    with _on(norm_coef):
-        _check(load().zs_clip_coef(_ptr_array(sumsq), len(sumsq), float(max_norm),
-                                   norm_coef.data_ptr(), _stream(norm_coef, stream)))
+    _enqueue(load().zs_clip_coef, norm_coef, stream, _ptr_array(sumsq), len(sumsq),
+             float(max_norm), norm_coef.data_ptr())
 
 
 # ------------------------------------------------------------- 8-bit moments
@@ -849,60 +857,51 @@ def zs_state8_layout(numels: Sequence[int]) -> List[int]:
     return list(off)
 
 
-def _state8(codes, scales, S):
-    torch = _torch()
-    _typed(codes, "codes", torch.uint8, S)
-    _typed(scales, "scales", torch.uint8, -(-S // 256))
-
-
 def zs_state8_encode(x, kind: int, codes, scales, stream=None) -> None:
     """codes (uint8, S) and scales (uint8, ceil(S / 256)) of the moments x
     (float32, S), rounded to nearest; kind ZS_STATE8_M or ZS_STATE8_V."""
+    torch = _torch()
     S = x.numel()
-    _typed(x, "x", _torch().float32)
-    _state8(codes, scales, S)
-    _same_device([x, codes, scales], "zs_state8_encode")
-    with _on(x):
-        _check(load().zs_state8_encode(x.data_ptr(), S, int(kind), codes.data_ptr(),
-                                       scales.data_ptr(), _stream(x, stream)))
+    _typed(x, "x", torch.float32)
+    _typed(codes, "codes", torch.uint8, S)
+    _typed(scales, "scales", torch.uint8, -(-S // 256))
+    _same_device((x, codes, scales), "zs_state8_encode")
+    _enqueue(load().zs_state8_encode, x, stream, x.data_ptr(), S, int(kind), codes.data_ptr(),
+             scales.data_ptr())
 
 
 def zs_state8_decode(codes, scales, kind: int, out, stream=None) -> None:
     """out (float32 or bf16, S) = the values of S 8-bit moments."""
+    torch = _torch()
     S = codes.numel()
-    _state8(codes, scales, S)
+    _typed(codes, "codes", torch.uint8)
+    _typed(scales, "scales", torch.uint8, -(-S // 256))
     _dev(out, "out")
-    code = _dtype_code(out)
     if out.numel() != S:
         raise ValueError(f"out must hold {S} elements")
-    _same_device([out, codes, scales], "zs_state8_decode")
-    with _on(out):
-        _check(load().zs_state8_decode(codes.data_ptr(), scales.data_ptr(), S, int(kind), code,
-                                       out.data_ptr(), _stream(out, stream)))
+    _same_device((out, codes, scales), "zs_state8_decode")
+    _enqueue(load().zs_state8_decode, out, stream, codes.data_ptr(), scales.data_ptr(), S,
+             int(kind), _dtype_code(out), out.data_ptr())
 
 
 # ------------------------------------------------------------- 4-bit shards
-def _mx4(codes, scales, S, what=""):
-    torch = _torch()
-    _typed(codes, f"codes{what}", torch.uint8, -(-S // 2))
-    _typed(scales, f"scales{what}", torch.uint8, -(-S // 32))
-
-
 def zs_quantize_mx4(src, codes, scales, stream=None) -> None:
     """codes (uint8, ceil(S / 2)) and scales (uint8, ceil(S / 32)) of a bf16 or
     fp32 shard of S elements in microscaled 4-bit floating point."""
+    torch = _torch()
     S = src.numel()
     _dev(src, "src")
     code = _dtype_code(src)
-    _mx4(codes, scales, S)
-    _same_device([src, codes, scales], "zs_quantize_mx4")
-    with _on(src):
-        _check(load().zs_quantize_mx4(src.data_ptr(), code, S, codes.data_ptr(),
-                                      scales.data_ptr(), _stream(src, stream)))
+    _typed(codes, "codes", torch.uint8, -(-S // 2))
+    _typed(scales, "scales", torch.uint8, -(-S // 32))
+    _same_device((src, codes, scales), "zs_quantize_mx4")
+    _enqueue(load().zs_quantize_mx4, src, stream, src.data_ptr(), code, S, codes.data_ptr(),
+             scales.data_ptr())
 
 
 def zs_gather_unit_mx4(codes: Sequence, scales: Sequence, flat_out, stream=None) -> None:
     """flat_out[r*S + i] (bf16 or fp32) = value of element i of 4-bit shard r."""
+    uint8 = _torch().uint8
     codes, scales = list(codes), list(scales)
     D = len(codes)
     _dev(flat_out, "flat_out")
@@ -910,12 +909,12 @@ def zs_gather_unit_mx4(codes: Sequence, scales: Sequence, flat_out, stream=None)
     if D < 1 or len(scales) != D or flat_out.numel() % D:
         raise ValueError("need D codes, D scales and a flat_out of D * S elements")
     S = flat_out.numel() // D
-    for r in range(D):
-        _mx4(codes[r], scales[r], S, f"[{r}]")
+    for c, s in zip(codes, scales):
+        _typed(c, "every shard's codes", uint8, -(-S // 2))
+        _typed(s, "every shard's scales", uint8, -(-S // 32))
     _same_device(codes + scales + [flat_out], "zs_gather_unit_mx4")
-    with _on(flat_out):
-        _check(load().zs_gather_unit_mx4(_ptr_array(codes), _ptr_array(scales), D, S, code,
-                                         flat_out.data_ptr(), _stream(flat_out, stream)))
+    _enqueue(load().zs_gather_unit_mx4, flat_out, stream, _ptr_array(codes), _ptr_array(scales), D,
+             S, code, flat_out.data_ptr())
 
 
 ZS_PROBE_READ, ZS_PROBE_WRITE, ZS_PROBE_COPY, ZS_PROBE_TRIAD = 0, 1, 2, 3

@@ -1,6 +1,5 @@
 // Entry points over many tensors (zs_multi_*, zs_adamw_multi, zs_grad_norm), of the
-// 8-bit moments and of the 4-bit shards: host-side checks, then one launch (the norm:
-// two). Nothing here allocates device memory or synchronizes.
+// 8-bit moments and of the 4-bit shards: host-side checks, then one launch. Nothing here allocates device memory or synchronizes.
 
 #include <algorithm>
 #include <cmath>
@@ -281,7 +280,6 @@ ZS_EXPORT zs_status zs_grad_norm(const zs_multi* multi, const void* image, doubl
                                  double* sumsq, float* norm_coef, void* workspace,
                                  hipStream_t stream) {
     const char* who = "zs_grad_norm";
-    static_assert(kNormGrid * sizeof(double) <= ZS_NORM_WORKSPACE, "the workspace holds a grid");
     zs_status st = check_multi(who, multi, image);
     if (st != ZS_OK) return st;
     st = check_max_norm(who, max_norm);
@@ -309,7 +307,7 @@ ZS_EXPORT zs_status zs_grad_norm(const zs_multi* multi, const void* image, doubl
         }
     }
     return hip_status(launch_norm(image_of(*multi, image), multi->dtype, max_norm, sumsq, norm_coef,
-                                  static_cast<double*>(workspace), stream),
+                                  static_cast<NormWorkspace*>(workspace), stream),
                       who);
 }
 

@@ -24,6 +24,16 @@ struct MultiArgs {
     const float* grad_scale;  // device, or nullptr
     uint32_t seed_lo, seed_hi;
 };
+constexpr unsigned kNormGroups = 16;
+struct NormWorkspace {
+    struct Count {  // on a cache line of its own; 0 between calls
+        uint32_t n, pad[31];
+    };
+    Count groups;                // groups of workgroups that are done
+    Count arrived[kNormGroups];  // workgroups of a group that are done
+    double partial[kNormGrid];
+};
+static_assert(sizeof(NormWorkspace) <= ZS_NORM_WORKSPACE, "the caller's workspace holds it");
 hipError_t launch_multi(const MultiImage& im, int state, int dtype, MultiArgs a, bool stoch,
                         hipStream_t stream);
 hipError_t launch_encode8(const float* x, int64_t S, bool is_signed, uint8_t* codes,
@@ -31,7 +41,7 @@ hipError_t launch_encode8(const float* x, int64_t S, bool is_signed, uint8_t* co
 hipError_t launch_decode8(const uint8_t* codes, const uint8_t* scales, int64_t S, bool is_signed,
                           int dtype, void* out, hipStream_t stream);
 hipError_t launch_norm(const MultiImage& im, int dtype, double max_norm, double* sumsq,
-                       float* norm_coef, double* partial, hipStream_t stream);
+                       float* norm_coef, NormWorkspace* ws, hipStream_t stream);
 hipError_t launch_clip(const PtrPack& sums, int D, double max_norm, float* norm_coef,
                        hipStream_t stream);
 hipError_t launch_quantize_mx4(const void* src, int dtype, int64_t S, uint8_t* codes,

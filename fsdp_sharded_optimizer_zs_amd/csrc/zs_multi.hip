@@ -48,90 +48,91 @@ __device__ __forceinline__ G* global(P* p) {
     return reinterpret_cast<G*>(reinterpret_cast<uintptr_t>(p));
 }
 
-// Four consecutive gradient elements, widened: whole (lanes of a full quarter)
-// or the first `live` of them, the others 0.
-template <int DT>
-__device__ __forceinline__ void load_grad(const void* base, int64_t i, float (&x)[4]) {
-    if constexpr (DT == ZS_BF16) {
-        const u32x2 h = __builtin_nontemporal_load(
-            reinterpret_cast<const g_u32x2*>(global<const g_u16>(base) + i));
-        x[0] = bf16_lo(h[0]), x[1] = bf16_hi(h[0]), x[2] = bf16_lo(h[1]), x[3] = bf16_hi(h[1]);
-    } else {
-        const f32x4 a = __builtin_nontemporal_load(
-            reinterpret_cast<const g_f32x4*>(global<const g_f32>(base) + i));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = a[e];
-    }
-}
-template <int DT>
-__device__ __forceinline__ void load_grad_part(const void* base, int64_t i, int live,
-                                               float (&x)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[e] = 0.0f;
-        if (e < live) {
-            if constexpr (DT == ZS_BF16)
-                x[e] = __uint_as_float(uint32_t(global<const g_u16>(base)[i + e]) << 16);
-            else
-                x[e] = global<const g_f32>(base)[i + e];
-        }
-    }
-}
-
-__device__ __forceinline__ void load_f32(const float* base, int64_t i, float (&x)[4]) {
-    const f32x4 a = __builtin_nontemporal_load(
-        reinterpret_cast<const g_f32x4*>(global<const g_f32>(base) + i));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = a[e];
-}
-__device__ __forceinline__ void load_f32_part(const float* base, int64_t i, int live,
-                                              float (&x)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = e < live ? global<const g_f32>(base)[i + e] : 0.0f;
-}
-__device__ __forceinline__ void store_f32(float* base, int64_t i, const float (&x)[4]) {
-    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]},
-                                reinterpret_cast<g_f32x4*>(global<g_f32>(base) + i));
-}
-__device__ __forceinline__ void store_f32_part(float* base, int64_t i, int live,
-                                               const float (&x)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < live) global<g_f32>(base)[i + e] = x[e];
-}
-__device__ __forceinline__ void store_bf16(uint16_t* base, int64_t i, const float (&x)[4]) {
-    const u32x2 h{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-    __builtin_nontemporal_store(h, reinterpret_cast<g_u32x2*>(global<g_u16>(base) + i));
-}
-__device__ __forceinline__ void store_bf16_part(uint16_t* base, int64_t i, int live,
-                                                const float (&x)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < live) global<g_u16>(base)[i + e] = uint16_t(f32_to_bf16(x[e]));
-}
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* base, int64_t i) {
-    return __builtin_nontemporal_load(
-        reinterpret_cast<const g_u32*>(global<const g_u8>(base) + i));
-}
-__device__ __forceinline__ uint32_t load_codes_part(const uint8_t* base, int64_t i, int live) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < live) w |= uint32_t(global<const g_u8>(base)[i + e]) << (8 * e);
-    return w;
-}
-__device__ __forceinline__ void store_codes(uint8_t* base, int64_t i, uint32_t w) {
-    __builtin_nontemporal_store(w, reinterpret_cast<g_u32*>(global<g_u8>(base) + i));
-}
-__device__ __forceinline__ void store_codes_part(uint8_t* base, int64_t i, int live, uint32_t w) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < live) global<g_u8>(base)[i + e] = uint8_t(w >> (8 * e));
-}
-
 // Elements of [i, n) that a lane's four hold: 0 .. 4.
 __device__ __forceinline__ int live_of(int64_t i, int64_t n) {
     return i >= n ? 0 : (n - i >= 4 ? 4 : int(n - i));
+}
+
+// Four consecutive elements from i, of which the first `live` exist (the others read as
+// 0 and are not written). Lanes whose four all exist access them at once; with ALL every
+// lane does, and `live` is not looked at.
+template <bool ALL>
+__device__ __forceinline__ void load_f32(const float* base, int64_t i, int live, float (&x)[4]) {
+    const g_f32* s = global<const g_f32>(base) + i;
+    if (ALL || live == 4) {
+        const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const g_f32x4*>(s));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = a[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = e < live ? s[e] : 0.0f;
+    }
+}
+template <bool ALL>
+__device__ __forceinline__ void store_f32(float* base, int64_t i, int live, const float (&x)[4]) {
+    g_f32* d = global<g_f32>(base) + i;
+    if (ALL || live == 4) {
+        __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<g_f32x4*>(d));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < live) d[e] = x[e];
+    }
+}
+// Gradients, widened.
+template <int DT, bool ALL>
+__device__ __forceinline__ void load_grad(const void* base, int64_t i, int live, float (&x)[4]) {
+    if constexpr (DT == ZS_F32) {
+        load_f32<ALL>(static_cast<const float*>(base), i, live, x);
+    } else {
+        const g_u16* s = global<const g_u16>(base) + i;
+        u32x2 h{0, 0};
+        if (ALL || live == 4) {
+            h = __builtin_nontemporal_load(reinterpret_cast<const g_u32x2*>(s));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (e < live) h[e / 2] |= uint32_t(s[e]) << (16 * (e & 1));
+        }
+        x[0] = bf16_lo(h[0]), x[1] = bf16_hi(h[0]), x[2] = bf16_lo(h[1]), x[3] = bf16_hi(h[1]);
+    }
+}
+template <bool ALL>
+__device__ __forceinline__ void store_bf16(uint16_t* base, int64_t i, int live,
+                                           const float (&x)[4]) {
+    g_u16* d = global<g_u16>(base) + i;
+    const u32x2 h{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+    if (ALL || live == 4) {
+        __builtin_nontemporal_store(h, reinterpret_cast<g_u32x2*>(d));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < live) d[e] = uint16_t(h[e / 2] >> (16 * (e & 1)));
+    }
+}
+template <bool ALL>
+__device__ __forceinline__ uint32_t load_codes(const void* base, int64_t i, int live) {
+    const g_u8* s = global<const g_u8>(base) + i;
+    uint32_t w = 0;
+    if (ALL || live == 4) {
+        w = __builtin_nontemporal_load(reinterpret_cast<const g_u32*>(s));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < live) w |= uint32_t(s[e]) << (8 * e);
+    }
+    return w;
+}
+template <bool ALL>
+__device__ __forceinline__ void store_codes(void* base, int64_t i, int live, uint32_t w) {
+    g_u8* d = global<g_u8>(base) + i;
+    if (ALL || live == 4) {
+        __builtin_nontemporal_store(w, reinterpret_cast<g_u32*>(d));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < live) d[e] = uint8_t(w >> (8 * e));
+    }
 }
 
 // ------------------------------------------------------------- 8-bit moments
@@ -237,48 +238,36 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 
 // ------------------------------------------------------------- the step
 
-// fp32 moments: the first `live` elements of each lane of one quarter.
-template <int DT>
-__device__ __forceinline__ void step32_part(const zs_multi_tensor& t, int64_t i, int live,
+// fp32 moments: a wavefront's 1024 elements from base (lane's first i), those below n;
+// every load ahead of the arithmetic, and each quarter stored as soon as it is done.
+// (202M parameters, bf16 gradients: 931 us, 6.1 TB/s, where a copy reaches 6.55; storing
+// stream by stream after all four quarters 993, loading two quarters at a time 951, one
+// at a time 954; fewer wavefronts a SIMD 944-965; temporal loads 1019.)
+template <int DT, bool ALL>
+__device__ __forceinline__ void step32_wave(const zs_multi_tensor& t, int64_t i, int64_t n,
                                             const MultiArgs& a, float mult) {
-    float p[4], m[4], v[4], g[4];
-    load_f32_part(t.p, i, live, p);
-    load_f32_part(static_cast<const float*>(t.m), i, live, m);
-    load_f32_part(static_cast<const float*>(t.v), i, live, v);
-    load_grad_part<DT>(t.g, i, live, g);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) adamw1(p[e], m[e], v[e], g[e] * mult, a.k);
-    store_f32_part(t.p, i, live, p);
-    store_f32_part(static_cast<float*>(t.m), i, live, m);
-    store_f32_part(static_cast<float*>(t.v), i, live, v);
-    if (t.w_out) store_bf16_part(t.w_out, i, live, p);
-}
-
-// fp32 moments: a wavefront's 1024 elements, every load ahead of the arithmetic.
-template <int DT>
-__device__ __forceinline__ void step32_wave(const zs_multi_tensor& t, int64_t i,
-                                            const MultiArgs& a, float mult) {
+    float* const tm = static_cast<float*>(t.m);
+    float* const tv = static_cast<float*>(t.v);
     float p[kQ][4], m[kQ][4], v[kQ][4], g[kQ][4];
+    int live[kQ];
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-        load_f32(t.p, i + q * kQuarter, p[q]);
-        load_f32(static_cast<const float*>(t.m), i + q * kQuarter, m[q]);
-        load_f32(static_cast<const float*>(t.v), i + q * kQuarter, v[q]);
-        load_grad<DT>(t.g, i + q * kQuarter, g[q]);
+        const int64_t at = i + q * kQuarter;
+        live[q] = ALL ? 4 : live_of(at, n);
+        load_f32<ALL>(t.p, at, live[q], p[q]);
+        load_f32<ALL>(tm, at, live[q], m[q]);
+        load_f32<ALL>(tv, at, live[q], v[q]);
+        load_grad<DT, ALL>(t.g, at, live[q], g[q]);
     }
 #pragma unroll
-    for (int q = 0; q < kQ; ++q)
+    for (int q = 0; q < kQ; ++q) {
+        const int64_t at = i + q * kQuarter;
 #pragma unroll
         for (int e = 0; e < 4; ++e) adamw1(p[q][e], m[q][e], v[q][e], g[q][e] * mult, a.k);
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) store_f32(t.p, i + q * kQuarter, p[q]);
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) store_f32(static_cast<float*>(t.m), i + q * kQuarter, m[q]);
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) store_f32(static_cast<float*>(t.v), i + q * kQuarter, v[q]);
-    if (t.w_out) {
-#pragma unroll
-        for (int q = 0; q < kQ; ++q) store_bf16(t.w_out, i + q * kQuarter, p[q]);
+        store_f32<ALL>(t.p, at, live[q], p[q]);
+        store_f32<ALL>(tm, at, live[q], m[q]);
+        store_f32<ALL>(tv, at, live[q], v[q]);
+        if (t.w_out) store_bf16<ALL>(t.w_out, at, live[q], p[q]);
     }
 }
 
@@ -304,19 +293,17 @@ __device__ __forceinline__ uint32_t tensor_key(const MultiArgs& a, int32_t tenso
     return mix(mix(a.seed_lo + 0x9e3779b9u * uint32_t(tensor + 1)) + a.seed_hi);
 }
 
-// 8-bit moments, any case: the first `live` elements of each lane of one quarter, its
+// 8-bit moments, any case: one quarter, the first `live` elements of each lane, its
 // scale bytes sm and sv in and out.
 template <int DT, bool STOCH, bool EXACT>
-__device__ __forceinline__ void step8_part(const zs_multi_tensor& t, int64_t i, int live,
-                                           const MultiArgs& a, float mult, uint32_t key, int* sm,
-                                           int* sv) {
+__device__ __forceinline__ void step8_quarter(const zs_multi_tensor& t, int64_t i, int live,
+                                              const MultiArgs& a, float mult, uint32_t key,
+                                              int* sm, int* sv) {
     float p[4], m[4], v[4], g[4];
-    uint8_t* const mc = static_cast<uint8_t*>(t.m);
-    uint8_t* const vc = static_cast<uint8_t*>(t.v);
-    load_f32_part(t.p, i, live, p);
-    load_grad_part<DT>(t.g, i, live, g);
-    decode4<true>(load_codes_part(mc, i, live), *sm, m);
-    decode4<false>(load_codes_part(vc, i, live), *sv, v);
+    load_f32<false>(t.p, i, live, p);
+    load_grad<DT, false>(t.g, i, live, g);
+    decode4<true>(load_codes<false>(t.m, i, live), *sm, m);
+    decode4<false>(load_codes<false>(t.v, i, live), *sv, v);
     uint32_t rm[4] = {}, rv[4] = {};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -332,10 +319,10 @@ __device__ __forceinline__ void step8_part(const zs_multi_tensor& t, int64_t i, 
     }
     *sm = scale_of<true>(wave_max(top_bits(m)));
     *sv = scale_of<false>(wave_max(top_bits(v)));
-    store_codes_part(mc, i, live, encode4<true, STOCH>(m, *sm, rm));
-    store_codes_part(vc, i, live, encode4<false, STOCH>(v, *sv, rv));
-    store_f32_part(t.p, i, live, p);
-    if (t.w_out) store_bf16_part(t.w_out, i, live, p);
+    store_codes<false>(t.m, i, live, encode4<true, STOCH>(m, *sm, rm));
+    store_codes<false>(t.v, i, live, encode4<false, STOCH>(v, *sv, rv));
+    store_f32<false>(t.p, i, live, p);
+    if (t.w_out) store_bf16<false>(t.w_out, i, live, p);
 }
 
 // Codes as encode4 gives them, for a scale byte below 254: then the largest magnitude
@@ -377,31 +364,41 @@ struct Loaded8 {
     float p[kQ][4], g[kQ][4];
     uint32_t wm[kQ], wv[kQ];
 };
-template <int DT>
-__device__ __forceinline__ void load8_wave(const zs_multi_tensor& t, int64_t i, Loaded8& d) {
+template <int DT, bool ALL>
+__device__ __forceinline__ void load8_wave(const zs_multi_tensor& t, int64_t i, int64_t n,
+                                           Loaded8& d) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-        d.wm[q] = load_codes(static_cast<const uint8_t*>(t.m), i + q * kQuarter);
-        d.wv[q] = load_codes(static_cast<const uint8_t*>(t.v), i + q * kQuarter);
-        load_grad<DT>(t.g, i + q * kQuarter, d.g[q]);
-        load_f32(t.p, i + q * kQuarter, d.p[q]);
+        const int64_t at = i + q * kQuarter;
+        const int live = ALL ? 4 : live_of(at, n);
+        d.wm[q] = load_codes<ALL>(t.m, at, live);
+        d.wv[q] = load_codes<ALL>(t.v, at, live);
+        load_grad<DT, ALL>(t.g, at, live, d.g[q]);
+        load_f32<ALL>(t.p, at, live, d.p[q]);
     }
+    // keeps the loads here, in flight beside the scale bytes, ahead of the branch that
+    // waits for those
+    asm volatile("" ::: "memory");
 }
 
-// 8-bit moments: a wavefront's 1024 elements; lane q < 4 holds the scale bytes of
-// quarter q, in and out. A code's value needs no scaling of its own: B1 * m is taken as
-// (B1 * 2^(s - 15)) * float_of_bits(c << 20), the same real product, rounded once.
-template <bool STOCH>
+// 8-bit moments: a wavefront's elements from i on, those below n; lane q < 4 holds the
+// scale bytes of quarter q, in and out. A code's value needs no scaling of its own: B1 * m
+// is taken as (B1 * 2^(s - 15)) * float_of_bits(c << 20), the same real product, rounded
+// once. What does not exist was loaded as zeros; its m and v stay 0 (no part of the
+// block's largest).
+template <bool STOCH, bool ALL>
 __device__ __forceinline__ void step8_wave(const zs_multi_tensor& t, Loaded8& d, int64_t i,
-                                           int lane, const MultiArgs& a, float mult, uint32_t key,
-                                           int* lm, int* lv) {
+                                           int64_t n, int lane, const MultiArgs& a, float mult,
+                                           uint32_t key, int* lm, int* lv) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
+        if (!ALL && i - 4 * lane + q * kQuarter >= n) break;
         const float b1 = __builtin_ldexpf(a.k.b1, __builtin_amdgcn_readlane(*lm, q) - 15);
         const float b2 = __builtin_ldexpf(a.k.b2, __builtin_amdgcn_readlane(*lv, q) - 31);
+        const int64_t at = i + q * kQuarter;
+        const int live = ALL ? 4 : live_of(at, n);
         float m[4], v[4];
         uint32_t r[4] = {};
-        const uint32_t at = uint32_t(i + q * kQuarter) ^ key;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int cm = (int(d.wm[q] << (24 - 8 * e)) >> 4) & int(0x87f00000u);
@@ -411,7 +408,8 @@ __device__ __forceinline__ void step8_wave(const zs_multi_tensor& t, Loaded8& d,
             m[e] = (b1 * __uint_as_float(uint32_t(cm))) + (a.k.b1c * x);
             v[e] = (b2 * __uint_as_float(cv)) + (a.k.b2c * (x * x));
             d.p[q][e] = new_p<false>(d.p[q][e], m[e], v[e], a);
-            if constexpr (STOCH) r[e] = mix(at ^ uint32_t(e));
+            if (!ALL && e >= live) m[e] = v[e] = 0.0f;  // 0 * mult may be NaN
+            if constexpr (STOCH) r[e] = mix(uint32_t(at + e) ^ key);
         }
         const int sm = scale_of<true>(wave_max(top_bits(m)));
         const int sv = scale_of<false>(wave_max(top_bits(v)));
@@ -428,10 +426,10 @@ __device__ __forceinline__ void step8_wave(const zs_multi_tensor& t, Loaded8& d,
             *lm = sm;
             *lv = sv;
         }
-        store_f32(t.p, i + q * kQuarter, d.p[q]);
-        if (t.w_out) store_bf16(t.w_out, i + q * kQuarter, d.p[q]);
-        store_codes(static_cast<uint8_t*>(t.m), i + q * kQuarter, wm);
-        store_codes(static_cast<uint8_t*>(t.v), i + q * kQuarter, wv);
+        store_f32<ALL>(t.p, at, live, d.p[q]);
+        if (t.w_out) store_bf16<ALL>(t.w_out, at, live, d.p[q]);
+        store_codes<ALL>(t.m, at, live, wm);
+        store_codes<ALL>(t.v, at, live, wv);
     }
 }
 
@@ -447,13 +445,8 @@ __global__ __launch_bounds__(kThreads) void multi32_kernel(
         const zs_multi_tensor t = table[ch.tensor];
         const int64_t n = t.numel;
         const int64_t base = int64_t(ch.index) * ZS_MULTI_CHUNK + wave * kWaveElems;
-        if (base + kWaveElems <= n) {
-            step32_wave<DT>(t, base + 4 * lane, a, mult);
-        } else {
-#pragma unroll 1
-            for (int64_t b = base; b < n; b += kQuarter)
-                step32_part<DT>(t, b + 4 * lane, live_of(b + 4 * lane, n), a, mult);
-        }
+        if (base + kWaveElems <= n) step32_wave<DT, true>(t, base + 4 * lane, n, a, mult);
+        else if (base < n) step32_wave<DT, false>(t, base + 4 * lane, n, a, mult);
     }
 }
 
@@ -480,23 +473,27 @@ __global__ __launch_bounds__(kThreads) void multi8_kernel(
             lm = *ms;
             lv = *vs;
         }
-        const bool whole = !EXACT && base + kWaveElems <= n;
-        Loaded8 d;
-        if (whole) {
-            load8_wave<DT>(t, base + 4 * lane, d);
-            // keeps the loads here, in flight beside the scale bytes, ahead of the branch
-            // that waits for those
-            asm volatile("" ::: "memory");
+        const int64_t i = base + 4 * lane;
+        bool done = false;
+        if constexpr (!EXACT) {
+            Loaded8 d;
+            if (base + kWaveElems <= n) {
+                load8_wave<DT, true>(t, i, n, d);
+                done = __all(lm <= kMostM && lv <= kMostV);
+                if (done) step8_wave<STOCH, true>(t, d, i, n, lane, a, mult, key, &lm, &lv);
+            } else {
+                load8_wave<DT, false>(t, i, n, d);
+                done = __all(lm <= kMostM && lv <= kMostV);
+                if (done) step8_wave<STOCH, false>(t, d, i, n, lane, a, mult, key, &lm, &lv);
+            }
         }
-        if (whole && __all(lm <= kMostM && lv <= kMostV)) {
-            step8_wave<STOCH>(t, d, base + 4 * lane, lane, a, mult, key, &lm, &lv);
-        } else {
+        if (!done) {
 #pragma unroll 1
             for (int q = 0; q < kQ && base + q * kQuarter < n; ++q) {
-                const int64_t i = base + q * kQuarter + 4 * lane;
+                const int64_t at = i + q * kQuarter;
                 int sm = __builtin_amdgcn_readlane(lm, q);
                 int sv = __builtin_amdgcn_readlane(lv, q);
-                step8_part<DT, STOCH, EXACT>(t, i, live_of(i, n), a, mult, key, &sm, &sv);
+                step8_quarter<DT, STOCH, EXACT>(t, at, live_of(at, n), a, mult, key, &sm, &sv);
                 if (lane == q) {
                     lm = sm;
                     lv = sv;
@@ -512,32 +509,38 @@ __global__ __launch_bounds__(kThreads) void multi8_kernel(
 
 // ------------------------------------------------------------- conversions
 
-// One block of 256 elements per wavefront.
+// kQ blocks of 256 elements per wavefront, all loads first. (One block a wavefront ran
+// the decode at half the rate.)
 template <bool SIGNED>
 __global__ __launch_bounds__(kThreads) void encode8_kernel(const float* __restrict__ x, int64_t S,
                                                            uint8_t* __restrict__ codes,
                                                            uint8_t* __restrict__ scales) {
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    const int64_t blocks = (S + kQuarter - 1) / kQuarter;
     const uint32_t none[4] = {};
-    for (int64_t b = int64_t(blockIdx.x) * kWaves + wave; b < blocks;
-         b += int64_t(gridDim.x) * kWaves) {
-        const int64_t i = b * kQuarter + 4 * lane;
-        const int live = live_of(i, S);
-        float y[4];
-        if (live == 4) load_f32(x, i, y);
-        else load_f32_part(x, i, live, y);
-        if constexpr (!SIGNED) {
+    for (int64_t base = (int64_t(blockIdx.x) * kWaves + wave) * kWaveElems; base < S;
+         base += int64_t(gridDim.x) * kWaves * kWaveElems) {
+        float y[kQ][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (y[e] < 0.0f) y[e] = __uint_as_float(0x7fc00000u);
+        for (int q = 0; q < kQ; ++q) {
+            const int64_t i = base + q * kQuarter + 4 * lane;
+            load_f32<false>(x, i, live_of(i, S), y[q]);
         }
-        const int s = scale_of<SIGNED>(wave_max(top_bits(y)));
-        const uint32_t w = encode4<SIGNED, false>(y, s, none);
-        if (live == 4) store_codes(codes, i, w);
-        else store_codes_part(codes, i, live, w);
-        if (lane == 0) global<g_u8>(scales)[b] = uint8_t(s);
+        int mine = 0;  // lane q: the scale byte of quarter q
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+            const int64_t i = base + q * kQuarter + 4 * lane;
+            if constexpr (!SIGNED) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (y[q][e] < 0.0f) y[q][e] = __uint_as_float(0x7fc00000u);
+            }
+            const int s = scale_of<SIGNED>(wave_max(top_bits(y[q])));
+            store_codes<false>(codes, i, live_of(i, S), encode4<SIGNED, false>(y[q], s, none));
+            if (lane == q) mine = s;
+        }
+        if (lane < kQ && base + lane * kQuarter < S)
+            global<g_u8>(scales)[base / kQuarter + lane] = uint8_t(mine);
     }
 }
 
@@ -547,28 +550,37 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const uint8_t* __rest
                                                            int64_t S, void* __restrict__ out) {
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    const int64_t blocks = (S + kQuarter - 1) / kQuarter;
-    for (int64_t b = int64_t(blockIdx.x) * kWaves + wave; b < blocks;
-         b += int64_t(gridDim.x) * kWaves) {
-        const int64_t i = b * kQuarter + 4 * lane;
-        const int live = live_of(i, S);
-        const int s = __builtin_amdgcn_readfirstlane(int(global<const g_u8>(scales)[b]));
-        const uint32_t w = live == 4 ? load_codes(codes, i) : load_codes_part(codes, i, live);
-        float x[4];
-        decode4<SIGNED>(w, s, x);
-        if constexpr (DT == ZS_F32) {
-            if (live == 4) store_f32(static_cast<float*>(out), i, x);
-            else store_f32_part(static_cast<float*>(out), i, live, x);
-        } else {
-            if (live == 4) store_bf16(static_cast<uint16_t*>(out), i, x);
-            else store_bf16_part(static_cast<uint16_t*>(out), i, live, x);
+    for (int64_t base = (int64_t(blockIdx.x) * kWaves + wave) * kWaveElems; base < S;
+         base += int64_t(gridDim.x) * kWaves * kWaveElems) {
+        int mine = 0;
+        if (lane < kQ && base + lane * kQuarter < S)
+            mine = global<const g_u8>(scales)[base / kQuarter + lane];
+        uint32_t w[kQ];
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+            const int64_t i = base + q * kQuarter + 4 * lane;
+            w[q] = load_codes<false>(codes, i, live_of(i, S));
+        }
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+            const int64_t i = base + q * kQuarter + 4 * lane;
+            float x[4];
+            decode4<SIGNED>(w[q], __builtin_amdgcn_readlane(mine, q), x);
+            if constexpr (DT == ZS_F32)
+                store_f32<false>(static_cast<float*>(out), i, live_of(i, S), x);
+            else
+                store_bf16<false>(static_cast<uint16_t*>(out), i, live_of(i, S), x);
         }
     }
 }
 
 // ------------------------------------------------------------- the norm
 
-// Sum over the workgroup, in a fixed order, valid in thread 0.
+// Workgroups of the norm are 16 wavefronts, so that few of them fill the chip: each one
+// counts itself in at the end, and additions to one address take about 12 ns apiece.
+constexpr int kNormWaves = kNormThreads / 64;
+
+// Sum over a workgroup of the norm, in a fixed order, valid in thread 0.
 __device__ __forceinline__ double block_sum(double x, double* slot) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) x += __shfl_down(x, d, 64);
@@ -577,45 +589,9 @@ __device__ __forceinline__ double block_sum(double x, double* slot) {
     double s = 0.0;
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) s += slot[w];
+        for (int w = 0; w < kNormWaves; ++w) s += slot[w];
     }
     return s;
-}
-
-// Partial sums of squares: workgroup b takes chunks b, b + gridDim.x, ... In fp64,
-// where the product of two fp32 numbers is exact and no square over- or underflows.
-template <int DT>
-__global__ __launch_bounds__(kThreads) void sumsq_kernel(const zs_multi_tensor* __restrict__ table,
-                                                         const MultiChunk* __restrict__ chunks,
-                                                         int64_t n_chunks,
-                                                         double* __restrict__ partial) {
-    __shared__ double slot[kWaves];
-    const int lane = int(threadIdx.x) & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    double s[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
-        const MultiChunk ch = chunks[c];
-        const void* g = table[ch.tensor].g;
-        const int64_t n = table[ch.tensor].numel;
-        const int64_t base = int64_t(ch.index) * ZS_MULTI_CHUNK + wave * kWaveElems;
-        float x[kQ][4];
-        if (base + kWaveElems <= n) {
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) load_grad<DT>(g, base + q * kQuarter + 4 * lane, x[q]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) {
-                const int64_t i = base + q * kQuarter + 4 * lane;
-                load_grad_part<DT>(g, i, live_of(i, n), x[q]);
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < kQ; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = __builtin_fma(double(x[q][e]), double(x[q][e]), s[e]);
-    }
-    const double t = block_sum((s[0] + s[1]) + (s[2] + s[3]), slot);
-    if (threadIdx.x == 0) partial[blockIdx.x] = t;
 }
 
 __device__ __forceinline__ void write_clip(double sum, double max_norm, float* norm_coef) {
@@ -629,17 +605,89 @@ __device__ __forceinline__ void write_clip(double sum, double max_norm, float* n
     norm_coef[1] = c;
 }
 
-__global__ __launch_bounds__(kThreads) void norm_final_kernel(const double* __restrict__ partial,
-                                                              int n, double max_norm,
-                                                              double* __restrict__ sumsq,
-                                                              float* __restrict__ norm_coef) {
-    __shared__ double slot[kWaves];
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
-    s = block_sum(s, slot);
+// Sum of squares, in fp64, where the product of two fp32 numbers is exact and no square
+// over- or underflows. Workgroup b takes kNormChunks chunks at a time; the one that
+// arrives last adds all partial sums, in their order, and leaves the count at 0 for the
+// next call. Nothing waits: which workgroup is last changes no result.
+//
+// A partial sum is one agent-scope atomic store, written through to memory that all XCDs
+// share, and it has arrived there once the wait for it is over; the count goes up after
+// that wait, so that whoever sees the whole count sees every sum.
+//
+// 3.3M bf16 gradients 6.6 us a call (a second launch for the final sum: 12.4); 108M fp32
+// ones in 2,000 tensors 133 us, 6.5 TB/s. One count for all workgroups 137; 2048 smaller
+// workgroups 140 and, on the 3.3M, 13.8; a release with the count, which writes back and
+// invalidates an XCD's whole L2 for every workgroup, 227 and 20.
+// Counts this workgroup in; true for the last one of the grid. Workgroups count in
+// groups (b mod kNormGroups), the last of each group for the group, so that the counts on
+// one address are few; each count is put back to 0 by the last that adds to it.
+__device__ __forceinline__ uint32_t count(uint32_t* n) {
+    return __hip_atomic_fetch_add(n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+}
+__device__ __forceinline__ void clear(uint32_t* n) {
+    __hip_atomic_store(n, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool arrive(NormWorkspace* ws) {
+    const unsigned group = blockIdx.x % kNormGroups;
+    const unsigned groups = gridDim.x < kNormGroups ? gridDim.x : kNormGroups;
+    const unsigned members = (gridDim.x - group + kNormGroups - 1) / kNormGroups;
+    if (count(&ws->arrived[group].n) != members) return false;
+    clear(&ws->arrived[group].n);
+    if (count(&ws->groups.n) != groups) return false;
+    clear(&ws->groups.n);
+    return true;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(
+    const zs_multi_tensor* __restrict__ table, const MultiChunk* __restrict__ chunks,
+    int64_t n_chunks, double max_norm, NormWorkspace* ws, double* sumsq, float* norm_coef) {
+    __shared__ double slot[kNormWaves];
+    __shared__ bool last;
+    const int lane = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    // 4 wavefronts to a chunk
+    for (int64_t c = int64_t(blockIdx.x) * kNormChunks + wave / kWaves; c < n_chunks;
+         c += int64_t(gridDim.x) * kNormChunks) {
+        const MultiChunk ch = chunks[c];
+        const void* g = table[ch.tensor].g;
+        const int64_t n = table[ch.tensor].numel;
+        const int64_t base =
+            int64_t(ch.index) * ZS_MULTI_CHUNK + (wave % kWaves) * kWaveElems;
+        float x[kQ][4];
+        if (base + kWaveElems <= n) {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q)
+                load_grad<DT, true>(g, base + q * kQuarter + 4 * lane, 4, x[q]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                const int64_t i = base + q * kQuarter + 4 * lane;
+                load_grad<DT, false>(g, i, live_of(i, n), x[q]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = __builtin_fma(double(x[q][e]), double(x[q][e]), s[e]);
+    }
+    const double mine = block_sum((s[0] + s[1]) + (s[2] + s[3]), slot);
     if (threadIdx.x == 0) {
-        *sumsq = s;
-        write_clip(s, max_norm, norm_coef);
+        __hip_atomic_store(&ws->partial[blockIdx.x], mine, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        last = arrive(ws);
+    }
+    __syncthreads();
+    if (!last) return;
+    double sum = 0.0;
+    for (unsigned k = threadIdx.x; k < gridDim.x; k += kNormThreads)
+        sum += __hip_atomic_load(&ws->partial[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    sum = block_sum(sum, slot);
+    if (threadIdx.x == 0) {
+        *sumsq = sum;
+        write_clip(sum, max_norm, norm_coef);
     }
 }
 
@@ -716,20 +764,14 @@ hipError_t launch_decode8(const uint8_t* codes, const uint8_t* scales, int64_t S
 }
 
 hipError_t launch_norm(const MultiImage& im, int dtype, double max_norm, double* sumsq,
-                       float* norm_coef, double* partial, hipStream_t stream) {
-    const int n = int(norm_grid(im.n_chunks));
-    if (n > 0) {
-        if (dtype == ZS_BF16)
-            hipLaunchKernelGGL((sumsq_kernel<ZS_BF16>), dim3(unsigned(n)), dim3(kThreads), 0,
-                               stream, im.table, im.chunks, im.n_chunks, partial);
-        else
-            hipLaunchKernelGGL((sumsq_kernel<ZS_F32>), dim3(unsigned(n)), dim3(kThreads), 0, stream,
-                               im.table, im.chunks, im.n_chunks, partial);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL(norm_final_kernel, dim3(1), dim3(kThreads), 0, stream, partial, n, max_norm,
-                       sumsq, norm_coef);
+                       float* norm_coef, NormWorkspace* ws, hipStream_t stream) {
+    const dim3 grid(unsigned(norm_grid(im.n_chunks)));
+    if (dtype == ZS_BF16)
+        hipLaunchKernelGGL((norm_kernel<ZS_BF16>), grid, dim3(kNormThreads), 0, stream, im.table,
+                           im.chunks, im.n_chunks, max_norm, ws, sumsq, norm_coef);
+    else
+        hipLaunchKernelGGL((norm_kernel<ZS_F32>), grid, dim3(kNormThreads), 0, stream, im.table,
+                           im.chunks, im.n_chunks, max_norm, ws, sumsq, norm_coef);
     return hipGetLastError();
 }
 

@@ -6,16 +6,20 @@
 
 namespace zs {
 
-// Conversions of 8-bit moments: one wavefront per block of 256 elements.
+// Conversions of 8-bit moments: one wavefront per 4 blocks of 256 elements.
 inline int64_t state8_grid(int64_t S) {
-    return grid_blocks(S / 256 + (S % 256 != 0), kBlockThreads / 64);
+    return grid_blocks(S / 1024 + (S % 1024 != 0), kBlockThreads / 64);
 }
 
-// Sums of squares over a table's chunks: as many workgroups as fill the chip (8 on
-// each of 256 CUs), whose partial sums fit zs_grad_norm's workspace; 0 chunks: 0.
-constexpr int64_t kNormGrid = 2048;
+// The norm over a table's chunks: workgroups of 16 wavefronts, 4 to a chunk, at most 2 on
+// each of 256 CUs (which fills them), whose partial sums fit zs_grad_norm's workspace; one
+// if there is nothing.
+constexpr int kNormThreads = 1024;
+constexpr int64_t kNormChunks = 4;
+constexpr int64_t kNormGrid = 512;
 inline int64_t norm_grid(int64_t n_chunks) {
-    return n_chunks < kNormGrid ? n_chunks : kNormGrid;
+    const int64_t b = n_chunks / kNormChunks + (n_chunks % kNormChunks != 0);
+    return b < 1 ? 1 : (b < kNormGrid ? b : kNormGrid);
 }
 
 // 4-bit quantisation: one workgroup per tile of kMx4Unroll groups of 8 elements a lane.

@@ -766,8 +766,9 @@ zs_status zs_state8_decode(const uint8_t* codes, const uint8_t* scales, int64_t 
  *   max_norm      > 0, or infinity: never clip
  *   sumsq         device, one double, 8-byte aligned
  *   norm_coef     device, two floats
- *   workspace     device, ZS_NORM_WORKSPACE bytes, 16-byte aligned, of any
- *                 contents; calls that may run at the same time (other streams,
+ *   workspace     device, ZS_NORM_WORKSPACE bytes, 16-byte aligned, zeroed by the
+ *                 caller before its first use; each call leaves it ready for the
+ *                 next one. Calls that may run at the same time (other streams,
  *                 graphs) need one each
  * A table without elements gives 0, 0 and 1.
  * Errors: ZS_EINVAL, ZS_EALIAS (outputs and workspace overlap, or one of them a
