@@ -679,7 +679,8 @@ typedef struct {
  * instead of an operation order, since roots and divisions rounded to the last bit
  * would cost more than the memory traffic: within 2^-21 |SS * (m' / den)| +
  * 2^-24 (|p * DEC| + |p'|) of the formula's value for these m' and v', the same in every
- * run (with eps < 2^-39 or a beta in (0, 2^-60), p' is the fp32 step's, bit for bit).
+ * run (with EPS * BC2S < 2^-38 or a beta in (0, 2^-60), p' is the fp32 step's, bit for
+ * bit).
  * Blocks of 256 elements, counted from the tensor's
  * first element, share a scale byte s, and a code c stands for
  *   m:  +-float_of_bits((c & 127) << 20) * 2^(s - 15)     (sign in bit 7)

@@ -113,7 +113,8 @@ class Case:
                     (mc, ms), (vc, vs) = self.m[t], self.v[t]
                     p0 = self.p[t]
                     self.p[t], mc, ms, vc, vs, w = F.adamw_step8(p0, mc, ms, vc, vs, g, hp, seed, t)
-                    if hp.eps >= 2.0**-39:
+                    k = O.adamw_constants(hp)
+                    if k["EPS"] * k["BC2S"] >= np.float32(2.0**-38):
                         self.p[t], w = self.near(t, p0, g, hp)
                     self.m[t], self.v[t] = (mc, ms), (vc, vs)
             self.w.append(w)
