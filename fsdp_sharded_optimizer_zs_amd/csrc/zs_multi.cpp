@@ -21,6 +21,7 @@ struct zs_multi {
     int64_t T;
     int64_t n_chunks;
     std::vector<uint8_t> image;
+    std::vector<Range> grads;  // what the gradients cover: sorted, disjoint
 };
 
 namespace {
@@ -125,7 +126,22 @@ zs_status check_alias(const zs_multi_tensor* ts, int32_t T, int32_t state, int e
     return ZS_OK;
 }
 
-// The checks that the moment conversions share; n_scales scale bytes.
+// The union of the gradients' ranges (gradients may overlap each other).
+std::vector<Range> grad_ranges(const zs_multi_tensor* ts, int32_t T, int es) {
+    std::vector<Range> r;
+    for (int32_t t = 0; t < T; ++t)
+        if (ts[t].numel > 0) r.push_back(range_of(ts[t].g, ts[t].numel, es));
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    size_t n = 0;
+    for (size_t i = 0; i < r.size(); ++i) {
+        if (n > 0 && r[i].lo <= r[n - 1].hi) r[n - 1].hi = std::max(r[n - 1].hi, r[i].hi);
+        else r[n++] = r[i];
+    }
+    r.resize(n);
+    return r;
+}
+
+// The checks that the moment conversions share.
 zs_status check_state8(const char* who, int64_t S, int32_t kind) {
     if (kind != ZS_STATE8_M && kind != ZS_STATE8_V)
         return fail(ZS_EUNSUPPORTED, "%s: unknown kind %d", who, kind);
@@ -152,8 +168,9 @@ ZS_EXPORT zs_status zs_multi_create(const zs_multi_tensor* tensors, int32_t T, i
         if (st != ZS_OK) return st;
         int64_t n = 0;
         for (int32_t t = 0; t < T; ++t) n += ceil_div(tensors[t].numel, ZS_MULTI_CHUNK);
-        zs_multi* m = new zs_multi{kMagic, state, dtype, T, n, {}};
+        zs_multi* m = new zs_multi{kMagic, state, dtype, T, n, {}, {}};
         try {
+            m->grads = grad_ranges(tensors, T, es);
             if (n > 0) {
                 const size_t head = size_t(T) * sizeof(zs_multi_tensor);
                 m->image.resize(head + size_t(n) * sizeof(MultiChunk));
@@ -294,17 +311,11 @@ ZS_EXPORT zs_status zs_grad_norm(const zs_multi* multi, const void* image, doubl
         for (int b = a + 1; b < 3; ++b)
             if (overlap(out[a], out[b]))
                 return fail(ZS_EALIAS, "%s: sumsq, norm_coef and workspace overlap", who);
-    if (multi->n_chunks > 0) {
-        const zs_multi_tensor* ts =
-            reinterpret_cast<const zs_multi_tensor*>(multi->image.data());
-        const int es = elem_size(multi->dtype);
-        for (int64_t t = 0; t < multi->T; ++t) {
-            const Range g = range_of(ts[t].g, ts[t].numel, es);
-            for (int a = 0; a < 3; ++a)
-                if (overlap(g, out[a]))
-                    return fail(ZS_EALIAS, "%s: an output or the workspace overlaps gradient %lld",
-                                who, (long long)t);
-        }
+    for (const Range& o : out) {
+        auto it = std::lower_bound(multi->grads.begin(), multi->grads.end(), o.hi,
+                                   [](const Range& g, uintptr_t hi) { return g.lo < hi; });
+        if (it != multi->grads.begin() && (it - 1)->hi > o.lo)
+            return fail(ZS_EALIAS, "%s: an output or the workspace overlaps a gradient", who);
     }
     return hip_status(launch_norm(image_of(*multi, image), multi->dtype, max_norm, sumsq, norm_coef,
                                   static_cast<NormWorkspace*>(workspace), stream),

@@ -339,6 +339,13 @@ def test_grad_norm_refuses(lib, no_gpu):
     for bad in (dict(nc=A + 16 * STEP), dict(sumsq=A + 18 * STEP + 32760),
                 dict(sumsq=A + 4 * STEP + 1992), dict(ws=A + 4 * STEP - 32768 + 16)):
         assert call(**bad) == zs.ZS_EALIAS, bad
+    # several gradients, one of them inside another, one joined to another, one apart
+    h = make(lib, [B.zs_multi_tensor(g=g, numel=n) for g, n in (
+        (A, 1000), (A + 400, 10), (A + 2000, 1000), (A + 64000, 8))], state=zs.ZS_STATE_NONE)
+    for at in (A, A + 1992, A + 2000, A + 3992, A + 64008):
+        assert call(multi=h, sumsq=at) == zs.ZS_EALIAS, at - A
+        assert call(multi=h, nc=at) == zs.ZS_EALIAS, at - A
+    assert call(multi=h, ws=A + 64000 - 16000) == zs.ZS_EALIAS
 
 
 def test_clip_coef_refuses(lib, no_gpu):

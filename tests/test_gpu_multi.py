@@ -516,6 +516,69 @@ def test_norm_clip_and_step_replayed_from_a_graph():
         e.check(f"eager {rep}")
 
 
+def test_tables_on_streams_of_their_own_at_once():
+    """Three tables' norm, clip factor and step enqueued together on three streams, each
+    with its own workspace, several times over; then the same from three host threads."""
+    import threading
+    dev = device()
+    sizes = [[60_000, 5], [4097] * 30, [123]]
+    cases = [Case(s, grads_of(s, "bf16", 40 + i, 0.05), zs.ZS_STATE_F32) for i, s in enumerate(sizes)]
+    outs = [(torch.zeros(1, dtype=torch.float64, device=dev), torch.zeros(2, device=dev),
+             torch.zeros(zs.ZS_NORM_WORKSPACE, dtype=torch.uint8, device=dev)) for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+
+    def enqueue(i, t):
+        s, nc, ws = outs[i]
+        zs.zs_grad_norm(cases[i].table, 0.5, s, nc, ws, stream=streams[i])
+        zs.zs_adamw_multi(cases[i].table, dict(step=t, **HP), grad_scale=nc[1:], stream=streams[i])
+
+    for t in (1, 2, 3):
+        for i in range(3):
+            enqueue(i, t)
+    threads = [threading.Thread(target=lambda i=i: [enqueue(i, t) for t in (4, 5)]) for i in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    for i, c in enumerate(cases):
+        check_norm(outs[i][0], outs[i][1], F.sumsq([widen(x) for x in c.g]), sum(c.sizes), 0.5)
+        for t in range(1, 6):
+            c.step_oracle(O.AdamWHP(step=t, **HP), to_np(outs[i][1])[1])
+        c.check(f"table {i}")
+
+
+def test_two_graphs_of_one_table_and_workspace_in_turn():
+    """Two captured norms that share a workspace, replayed one after the other with eager
+    calls between: each leaves the workspace as the next one needs it."""
+    dev = device()
+    g = [torch.randn(n, device=dev) for n in (70_000, 3)]
+    table = zs.MultiTable(grads=g)
+    ws = torch.zeros(zs.ZS_NORM_WORKSPACE, dtype=torch.uint8, device=dev)
+    outs = [(torch.zeros(1, dtype=torch.float64, device=dev), torch.zeros(2, device=dev))
+            for _ in range(2)]
+    zs.zs_grad_norm(table, 1.0, *outs[0], ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for o in outs:
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=side):
+            zs.zs_grad_norm(table, 1.0, *o, ws)
+        graphs.append(graph)
+    for rep in range(3):
+        for x in g:
+            x.mul_(1.5)
+        for graph in graphs:
+            graph.replay()
+        eager = norm_of(table, ws=ws)
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o[0], eager[0]) and torch.equal(o[1], eager[1])
+        check_norm(*eager, F.sumsq([to_np(x) for x in g]), 70_003, 1.0)
+
+
 def test_32bit_run_goes_on_in_8_bits_and_back():
     """A 32-bit run's moments encoded, stepped in 8 bits in one buffer laid out by
     zs_state8_layout, decoded and stepped in 32 bits again."""
