@@ -4,7 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <new>
+#include <memory>
 #include <vector>
 
 #include "zs_multi.h"
@@ -13,14 +13,12 @@
 
 using namespace zs;
 
-// A checked table: the descriptors, then the chunks, in one block of bytes.
+// A checked table, as the chunks that the kernels take.
 struct zs_multi {
     uint64_t magic;
     int32_t state;
     int32_t dtype;
-    int64_t T;
-    int64_t n_chunks;
-    std::vector<uint8_t> image;
+    std::vector<MultiChunk> chunks;
     std::vector<Range> grads;  // what the gradients cover: sorted, disjoint
 };
 
@@ -41,18 +39,40 @@ struct Owned {  // a range that the step writes, and whose it is
 zs_status check_multi(const char* who, const zs_multi* multi, const void* image) {
     if (multi == nullptr || multi->magic != kMagic)
         return fail(ZS_EINVAL, "%s: multi is NULL or not a live zs_multi", who);
-    if (multi->n_chunks > 0 && (image == nullptr || !aligned(image, 16)))
+    if (!multi->chunks.empty() && (image == nullptr || !aligned(image, 16)))
         return fail(ZS_EINVAL, "%s: image is NULL or not 16-byte aligned", who);
     return ZS_OK;
 }
 
 MultiImage image_of(const zs_multi& m, const void* image) {
-    MultiImage im;
-    im.table = static_cast<const zs_multi_tensor*>(image);
-    im.chunks = reinterpret_cast<const MultiChunk*>(static_cast<const uint8_t*>(image) +
-                                                    size_t(m.T) * sizeof(zs_multi_tensor));
-    im.n_chunks = m.n_chunks;
-    return im;
+    return MultiImage{static_cast<const MultiChunk*>(image), int64_t(m.chunks.size())};
+}
+
+// The chunks of one tensor, its arrays offset to each one's first element.
+void add_chunks(const zs_multi_tensor& x, int32_t t, int32_t state, int es,
+                std::vector<MultiChunk>* out) {
+    const int ms = state == ZS_STATE_F32 ? 4 : 1;
+    const auto at = [](const void* base, int64_t bytes) -> void* {
+        return base ? const_cast<char*>(static_cast<const char*>(base)) + bytes : nullptr;
+    };
+    for (int64_t i = 0; i < x.numel; i += ZS_MULTI_CHUNK) {
+        MultiChunk c{};
+        if (state != ZS_STATE_NONE) {
+            c.p = static_cast<float*>(at(x.p, i * 4));
+            c.m = at(x.m, i * ms);
+            c.v = at(x.v, i * ms);
+            c.w_out = static_cast<uint16_t*>(at(x.w_out, i * 2));
+        }
+        if (state == ZS_STATE_8BIT) {
+            c.m_scale = static_cast<uint8_t*>(at(x.m_scale, i / kBlock8));
+            c.v_scale = static_cast<uint8_t*>(at(x.v_scale, i / kBlock8));
+        }
+        c.g = at(x.g, i * es);
+        c.first = uint32_t(i);
+        c.tensor = t;
+        c.live = int32_t(std::min<int64_t>(x.numel - i, ZS_MULTI_CHUNK));
+        out->push_back(c);
+    }
 }
 
 zs_status check_max_norm(const char* who, double max_norm) {
@@ -66,8 +86,6 @@ zs_status check_tensors(const zs_multi_tensor* ts, int32_t T, int32_t state, int
         const zs_multi_tensor& x = ts[t];
         if (!size_ok(x.numel, 4))
             return fail(ZS_EINVAL, "%s: tensor %d has numel %lld", who, t, (long long)x.numel);
-        if (ceil_div(x.numel, ZS_MULTI_CHUNK) > INT32_MAX)
-            return fail(ZS_EUNSUPPORTED, "%s: tensor %d has too many chunks", who, t);
         if (x.numel == 0) continue;
         if (x.g == nullptr) return fail(ZS_EINVAL, "%s: tensor %d: g is NULL", who, t);
         if (!aligned(x.g, uintptr_t(es)))
@@ -168,24 +186,11 @@ ZS_EXPORT zs_status zs_multi_create(const zs_multi_tensor* tensors, int32_t T, i
         if (st != ZS_OK) return st;
         int64_t n = 0;
         for (int32_t t = 0; t < T; ++t) n += ceil_div(tensors[t].numel, ZS_MULTI_CHUNK);
-        zs_multi* m = new zs_multi{kMagic, state, dtype, T, n, {}, {}};
-        try {
-            m->grads = grad_ranges(tensors, T, es);
-            if (n > 0) {
-                const size_t head = size_t(T) * sizeof(zs_multi_tensor);
-                m->image.resize(head + size_t(n) * sizeof(MultiChunk));
-                std::memcpy(m->image.data(), tensors, head);
-                MultiChunk* c = reinterpret_cast<MultiChunk*>(m->image.data() + head);
-                for (int32_t t = 0; t < T; ++t) {
-                    const int64_t k = ceil_div(tensors[t].numel, ZS_MULTI_CHUNK);
-                    for (int64_t j = 0; j < k; ++j) *c++ = MultiChunk{t, int32_t(j)};
-                }
-            }
-        } catch (...) {
-            delete m;
-            throw;
-        }
-        *out = m;
+        std::unique_ptr<zs_multi> m(new zs_multi{kMagic, state, dtype, {}, {}});
+        m->grads = grad_ranges(tensors, T, es);
+        m->chunks.reserve(size_t(n));
+        for (int32_t t = 0; t < T; ++t) add_chunks(tensors[t], t, state, es, &m->chunks);
+        *out = m.release();
     } catch (const std::exception&) {
         return fail(ZS_EINVAL, "%s: out of host memory", who);
     }
@@ -196,8 +201,8 @@ ZS_EXPORT zs_status zs_multi_image(const zs_multi* multi, const void** image, in
     if (multi == nullptr || multi->magic != kMagic)
         return fail(ZS_EINVAL, "zs_multi_image: multi is NULL or not a live zs_multi");
     if (!image || !bytes) return fail(ZS_EINVAL, "zs_multi_image: an output pointer is NULL");
-    *image = multi->image.data();
-    *bytes = int64_t(multi->image.size());
+    *image = multi->chunks.data();
+    *bytes = int64_t(multi->chunks.size() * sizeof(MultiChunk));
     return ok();
 }
 
@@ -233,7 +238,7 @@ ZS_EXPORT zs_status zs_adamw_multi(const zs_multi* multi, const void* image, con
         a.seed_lo = uint32_t(round->seed);
         a.seed_hi = uint32_t(round->seed >> 32);
     }
-    if (multi->n_chunks == 0) return ok();
+    if (multi->chunks.empty()) return ok();
     a.k = adam_consts(*hp, 1);
     a.grad_scale = grad_scale;
     return hip_status(

@@ -7,15 +7,25 @@
 
 namespace zs {
 
-// Many tensors at once (zs_multi.cpp, zs_multi.hip): the device image of a table
-// is the T descriptors followed by the chunks.
+// Many tensors at once (zs_multi.cpp, zs_multi.hip): the device image of a table is an
+// array of chunks, each with everything that the workgroup that takes it has to know, so
+// that one scalar load stands before its data and every offset fits 32 bits.
 struct MultiChunk {
-    int32_t tensor;  // index into the table
-    int32_t index;   // chunk of that tensor: elements [index, index + 1) * ZS_MULTI_CHUNK
+    float* p;  // the tensor's arrays from the chunk's first element on
+    void* m;
+    void* v;
+    uint8_t* m_scale;
+    uint8_t* v_scale;
+    uint16_t* w_out;
+    const void* g;
+    uint32_t first;  // the chunk's first element in its tensor, modulo 2^32
+    int32_t tensor;  // the tensor's place in the table
+    int32_t live;    // elements, 1 .. ZS_MULTI_CHUNK
+    int32_t pad[3];
 };
+static_assert(sizeof(MultiChunk) == 80, "chunks are read by 16-byte aligned scalar loads");
 struct MultiImage {
-    const zs_multi_tensor* table;  // device
-    const MultiChunk* chunks;      // device
+    const MultiChunk* chunks;  // device
     int64_t n_chunks;
 };
 struct MultiArgs {

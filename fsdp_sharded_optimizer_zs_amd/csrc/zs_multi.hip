@@ -1,9 +1,9 @@
 // AdamW over many tensors in one launch (moments in fp32 or in 8-bit codes), the
 // conversions of the 8-bit moments, and the L2 norm of many gradients, for gfx950.
 //
-// All are streaming kernels bound by HBM. A workgroup takes one chunk of
-// ZS_MULTI_CHUNK elements of one tensor, found in a table in device memory, and
-// each of its 4 wavefronts 1024 elements of it, in 4 quarters of 256: lane l holds
+// All are streaming kernels bound by HBM. A workgroup takes one chunk of at most
+// ZS_MULTI_CHUNK elements of one tensor, described in device memory, and each of its 4
+// wavefronts 1024 elements of it, in 4 quarters of 256: lane l holds
 // elements 4l .. 4l+3 of each quarter, so that every fp32 access of a wavefront is
 // one run of 1 KiB. A quarter is one block of the 8-bit moments, whose scale is
 // therefore the same for the whole wavefront: it lives in a scalar register and the
@@ -47,20 +47,28 @@ template <typename G, typename P>
 __device__ __forceinline__ G* global(P* p) {
     return reinterpret_cast<G*>(reinterpret_cast<uintptr_t>(p));
 }
-
-// Elements of [i, n) that a lane's four hold: 0 .. 4.
-__device__ __forceinline__ int live_of(int64_t i, int64_t n) {
-    return i >= n ? 0 : (n - i >= 4 ? 4 : int(n - i));
+// Element q * kQuarter + i of an array whose base scalar registers hold: i is the lane's
+// own 32-bit offset and the quarter's goes into the instruction.
+template <typename G>
+__device__ __forceinline__ G* element(const void* base, int q, uint32_t i) {
+    return reinterpret_cast<G*>(reinterpret_cast<uintptr_t>(base) +
+                                uint32_t(q) * uint32_t(kQuarter * sizeof(G)) +
+                                i * uint32_t(sizeof(G)));
 }
 
-// Four consecutive elements from i, of which the first `live` exist (the others read as
+// Elements of [i, n) that a lane's four hold: 0 .. 4.
+__device__ __forceinline__ int live_of(int i, int n) {
+    return i >= n ? 0 : (n - i >= 4 ? 4 : n - i);
+}
+
+// A lane's four elements of quarter q, from its i on, of which the first `live` exist (the others read as
 // 0 and are not written). Lanes whose four all exist access them at once; with ALL every
 // lane does, and `live` is not looked at. Streams are touched once a step and go by
 // non-temporal accesses, except (CACHED) where a whole step stays in the memory-side
 // cache until the next one.
 template <bool ALL, bool CACHED = false>
-__device__ __forceinline__ void load_f32(const float* base, int64_t i, int live, float (&x)[4]) {
-    const g_f32* s = global<const g_f32>(base) + i;
+__device__ __forceinline__ void load_f32(const float* base, int q, uint32_t i, int live, float (&x)[4]) {
+    const g_f32* s = element<const g_f32>(base, q, i);
     if (ALL || live == 4) {
         const g_f32x4* v = reinterpret_cast<const g_f32x4*>(s);
         const f32x4 a = CACHED ? f32x4(*v) : f32x4(__builtin_nontemporal_load(v));
@@ -72,8 +80,8 @@ __device__ __forceinline__ void load_f32(const float* base, int64_t i, int live,
     }
 }
 template <bool ALL, bool CACHED = false>
-__device__ __forceinline__ void store_f32(float* base, int64_t i, int live, const float (&x)[4]) {
-    g_f32* d = global<g_f32>(base) + i;
+__device__ __forceinline__ void store_f32(float* base, int q, uint32_t i, int live, const float (&x)[4]) {
+    g_f32* d = element<g_f32>(base, q, i);
     if (ALL || live == 4) {
         g_f32x4* v = reinterpret_cast<g_f32x4*>(d);
         const f32x4 a{x[0], x[1], x[2], x[3]};
@@ -87,11 +95,11 @@ __device__ __forceinline__ void store_f32(float* base, int64_t i, int live, cons
 }
 // Gradients, widened.
 template <int DT, bool ALL, bool CACHED = false>
-__device__ __forceinline__ void load_grad(const void* base, int64_t i, int live, float (&x)[4]) {
+__device__ __forceinline__ void load_grad(const void* base, int q, uint32_t i, int live, float (&x)[4]) {
     if constexpr (DT == ZS_F32) {
-        load_f32<ALL, CACHED>(static_cast<const float*>(base), i, live, x);
+        load_f32<ALL, CACHED>(static_cast<const float*>(base), q, i, live, x);
     } else {
-        const g_u16* s = global<const g_u16>(base) + i;
+        const g_u16* s = element<const g_u16>(base, q, i);
         u32x2 h{0, 0};
         if (ALL || live == 4) {
             const g_u32x2* v = reinterpret_cast<const g_u32x2*>(s);
@@ -105,9 +113,9 @@ __device__ __forceinline__ void load_grad(const void* base, int64_t i, int live,
     }
 }
 template <bool ALL, bool CACHED = false>
-__device__ __forceinline__ void store_bf16(uint16_t* base, int64_t i, int live,
+__device__ __forceinline__ void store_bf16(uint16_t* base, int q, uint32_t i, int live,
                                            const float (&x)[4]) {
-    g_u16* d = global<g_u16>(base) + i;
+    g_u16* d = element<g_u16>(base, q, i);
     const u32x2 h{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
     if (ALL || live == 4) {
         g_u32x2* v = reinterpret_cast<g_u32x2*>(d);
@@ -120,8 +128,8 @@ __device__ __forceinline__ void store_bf16(uint16_t* base, int64_t i, int live,
     }
 }
 template <bool ALL>
-__device__ __forceinline__ uint32_t load_codes(const void* base, int64_t i, int live) {
-    const g_u8* s = global<const g_u8>(base) + i;
+__device__ __forceinline__ uint32_t load_codes(const void* base, int q, uint32_t i, int live) {
+    const g_u8* s = element<const g_u8>(base, q, i);
     uint32_t w = 0;
     if (ALL || live == 4) {
         w = __builtin_nontemporal_load(reinterpret_cast<const g_u32*>(s));
@@ -133,8 +141,8 @@ __device__ __forceinline__ uint32_t load_codes(const void* base, int64_t i, int 
     return w;
 }
 template <bool ALL>
-__device__ __forceinline__ void store_codes(void* base, int64_t i, int live, uint32_t w) {
-    g_u8* d = global<g_u8>(base) + i;
+__device__ __forceinline__ void store_codes(void* base, int q, uint32_t i, int live, uint32_t w) {
+    g_u8* d = element<g_u8>(base, q, i);
     if (ALL || live == 4) {
         __builtin_nontemporal_store(w, reinterpret_cast<g_u32*>(d));
     } else {
@@ -247,13 +255,12 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 
 // ------------------------------------------------------------- the step
 
-// fp32 moments: a wavefront's 1024 elements from base (lane's first i), those below n;
-// every load ahead of the arithmetic, and each quarter stored as soon as it is done.
+// fp32 moments: a wavefront's 1024 elements, those below n (i: the lane's first); every load ahead of the arithmetic, and each quarter stored as soon as it is done.
 // (202M parameters, bf16 gradients: 931 us, 6.1 TB/s, where a copy reaches 6.55; storing
 // stream by stream after all four quarters 993, loading two quarters at a time 951, one
 // at a time 954; fewer wavefronts a SIMD 944-965; temporal loads 1019.)
 template <int DT, bool ALL, bool CACHED>
-__device__ __forceinline__ void step32_wave(const zs_multi_tensor& t, int64_t i, int64_t n,
+__device__ __forceinline__ void step32_wave(const MultiChunk& t, int i, int n,
                                             const MultiArgs& a, float mult) {
     float* const tm = static_cast<float*>(t.m);
     float* const tv = static_cast<float*>(t.v);
@@ -261,22 +268,20 @@ __device__ __forceinline__ void step32_wave(const zs_multi_tensor& t, int64_t i,
     int live[kQ];
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-        const int64_t at = i + q * kQuarter;
-        live[q] = ALL ? 4 : live_of(at, n);
-        load_f32<ALL, CACHED>(t.p, at, live[q], p[q]);
-        load_f32<ALL, CACHED>(tm, at, live[q], m[q]);
-        load_f32<ALL, CACHED>(tv, at, live[q], v[q]);
-        load_grad<DT, ALL, CACHED>(t.g, at, live[q], g[q]);
+        live[q] = ALL ? 4 : live_of(q * kQuarter + i, n);
+        load_f32<ALL, CACHED>(t.p, q, i, live[q], p[q]);
+        load_f32<ALL, CACHED>(tm, q, i, live[q], m[q]);
+        load_f32<ALL, CACHED>(tv, q, i, live[q], v[q]);
+        load_grad<DT, ALL, CACHED>(t.g, q, i, live[q], g[q]);
     }
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-        const int64_t at = i + q * kQuarter;
 #pragma unroll
         for (int e = 0; e < 4; ++e) adamw1(p[q][e], m[q][e], v[q][e], g[q][e] * mult, a.k);
-        store_f32<ALL, CACHED>(t.p, at, live[q], p[q]);
-        store_f32<ALL, CACHED>(tm, at, live[q], m[q]);
-        store_f32<ALL, CACHED>(tv, at, live[q], v[q]);
-        if (t.w_out) store_bf16<ALL, CACHED>(t.w_out, at, live[q], p[q]);
+        store_f32<ALL, CACHED>(t.p, q, i, live[q], p[q]);
+        store_f32<ALL, CACHED>(tm, q, i, live[q], m[q]);
+        store_f32<ALL, CACHED>(tv, q, i, live[q], v[q]);
+        if (t.w_out) store_bf16<ALL, CACHED>(t.w_out, q, i, live[q], p[q]);
     }
 }
 
@@ -306,14 +311,14 @@ __device__ __forceinline__ uint32_t tensor_key(const MultiArgs& a, int32_t tenso
 // 8-bit moments, any case: one quarter, the first `live` elements of each lane, its
 // scale bytes sm and sv in and out.
 template <int DT, bool STOCH, bool EXACT>
-__device__ __forceinline__ void step8_quarter(const zs_multi_tensor& t, int64_t i, int live,
+__device__ __forceinline__ void step8_quarter(const MultiChunk& t, int q, int i, int live,
                                               const MultiArgs& a, float mult, uint32_t key,
                                               int* sm, int* sv) {
     float p[4], m[4], v[4], g[4];
-    load_f32<false>(t.p, i, live, p);
-    load_grad<DT, false>(t.g, i, live, g);
-    decode4<true>(load_codes<false>(t.m, i, live), *sm, m);
-    decode4<false>(load_codes<false>(t.v, i, live), *sv, v);
+    load_f32<false>(t.p, q, i, live, p);
+    load_grad<DT, false>(t.g, q, i, live, g);
+    decode4<true>(load_codes<false>(t.m, q, i, live), *sm, m);
+    decode4<false>(load_codes<false>(t.v, q, i, live), *sv, v);
     uint32_t rm[4] = {}, rv[4] = {};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -323,16 +328,16 @@ __device__ __forceinline__ void step8_quarter(const zs_multi_tensor& t, int64_t 
         p[e] = new_p<EXACT>(p[e], m[e], v[e], a);
         if (e >= live) m[e] = v[e] = 0.0f;  // no part of the block's largest
         if constexpr (STOCH) {
-            rm[e] = mix(uint32_t(i + e) ^ key);
+            rm[e] = mix((t.first + uint32_t(q * kQuarter + i + e)) ^ key);
             rv[e] = rm[e] >> 16;
         }
     }
     *sm = scale_of<true>(wave_max(top_bits(m)));
     *sv = scale_of<false>(wave_max(top_bits(v)));
-    store_codes<false>(t.m, i, live, encode4<true, STOCH>(m, *sm, rm));
-    store_codes<false>(t.v, i, live, encode4<false, STOCH>(v, *sv, rv));
-    store_f32<false>(t.p, i, live, p);
-    if (t.w_out) store_bf16<false>(t.w_out, i, live, p);
+    store_codes<false>(t.m, q, i, live, encode4<true, STOCH>(m, *sm, rm));
+    store_codes<false>(t.v, q, i, live, encode4<false, STOCH>(v, *sv, rv));
+    store_f32<false>(t.p, q, i, live, p);
+    if (t.w_out) store_bf16<false>(t.w_out, q, i, live, p);
 }
 
 // Codes as encode4 gives them, for a scale byte below 254: then the largest magnitude
@@ -375,16 +380,15 @@ struct Loaded8 {
     uint32_t wm[kQ], wv[kQ];
 };
 template <int DT, bool ALL>
-__device__ __forceinline__ void load8_wave(const zs_multi_tensor& t, int64_t i, int64_t n,
+__device__ __forceinline__ void load8_wave(const MultiChunk& t, int i, int n,
                                            Loaded8& d) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-        const int64_t at = i + q * kQuarter;
-        const int live = ALL ? 4 : live_of(at, n);
-        d.wm[q] = load_codes<ALL>(t.m, at, live);
-        d.wv[q] = load_codes<ALL>(t.v, at, live);
-        load_grad<DT, ALL>(t.g, at, live, d.g[q]);
-        load_f32<ALL>(t.p, at, live, d.p[q]);
+        const int live = ALL ? 4 : live_of(q * kQuarter + i, n);
+        d.wm[q] = load_codes<ALL>(t.m, q, i, live);
+        d.wv[q] = load_codes<ALL>(t.v, q, i, live);
+        load_grad<DT, ALL>(t.g, q, i, live, d.g[q]);
+        load_f32<ALL>(t.p, q, i, live, d.p[q]);
     }
     // keeps the loads here, in flight beside the scale bytes, ahead of the branch that
     // waits for those
@@ -397,16 +401,15 @@ __device__ __forceinline__ void load8_wave(const zs_multi_tensor& t, int64_t i, 
 // once. What does not exist was loaded as zeros; its m and v stay 0 (no part of the
 // block's largest).
 template <bool STOCH, bool ALL>
-__device__ __forceinline__ void step8_wave(const zs_multi_tensor& t, Loaded8& d, int64_t i,
-                                           int64_t n, int lane, const MultiArgs& a, float mult,
+__device__ __forceinline__ void step8_wave(const MultiChunk& t, Loaded8& d, int i,
+                                           int n, int lane, const MultiArgs& a, float mult,
                                            uint32_t key, int* lm, int* lv) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-        if (!ALL && i - 4 * lane + q * kQuarter >= n) break;
+        if (!ALL && q * kQuarter >= n) break;
         const float b1 = __builtin_ldexpf(a.k.b1, __builtin_amdgcn_readlane(*lm, q) - 15);
         const float b2 = __builtin_ldexpf(a.k.b2, __builtin_amdgcn_readlane(*lv, q) - 31);
-        const int64_t at = i + q * kQuarter;
-        const int live = ALL ? 4 : live_of(at, n);
+        const int live = ALL ? 4 : live_of(q * kQuarter + i, n);
         float m[4], v[4];
         uint32_t r[4] = {};
 #pragma unroll
@@ -419,7 +422,7 @@ __device__ __forceinline__ void step8_wave(const zs_multi_tensor& t, Loaded8& d,
             v[e] = (b2 * __uint_as_float(cv)) + (a.k.b2c * (x * x));
             d.p[q][e] = new_p<false>(d.p[q][e], m[e], v[e], a);
             if (!ALL && e >= live) m[e] = v[e] = 0.0f;  // 0 * mult may be NaN
-            if constexpr (STOCH) r[e] = mix(uint32_t(at + e) ^ key);
+            if constexpr (STOCH) r[e] = mix((t.first + uint32_t(q * kQuarter + i + e)) ^ key);
         }
         const int sm = scale_of<true>(wave_max(top_bits(m)));
         const int sv = scale_of<false>(wave_max(top_bits(v)));
@@ -436,60 +439,73 @@ __device__ __forceinline__ void step8_wave(const zs_multi_tensor& t, Loaded8& d,
             *lm = sm;
             *lv = sv;
         }
-        store_f32<ALL>(t.p, at, live, d.p[q]);
-        if (t.w_out) store_bf16<ALL>(t.w_out, at, live, d.p[q]);
-        store_codes<ALL>(t.m, at, live, wm);
-        store_codes<ALL>(t.v, at, live, wv);
+        store_f32<ALL>(t.p, q, i, live, d.p[q]);
+        if (t.w_out) store_bf16<ALL>(t.w_out, q, i, live, d.p[q]);
+        store_codes<ALL>(t.m, q, i, live, wm);
+        store_codes<ALL>(t.v, q, i, live, wv);
     }
 }
 
+template <int DT>
+__device__ __forceinline__ const void* grad_part(const void* g, int wave) {
+    return static_cast<const char*>(g) + wave * kWaveElems * (DT == ZS_BF16 ? 2 : 4);
+}
+
+// The part of a chunk that one of its 4 wavefronts takes: every array from the
+// wavefront's first element on, live the elements from there (none if not above 0).
+// Moments of MS bytes.
+template <int DT, int MS>
+__device__ __forceinline__ MultiChunk wave_part(const MultiChunk& c, int wave) {
+    MultiChunk t = c;
+    t.g = grad_part<DT>(t.g, wave);
+    const int base = wave * kWaveElems;
+    t.p += base;
+    t.m = static_cast<char*>(t.m) + base * MS;
+    t.v = static_cast<char*>(t.v) + base * MS;
+    t.m_scale += base / kQuarter;
+    t.v_scale += base / kQuarter;
+    if (t.w_out) t.w_out += base;
+    t.first += uint32_t(base);
+    t.live -= base;
+    return t;
+}
 template <int DT, bool CACHED>
 __global__ __launch_bounds__(kThreads) void multi32_kernel(
-    const zs_multi_tensor* __restrict__ table, const MultiChunk* __restrict__ chunks,
-    int64_t n_chunks, MultiArgs a) {
+    const MultiChunk* __restrict__ chunks, int64_t n_chunks, MultiArgs a) {
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const float mult = a.grad_scale ? *a.grad_scale : 1.0f;
     for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
-        const MultiChunk ch = chunks[c];
-        const zs_multi_tensor t = table[ch.tensor];
-        const int64_t n = t.numel;
-        const int64_t base = int64_t(ch.index) * ZS_MULTI_CHUNK + wave * kWaveElems;
-        if (base + kWaveElems <= n)
-            step32_wave<DT, true, CACHED>(t, base + 4 * lane, n, a, mult);
-        else if (base < n)
-            step32_wave<DT, false, CACHED>(t, base + 4 * lane, n, a, mult);
+        const MultiChunk t = wave_part<DT, 4>(chunks[c], wave);
+        if (t.live >= kWaveElems) step32_wave<DT, true, CACHED>(t, 4 * lane, t.live, a, mult);
+        else if (t.live > 0) step32_wave<DT, false, CACHED>(t, 4 * lane, t.live, a, mult);
     }
 }
 
 template <int DT, bool STOCH, bool EXACT>
 __global__ __launch_bounds__(kThreads) void multi8_kernel(
-    const zs_multi_tensor* __restrict__ table, const MultiChunk* __restrict__ chunks,
-    int64_t n_chunks, MultiArgs a) {
+    const MultiChunk* __restrict__ chunks, int64_t n_chunks, MultiArgs a) {
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const float mult = a.grad_scale ? *a.grad_scale : 1.0f;
     for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
-        const MultiChunk ch = chunks[c];
-        const zs_multi_tensor t = table[ch.tensor];
-        const int64_t n = t.numel;
-        const int64_t base = int64_t(ch.index) * ZS_MULTI_CHUNK + wave * kWaveElems;
-        if (base >= n) continue;
-        const uint32_t key = STOCH ? tensor_key(a, ch.tensor) : 0u;
+        const MultiChunk t = wave_part<DT, 1>(chunks[c], wave);
+        const int n = t.live, i = 4 * lane;
+        if (n <= 0) continue;
+        const uint32_t key = STOCH ? tensor_key(a, t.tensor) : 0u;
         // lane q < 4 holds the scale bytes of quarter q
-        g_u8* const ms = global<g_u8>(t.m_scale) + base / kQuarter + lane;
-        g_u8* const vs = global<g_u8>(t.v_scale) + base / kQuarter + lane;
-        const bool mine = lane < kQ && base + lane * kQuarter < n;
+        g_u8* const ms = element<g_u8>(t.m_scale, 0, lane);
+        g_u8* const vs = element<g_u8>(t.v_scale, 0, lane);
+        const bool mine = lane < kQ && lane * kQuarter < n;
         int lm = 0, lv = 0;
         if (mine) {
             lm = *ms;
             lv = *vs;
         }
-        const int64_t i = base + 4 * lane;
         bool done = false;
         if constexpr (!EXACT) {
             Loaded8 d;
-            if (base + kWaveElems <= n) {
+            if (n >= kWaveElems) {
                 load8_wave<DT, true>(t, i, n, d);
                 done = __all(lm <= kMostM && lv <= kMostV);
                 if (done) step8_wave<STOCH, true>(t, d, i, n, lane, a, mult, key, &lm, &lv);
@@ -501,11 +517,11 @@ __global__ __launch_bounds__(kThreads) void multi8_kernel(
         }
         if (!done) {
 #pragma unroll 1
-            for (int q = 0; q < kQ && base + q * kQuarter < n; ++q) {
-                const int64_t at = i + q * kQuarter;
+            for (int q = 0; q < kQ && q * kQuarter < n; ++q) {
                 int sm = __builtin_amdgcn_readlane(lm, q);
                 int sv = __builtin_amdgcn_readlane(lv, q);
-                step8_quarter<DT, STOCH, EXACT>(t, at, live_of(at, n), a, mult, key, &sm, &sv);
+                step8_quarter<DT, STOCH, EXACT>(t, q, i, live_of(q * kQuarter + i, n), a, mult, key,
+                                                &sm, &sv);
                 if (lane == q) {
                     lm = sm;
                     lv = sv;
@@ -532,27 +548,28 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const float* __restri
     const uint32_t none[4] = {};
     for (int64_t base = (int64_t(blockIdx.x) * kWaves + wave) * kWaveElems; base < S;
          base += int64_t(gridDim.x) * kWaves * kWaveElems) {
+        const int n = int(S - base < kWaveElems ? S - base : kWaveElems);
         float y[kQ][4];
 #pragma unroll
         for (int q = 0; q < kQ; ++q) {
-            const int64_t i = base + q * kQuarter + 4 * lane;
-            load_f32<false>(x, i, live_of(i, S), y[q]);
+            const int live = live_of(q * kQuarter + 4 * lane, n);
+            load_f32<false>(x + base, q, 4 * lane, live, y[q]);
         }
         int mine = 0;  // lane q: the scale byte of quarter q
 #pragma unroll
         for (int q = 0; q < kQ; ++q) {
-            const int64_t i = base + q * kQuarter + 4 * lane;
+            const int live = live_of(q * kQuarter + 4 * lane, n);
             if constexpr (!SIGNED) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (y[q][e] < 0.0f) y[q][e] = __uint_as_float(0x7fc00000u);
             }
             const int s = scale_of<SIGNED>(wave_max(top_bits(y[q])));
-            store_codes<false>(codes, i, live_of(i, S), encode4<SIGNED, false>(y[q], s, none));
+            store_codes<false>(codes + base, q, 4 * lane, live, encode4<SIGNED, false>(y[q], s, none));
             if (lane == q) mine = s;
         }
-        if (lane < kQ && base + lane * kQuarter < S)
-            global<g_u8>(scales)[base / kQuarter + lane] = uint8_t(mine);
+        if (lane * kQuarter < n && lane < kQ)
+            *element<g_u8>(scales + base / kQuarter, 0, lane) = uint8_t(mine);
     }
 }
 
@@ -564,24 +581,25 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const uint8_t* __rest
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     for (int64_t base = (int64_t(blockIdx.x) * kWaves + wave) * kWaveElems; base < S;
          base += int64_t(gridDim.x) * kWaves * kWaveElems) {
+        const int n = int(S - base < kWaveElems ? S - base : kWaveElems);
         int mine = 0;
-        if (lane < kQ && base + lane * kQuarter < S)
-            mine = global<const g_u8>(scales)[base / kQuarter + lane];
+        if (lane * kQuarter < n && lane < kQ)
+            mine = *element<const g_u8>(scales + base / kQuarter, 0, lane);
         uint32_t w[kQ];
 #pragma unroll
         for (int q = 0; q < kQ; ++q) {
-            const int64_t i = base + q * kQuarter + 4 * lane;
-            w[q] = load_codes<false>(codes, i, live_of(i, S));
+            const int live = live_of(q * kQuarter + 4 * lane, n);
+            w[q] = load_codes<false>(codes + base, q, 4 * lane, live);
         }
 #pragma unroll
         for (int q = 0; q < kQ; ++q) {
-            const int64_t i = base + q * kQuarter + 4 * lane;
+            const int live = live_of(q * kQuarter + 4 * lane, n);
             float x[4];
             decode4<SIGNED>(w[q], __builtin_amdgcn_readlane(mine, q), x);
             if constexpr (DT == ZS_F32)
-                store_f32<false>(static_cast<float*>(out), i, live_of(i, S), x);
+                store_f32<false>(static_cast<float*>(out) + base, q, 4 * lane, live, x);
             else
-                store_bf16<false>(static_cast<uint16_t*>(out), i, live_of(i, S), x);
+                store_bf16<false>(static_cast<uint16_t*>(out) + base, q, 4 * lane, live, x);
         }
     }
 }
@@ -652,8 +670,8 @@ __device__ __forceinline__ bool arrive(NormWorkspace* ws) {
 
 template <int DT>
 __global__ __launch_bounds__(kNormThreads) void norm_kernel(
-    const zs_multi_tensor* __restrict__ table, const MultiChunk* __restrict__ chunks,
-    int64_t n_chunks, double max_norm, NormWorkspace* ws, double* sumsq, float* norm_coef) {
+    const MultiChunk* __restrict__ chunks, int64_t n_chunks, double max_norm, NormWorkspace* ws,
+    double* sumsq, float* norm_coef) {
     __shared__ double slot[kNormWaves];
     __shared__ bool last;
     const int lane = int(threadIdx.x) & 63;
@@ -662,22 +680,16 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(
     // 4 wavefronts to a chunk
     for (int64_t c = int64_t(blockIdx.x) * kNormChunks + wave / kWaves; c < n_chunks;
          c += int64_t(gridDim.x) * kNormChunks) {
-        const MultiChunk ch = chunks[c];
-        const void* g = table[ch.tensor].g;
-        const int64_t n = table[ch.tensor].numel;
-        const int64_t base =
-            int64_t(ch.index) * ZS_MULTI_CHUNK + (wave % kWaves) * kWaveElems;
+        const void* g = grad_part<DT>(chunks[c].g, wave % kWaves);
+        const int n = chunks[c].live - (wave % kWaves) * kWaveElems;
         float x[kQ][4];
-        if (base + kWaveElems <= n) {
+        if (n >= kWaveElems) {
 #pragma unroll
-            for (int q = 0; q < kQ; ++q)
-                load_grad<DT, true>(g, base + q * kQuarter + 4 * lane, 4, x[q]);
+            for (int q = 0; q < kQ; ++q) load_grad<DT, true>(g, q, 4 * lane, 4, x[q]);
         } else {
 #pragma unroll
-            for (int q = 0; q < kQ; ++q) {
-                const int64_t i = base + q * kQuarter + 4 * lane;
-                load_grad<DT, false>(g, i, live_of(i, n), x[q]);
-            }
+            for (int q = 0; q < kQ; ++q)
+                load_grad<DT, false>(g, q, 4 * lane, live_of(q * kQuarter + 4 * lane, n), x[q]);
         }
 #pragma unroll
         for (int q = 0; q < kQ; ++q)
@@ -715,14 +727,14 @@ template <int DT, bool STOCH, bool EXACT>
 void launch8(const MultiImage& im, const MultiArgs& a, hipStream_t stream) {
     const unsigned grid = unsigned(grid_blocks(im.n_chunks, 1));
     hipLaunchKernelGGL((multi8_kernel<DT, STOCH, EXACT>), dim3(grid), dim3(kThreads), 0, stream,
-                       im.table, im.chunks, im.n_chunks, a);
+                       im.chunks, im.n_chunks, a);
 }
 
 template <int DT, bool CACHED>
 void launch32(const MultiImage& im, const MultiArgs& a, hipStream_t stream) {
     const unsigned grid = unsigned(grid_blocks(im.n_chunks, 1));
     hipLaunchKernelGGL((multi32_kernel<DT, CACHED>), dim3(grid), dim3(kThreads), 0, stream,
-                       im.table, im.chunks, im.n_chunks, a);
+                       im.chunks, im.n_chunks, a);
 }
 
 // Chunks of a step with fp32 moments that is taken to stay in the memory-side cache
@@ -792,10 +804,10 @@ hipError_t launch_norm(const MultiImage& im, int dtype, double max_norm, double*
                        float* norm_coef, NormWorkspace* ws, hipStream_t stream) {
     const dim3 grid(unsigned(norm_grid(im.n_chunks)));
     if (dtype == ZS_BF16)
-        hipLaunchKernelGGL((norm_kernel<ZS_BF16>), grid, dim3(kNormThreads), 0, stream, im.table,
+        hipLaunchKernelGGL((norm_kernel<ZS_BF16>), grid, dim3(kNormThreads), 0, stream,
                            im.chunks, im.n_chunks, max_norm, ws, sumsq, norm_coef);
     else
-        hipLaunchKernelGGL((norm_kernel<ZS_F32>), grid, dim3(kNormThreads), 0, stream, im.table,
+        hipLaunchKernelGGL((norm_kernel<ZS_F32>), grid, dim3(kNormThreads), 0, stream,
                            im.chunks, im.n_chunks, max_norm, ws, sumsq, norm_coef);
     return hipGetLastError();
 }

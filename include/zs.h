@@ -606,9 +606,9 @@ zs_status zs_hbm_probe(int32_t kind, void* buf, void* buf2, int64_t bytes,
  * Many tensors at once. A zs_multi is a host object that describes T tensors
  * (their gradients, and for the step their parameters and moments): it is
  * checked once, when it is made, and every later call reads the checked
- * description. Its image -- the tensors' pointers and a table of the chunks of
- * at most ZS_MULTI_CHUNK elements that workgroups take -- is copied by the
- * caller to device memory once and read there by the kernels.
+ * description. Its image -- 80 bytes for each chunk of at most ZS_MULTI_CHUNK
+ * elements of a tensor, one chunk a workgroup -- is copied by the caller to
+ * device memory once and read there by the kernels.
  */
 #define ZS_MULTI_CHUNK 4096
 
@@ -644,7 +644,7 @@ typedef struct zs_multi zs_multi;
  * Errors: ZS_EINVAL (NULLs, misalignment, sizes), ZS_EALIAS (a written array
  * -- p, m, v, their scales, w_out -- overlaps another written array or a
  * gradient, of the same tensor or another: so a tensor listed twice),
- * ZS_EUNSUPPORTED (state, dtype, more than 2^31 - 1 chunks of one tensor).
+ * ZS_EUNSUPPORTED (state, dtype).
  */
 zs_status zs_multi_create(const zs_multi_tensor* tensors, int32_t T, int32_t state,
                           int32_t dtype, zs_multi** out);

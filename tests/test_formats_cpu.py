@@ -234,16 +234,30 @@ def make(lib, *args, **kw):
     return h
 
 
-def test_image_holds_the_table_and_its_chunks(lib, no_gpu):
+@pytest.mark.parametrize("state", (zs.ZS_STATE_NONE, zs.ZS_STATE_F32, zs.ZS_STATE_8BIT))
+def test_image_holds_every_chunk(lib, no_gpu, state):
+    """Each chunk's pointers, first element, tensor and length, tensors in order."""
     sizes = [0, 1, 4096, 4097, 0, 10000]
-    es = [entry(i, n) if n else B.zs_multi_tensor() for i, n in enumerate(sizes)]
-    h = make(lib, es)
+    es = [entry(i, n, state) if n else B.zs_multi_tensor() for i, n in enumerate(sizes)]
+    es[3].w_out = None
+    h = make(lib, es, state=state)
     img, nbytes = ctypes.c_void_p(), ctypes.c_int64()
     assert lib.zs_multi_image(h, ctypes.byref(img), ctypes.byref(nbytes)) == zs.ZS_OK
     raw = ctypes.string_at(img.value, nbytes.value)
-    assert raw[:64 * len(es)] == b"".join(bytes(e) for e in es)
-    chunks = np.frombuffer(raw[64 * len(es):], np.int32).reshape(-1, 2).tolist()
-    assert chunks == [[t, j] for t, n in enumerate(sizes) for j in range(-(-n // 4096))]
+    got = [(*np.frombuffer(c[:56], np.uint64).tolist(), *np.frombuffer(c[56:68], np.uint32).tolist())
+           for c in (raw[k:k + 80] for k in range(0, len(raw), 80))]
+    want = []
+    for t, n in enumerate(sizes):
+        for i in range(0, n, 4096):
+            e, ms = es[t], 4 if state == zs.ZS_STATE_F32 else 1
+            arrays = [0] * 6
+            if state != zs.ZS_STATE_NONE:
+                arrays = [e.p + 4 * i, e.m + ms * i, e.v + ms * i, 0, 0,
+                          e.w_out + 2 * i if e.w_out else 0]
+            if state == zs.ZS_STATE_8BIT:
+                arrays[3:5] = [e.m_scale + i // 256, e.v_scale + i // 256]
+            want.append((*arrays, e.g + 2 * i, i, t, min(4096, n - i)))
+    assert got == want
     assert lib.zs_multi_destroy(h) == zs.ZS_OK
     assert lib.zs_multi_destroy(None) == zs.ZS_OK
 
@@ -254,7 +268,6 @@ def test_image_holds_the_table_and_its_chunks(lib, no_gpu):
     (dict(p=A + 2), zs.ZS_EINVAL), (dict(g=A + STEP * 4 + 1), zs.ZS_EINVAL),
     (dict(w_out=A + 3 * STEP + 1), zs.ZS_EINVAL), (dict(numel=-1), zs.ZS_EINVAL),
     (dict(numel=1 << 61), zs.ZS_EINVAL),
-    (dict(numel=(1 << 43) + 1), zs.ZS_EUNSUPPORTED),               # chunks of one tensor
     (dict(m=A + 4 * 999), zs.ZS_EALIAS),                           # last byte of p
     (dict(v=A + STEP + 999), zs.ZS_EALIAS), (dict(w_out=A + 4 * 998), zs.ZS_EALIAS),
     (dict(m_scale=A + 2 * STEP + 5), zs.ZS_EALIAS), (dict(v_scale=A + 5 * STEP + 3), zs.ZS_EALIAS),
