@@ -262,6 +262,26 @@ def test_image_holds_every_chunk(lib, no_gpu, state):
     assert lib.zs_multi_destroy(None) == zs.ZS_OK
 
 
+@pytest.mark.parametrize("off", (0, 1, 31, 32, 63, 64, 65))
+@pytest.mark.parametrize("n", (1, 63, 4032, 4033, 4095, 4096, 4097, 20_000))
+def test_fp32_chunks_cover_a_tensor_and_start_on_lines(lib, no_gpu, n, off):
+    """The chunks follow one another over the tensor, none over 4096 elements, and all
+    but the first start where p is 256-byte aligned."""
+    h = make(lib, [entry(0, n, zs.ZS_STATE_F32, p=A + 4 * off)], state=zs.ZS_STATE_F32)
+    img, nbytes = ctypes.c_void_p(), ctypes.c_int64()
+    lib.zs_multi_image(h, ctypes.byref(img), ctypes.byref(nbytes))
+    raw = ctypes.string_at(img.value, nbytes.value)
+    at = 0
+    for k in range(0, len(raw), 80):
+        p, m = np.frombuffer(raw[k:k + 16], np.uint64).tolist()
+        first, _, live = np.frombuffer(raw[k + 56:k + 68], np.uint32).tolist()
+        assert first == at and 1 <= live <= 4096
+        assert p == A + 4 * off + 4 * at and m == A + STEP + 4 * at
+        assert k == 0 or p % 256 == 0
+        at += live
+    assert at == n
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(p=0), zs.ZS_EINVAL), (dict(m=0), zs.ZS_EINVAL), (dict(v=0), zs.ZS_EINVAL),
     (dict(g=0), zs.ZS_EINVAL), (dict(m_scale=0), zs.ZS_EINVAL), (dict(v_scale=0), zs.ZS_EINVAL),
