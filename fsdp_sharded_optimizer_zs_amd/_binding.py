@@ -712,7 +712,9 @@ class MultiTable:
     each per gradient and contiguous. Moments are float32, or uint8 codes with
     m_scale and v_scale (uint8, ceil(numel / 256) each: zs_state8_layout). It
     holds the tensors, whose addresses it has given to the device: new tensors
-    (gradients that were reallocated, too) need a new table."""
+    (gradients that were reallocated, too) need a new table (2 ms for 1,000
+    tensors). Keep it while work enqueued with it, or a captured graph, may run;
+    make it outside of a capture."""
 
     def __init__(self, p: Sequence = None, m: Sequence = None, v: Sequence = None,
                  grads: Sequence = (), w: Sequence = None, m_scale: Sequence = None,
@@ -737,30 +739,33 @@ class MultiTable:
             raise ValueError("8-bit moments need both m_scale and v_scale")
         else:
             self.state = ZS_STATE_8BIT if "m_scale" in lists else ZS_STATE_F32
-        moment = torch.float32 if self.state == ZS_STATE_F32 else torch.uint8
         code = _dtype_code(grads[0]) if grads else ZS_F32
-        for i, g in enumerate(grads):
-            _dev(g, f"grads[{i}]")
-            if _dtype_code(g) != code:
-                raise TypeError("gradients must share one dtype")
-            for k, x in lists.items():
-                if k == "w_out":
-                    _dev(x[i], f"w[{i}]")
-                    if _dtype_code(x[i]) != ZS_BF16 or x[i].numel() != numels[i]:
-                        raise ValueError(f"w[{i}] must be bf16 bits with {numels[i]} elements")
-                elif k in ("m_scale", "v_scale"):
-                    _typed(x[i], f"{k}[{i}]", torch.uint8, -(-numels[i] // 256))
-                else:
-                    _typed(x[i], f"{k}[{i}]", torch.float32 if k == "p" else moment, numels[i])
-        every = grads + [t for x in lists.values() for t in x]
-        _same_device(every, "MultiTable")
+        moment = torch.float32 if self.state == ZS_STATE_F32 else torch.uint8
+        bf16 = (torch.bfloat16, torch.int16, getattr(torch, "uint16", torch.int16))
+        kinds = dict(p=(torch.float32,), m=(moment,), v=(moment,), m_scale=(torch.uint8,),
+                     v_scale=(torch.uint8,), w_out=bf16,
+                     g=bf16 if code == ZS_BF16 else (torch.float32,))
+        lists["g"] = grads
+        scales = [-(-n // 256) for n in numels] if self.state == ZS_STATE_8BIT else None
+        every = [t for x in lists.values() for t in x]
+        for k, x in lists.items():
+            want = scales if k in ("m_scale", "v_scale") else numels
+            # one pass per property, then the failing tensor for the message
+            if not ([t.numel() for t in x] == want and {t.dtype for t in x} <= set(kinds[k])
+                    and all([t.is_contiguous() for t in x]) and all([t.is_cuda for t in x])):
+                for i, t in enumerate(x):
+                    _dev(t, f"{k}[{i}]")
+                    if t.dtype not in kinds[k] or t.numel() != want[i]:
+                        raise ValueError(f"{k}[{i}] must be {kinds[k][0]} with {want[i]} elements")
+        if len({t.device for t in every}) > 1:
+            raise ValueError("MultiTable: every tensor must be on one device")
         self.tensors = every
         # rows are zs_multi_tensor: 7 pointers and numel, 8 bytes each
         rows = np.zeros((max(1, T), 8), dtype=np.int64)
         for j, k in enumerate(("p", "m", "v", "m_scale", "v_scale", "w_out", "g")):
-            x = grads if k == "g" else lists.get(k)
-            if x and T:
-                rows[:T, j] = np.array([t.data_ptr() for t in x], dtype=np.uint64).view(np.int64)
+            if T and k in lists:
+                rows[:T, j] = np.array([t.data_ptr() for t in lists[k]],
+                                       dtype=np.uint64).view(np.int64)
         rows[:T, 7] = numels
         multi = ctypes.c_void_p()
         lib = load()

@@ -256,9 +256,10 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 // ------------------------------------------------------------- the step
 
 // fp32 moments: a wavefront's 1024 elements, those below n (i: the lane's first); every load ahead of the arithmetic, and each quarter stored as soon as it is done.
-// (202M parameters, bf16 gradients: 931 us, 6.1 TB/s, where a copy reaches 6.55; storing
-// stream by stream after all four quarters 993, loading two quarters at a time 951, one
-// at a time 954; fewer wavefronts a SIMD 944-965; temporal loads 1019.)
+// Bound by HBM: 202M parameters with bf16 gradients 940 us, 6.0 TB/s, where a copy reaches
+// 6.57. In one process, at 931: storing stream by stream after all four quarters 993,
+// loading two quarters at a time 951, one at a time 954, fewer wavefronts a SIMD 944-965,
+// temporal loads 1019; at 945: six or eight wavefronts a SIMD 959 and 1029.
 template <int DT, bool ALL, bool CACHED>
 __device__ __forceinline__ void step32_wave(const MultiChunk& t, int i, int n,
                                             const MultiArgs& a, float mult) {
@@ -400,6 +401,11 @@ __device__ __forceinline__ void load8_wave(const MultiChunk& t, int i, int n,
 // is taken as (B1 * 2^(s - 15)) * float_of_bits(c << 20), the same real product, rounded
 // once. What does not exist was loaded as zeros; its m and v stay 0 (no part of the
 // block's largest).
+//
+// About 60 VALU instructions an element (stochastic; some of quarter rate), which HBM's time
+// of about 100 hides: 202M parameters with bf16 gradients 528 us, 6.1 TB/s. The fp32 step's
+// roots and divisions bound it by arithmetic instead (about 750); each quarter loaded on its
+// own and general decoding and encoding for every block were the rest of that.
 template <bool STOCH, bool ALL>
 __device__ __forceinline__ void step8_wave(const MultiChunk& t, Loaded8& d, int i,
                                            int n, int lane, const MultiArgs& a, float mult,
@@ -537,8 +543,8 @@ __global__ __launch_bounds__(kThreads) void multi8_kernel(
 
 // ------------------------------------------------------------- conversions
 
-// kQ blocks of 256 elements per wavefront, all loads first. (One block a wavefront ran
-// the decode at half the rate.)
+// kQ blocks of 256 elements per wavefront, all loads first: 202M codes to bf16 in 97 us,
+// 6.3 TB/s (one block a wavefront: 200).
 template <bool SIGNED>
 __global__ __launch_bounds__(kThreads) void encode8_kernel(const float* __restrict__ x, int64_t S,
                                                            uint8_t* __restrict__ codes,
