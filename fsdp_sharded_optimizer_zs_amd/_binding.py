@@ -780,6 +780,8 @@ class MultiTable:
             view = (ctypes.c_uint8 * nbytes.value).from_address(host.value)
             # a synchronous copy: the image is whole for every stream when this returns
             self.image = torch.from_numpy(np.frombuffer(view, dtype=np.uint8).copy()).to(device)
+            self._dev = self.image.get_device()
+            self._home = torch._C._cuda_getCurrentRawStream(self._dev)
         self._ref = every[0] if every else None
 
     def __del__(self):
@@ -789,10 +791,14 @@ class MultiTable:
 
     def _image(self, stream):
         """Address of the device image, which stays allocated until the work on
-        `stream` is done."""
+        a stream other than the one it was made on is done."""
         if self.image is None:
             return None
-        if stream is not None and isinstance(stream, _torch().cuda.Stream):
+        torch = _torch()
+        if stream is None:
+            if torch._C._cuda_getCurrentRawStream(self._dev) != self._home:
+                self.image.record_stream(torch.cuda.current_stream(self._dev))
+        elif isinstance(stream, torch.cuda.Stream) and stream.cuda_stream != self._home:
             self.image.record_stream(stream)
         return self.image.data_ptr()
 
@@ -914,12 +920,18 @@ def zs_gather_unit_mx4(codes: Sequence, scales: Sequence, flat_out, stream=None)
     if D < 1 or len(scales) != D or flat_out.numel() % D:
         raise ValueError("need D codes, D scales and a flat_out of D * S elements")
     S = flat_out.numel() // D
-    for c, s in zip(codes, scales):
-        _typed(c, "every shard's codes", uint8, -(-S // 2))
-        _typed(s, "every shard's scales", uint8, -(-S // 32))
-    _same_device(codes + scales + [flat_out], "zs_gather_unit_mx4")
-    _enqueue(load().zs_gather_unit_mx4, flat_out, stream, _ptr_array(codes), _ptr_array(scales), D,
-             S, code, flat_out.data_ptr())
+    arrays = []
+    for what, ts, n in (("codes", codes, -(-S // 2)), ("scales", scales, -(-S // 32))):
+        # one pass over all of them, then the failing one for the message
+        if not all([t.is_cuda and t.dtype == uint8 and t.numel() == n and t.is_contiguous()
+                    for t in ts]):
+            for r, t in enumerate(ts):
+                _typed(t, f"{what}[{r}]", uint8, n)
+        _same_device(ts, "zs_gather_unit_mx4")
+        arrays.append((ctypes.c_void_p * D)(*[t.data_ptr() for t in ts]))
+    _same_device((flat_out, codes[0], scales[0]), "zs_gather_unit_mx4")
+    _enqueue(load().zs_gather_unit_mx4, flat_out, stream, *arrays, D, S, code,
+             flat_out.data_ptr())
 
 
 ZS_PROBE_READ, ZS_PROBE_WRITE, ZS_PROBE_COPY, ZS_PROBE_TRIAD = 0, 1, 2, 3

@@ -1,5 +1,6 @@
 // Entry points over many tensors (zs_multi_*, zs_adamw_multi, zs_grad_norm), of the
-// 8-bit moments and of the 4-bit shards: host-side checks, then one launch. Nothing here allocates device memory or synchronizes.
+// 8-bit moments and of the 4-bit shards: host-side checks, then one launch. Nothing here
+// allocates device memory or synchronizes.
 
 #include <algorithm>
 #include <cmath>

@@ -3,11 +3,11 @@
 //
 // All are streaming kernels bound by HBM. A workgroup takes one chunk of at most
 // ZS_MULTI_CHUNK elements of one tensor, described in device memory, and each of its 4
-// wavefronts 1024 elements of it, in 4 quarters of 256: lane l holds
-// elements 4l .. 4l+3 of each quarter, so that every fp32 access of a wavefront is
-// one run of 1 KiB. A quarter is one block of the 8-bit moments, whose scale is
-// therefore the same for the whole wavefront: it lives in a scalar register and the
-// block's largest magnitude is one reduction over the wavefront.
+// wavefronts 1024 elements of it, in 4 quarters of 256: lane l holds elements 4l .. 4l+3
+// of each quarter, so that every fp32 access of a wavefront is one run of 1 KiB. A quarter
+// is one block of the 8-bit moments, whose scale is therefore the same for the whole
+// wavefront: it lives in a scalar register and the block's largest magnitude is one
+// reduction over the wavefront.
 
 #include "zs_multi.h"
 #include "zs_math.h"
@@ -30,10 +30,8 @@ static_assert(kWaves * kWaveElems == ZS_MULTI_CHUNK, "a workgroup covers one chu
 // Pointers read from the table are global memory, never LDS or private memory.
 #define ZS_GLOBAL __attribute__((address_space(1)))
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32_u __attribute__((aligned(1)));
 typedef ZS_GLOBAL f32x4_u g_f32x4;
@@ -61,13 +59,14 @@ __device__ __forceinline__ int live_of(int i, int n) {
     return i >= n ? 0 : (n - i >= 4 ? 4 : n - i);
 }
 
-// A lane's four elements of quarter q, from its i on, of which the first `live` exist (the others read as
-// 0 and are not written). Lanes whose four all exist access them at once; with ALL every
-// lane does, and `live` is not looked at. Streams are touched once a step and go by
-// non-temporal accesses, except (CACHED) where a whole step stays in the memory-side
-// cache until the next one.
+// A lane's four elements of quarter q, from its i on, of which the first `live` exist (the
+// others read as 0 and are not written). Lanes whose four all exist access them at once;
+// with ALL every lane does, and `live` is not looked at. Streams are touched once a step
+// and go by non-temporal accesses, except (CACHED) where a whole step stays in the
+// memory-side cache until the next one.
 template <bool ALL, bool CACHED = false>
-__device__ __forceinline__ void load_f32(const float* base, int q, uint32_t i, int live, float (&x)[4]) {
+__device__ __forceinline__ void load_f32(const float* base, int q, uint32_t i, int live,
+                                         float (&x)[4]) {
     const g_f32* s = element<const g_f32>(base, q, i);
     if (ALL || live == 4) {
         const g_f32x4* v = reinterpret_cast<const g_f32x4*>(s);
@@ -80,7 +79,8 @@ __device__ __forceinline__ void load_f32(const float* base, int q, uint32_t i, i
     }
 }
 template <bool ALL, bool CACHED = false>
-__device__ __forceinline__ void store_f32(float* base, int q, uint32_t i, int live, const float (&x)[4]) {
+__device__ __forceinline__ void store_f32(float* base, int q, uint32_t i, int live,
+                                          const float (&x)[4]) {
     g_f32* d = element<g_f32>(base, q, i);
     if (ALL || live == 4) {
         g_f32x4* v = reinterpret_cast<g_f32x4*>(d);
@@ -95,7 +95,8 @@ __device__ __forceinline__ void store_f32(float* base, int q, uint32_t i, int li
 }
 // Gradients, widened.
 template <int DT, bool ALL, bool CACHED = false>
-__device__ __forceinline__ void load_grad(const void* base, int q, uint32_t i, int live, float (&x)[4]) {
+__device__ __forceinline__ void load_grad(const void* base, int q, uint32_t i, int live,
+                                          float (&x)[4]) {
     if constexpr (DT == ZS_F32) {
         load_f32<ALL, CACHED>(static_cast<const float*>(base), q, i, live, x);
     } else {
@@ -255,7 +256,8 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 
 // ------------------------------------------------------------- the step
 
-// fp32 moments: a wavefront's 1024 elements, those below n (i: the lane's first); every load ahead of the arithmetic, and each quarter stored as soon as it is done.
+// fp32 moments: a wavefront's 1024 elements, those below n (i: the lane's first); every
+// load ahead of the arithmetic, and each quarter stored as soon as it is done.
 // Bound by HBM: 202M parameters with bf16 gradients 940 us, 6.0 TB/s, where a copy reaches
 // 6.57. In one process, at 931: storing stream by stream after all four quarters 993,
 // loading two quarters at a time 951, one at a time 954, fewer wavefronts a SIMD 944-965,
@@ -381,8 +383,7 @@ struct Loaded8 {
     uint32_t wm[kQ], wv[kQ];
 };
 template <int DT, bool ALL>
-__device__ __forceinline__ void load8_wave(const MultiChunk& t, int i, int n,
-                                           Loaded8& d) {
+__device__ __forceinline__ void load8_wave(const MultiChunk& t, int i, int n, Loaded8& d) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
         const int live = ALL ? 4 : live_of(q * kQuarter + i, n);
@@ -407,9 +408,9 @@ __device__ __forceinline__ void load8_wave(const MultiChunk& t, int i, int n,
 // roots and divisions bound it by arithmetic instead (about 750); each quarter loaded on its
 // own and general decoding and encoding for every block were the rest of that.
 template <bool STOCH, bool ALL>
-__device__ __forceinline__ void step8_wave(const MultiChunk& t, Loaded8& d, int i,
-                                           int n, int lane, const MultiArgs& a, float mult,
-                                           uint32_t key, int* lm, int* lv) {
+__device__ __forceinline__ void step8_wave(const MultiChunk& t, Loaded8& d, int i, int n, int lane,
+                                           const MultiArgs& a, float mult, uint32_t key, int* lm,
+                                           int* lv) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
         if (!ALL && q * kQuarter >= n) break;
@@ -475,6 +476,7 @@ __device__ __forceinline__ MultiChunk wave_part(const MultiChunk& c, int wave) {
     t.live -= base;
     return t;
 }
+
 template <int DT, bool CACHED>
 __global__ __launch_bounds__(kThreads) void multi32_kernel(
     const MultiChunk* __restrict__ chunks, int64_t n_chunks, MultiArgs a) {
@@ -571,7 +573,8 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const float* __restri
                     if (y[q][e] < 0.0f) y[q][e] = __uint_as_float(0x7fc00000u);
             }
             const int s = scale_of<SIGNED>(wave_max(top_bits(y[q])));
-            store_codes<false>(codes + base, q, 4 * lane, live, encode4<SIGNED, false>(y[q], s, none));
+            store_codes<false>(codes + base, q, 4 * lane, live,
+                               encode4<SIGNED, false>(y[q], s, none));
             if (lane == q) mine = s;
         }
         if (lane * kQuarter < n && lane < kQ)
@@ -641,19 +644,6 @@ __device__ __forceinline__ void write_clip(double sum, double max_norm, float* n
     norm_coef[1] = c;
 }
 
-// Sum of squares, in fp64, where the product of two fp32 numbers is exact and no square
-// over- or underflows. Workgroup b takes kNormChunks chunks at a time; the one that
-// arrives last adds all partial sums, in their order, and leaves the count at 0 for the
-// next call. Nothing waits: which workgroup is last changes no result.
-//
-// A partial sum is one agent-scope atomic store, written through to memory that all XCDs
-// share, and it has arrived there once the wait for it is over; the count goes up after
-// that wait, so that whoever sees the whole count sees every sum.
-//
-// 3.3M bf16 gradients 6.6 us a call (a second launch for the final sum: 12.4); 108M fp32
-// ones in 2,000 tensors 133 us, 6.5 TB/s. One count for all workgroups 137; 2048 smaller
-// workgroups 140 and, on the 3.3M, 13.8; a release with the count, which writes back and
-// invalidates an XCD's whole L2 for every workgroup, 227 and 20.
 // Counts this workgroup in; true for the last one of the grid. Workgroups count in
 // groups (b mod kNormGroups), the last of each group for the group, so that the counts on
 // one address are few; each count is put back to 0 by the last that adds to it.
@@ -674,6 +664,19 @@ __device__ __forceinline__ bool arrive(NormWorkspace* ws) {
     return true;
 }
 
+// Sum of squares, in fp64, where the product of two fp32 numbers is exact and no square
+// over- or underflows. Workgroup b takes kNormChunks chunks at a time; the one that
+// arrives last adds all partial sums, in their order, and leaves the count at 0 for the
+// next call. Nothing waits: which workgroup is last changes no result.
+//
+// A partial sum is one agent-scope atomic store, written through to memory that all XCDs
+// share, and it has arrived there once the wait for it is over; the count goes up after
+// that wait, so that whoever sees the whole count sees every sum.
+//
+// Bound by HBM: 108M fp32 gradients in 2,000 tensors 131 us, 6.6 TB/s; 3.3M bf16 ones 6.0 us
+// a call (a second launch for the final sum: 12.4). One count for all workgroups 137; 2048
+// smaller workgroups 140 and, on the 3.3M, 13.8; a release with the count, which writes back
+// and invalidates an XCD's whole L2 for every workgroup, 227 and 20.
 template <int DT>
 __global__ __launch_bounds__(kNormThreads) void norm_kernel(
     const MultiChunk* __restrict__ chunks, int64_t n_chunks, double max_norm, NormWorkspace* ws,
