@@ -95,27 +95,28 @@ def _mix(x):
     return x ^ (x >> np.uint64(16))
 
 
-def random_words(seed: int, tensor: int, n: int) -> np.ndarray:
-    """The 32 random bits of each of a tensor's n elements."""
+def random_words(seed: int, tensor: int, n: int, first: int = 0) -> np.ndarray:
+    """The 32 random bits of each of a tensor's n elements from `first` on."""
     u = np.uint64
     lo, hi = u(seed & 0xFFFFFFFF), u(seed >> 32)
     key = _mix(u((int(lo) + 0x9E3779B9 * (tensor + 1)) & 0xFFFFFFFF))
     key = _mix((key + hi) & u(0xFFFFFFFF))
-    return _mix((np.arange(n, dtype=np.uint64) & u(0xFFFFFFFF)) ^ key)
+    return _mix((np.arange(first, first + n, dtype=np.uint64) & u(0xFFFFFFFF)) ^ key)
 
 
-def rounding_places(seed: int, tensor: int, n: int):
+def rounding_places(seed: int, tensor: int, n: int, first: int = 0):
     """rnd of state8_encode for m and for v."""
-    r = random_words(seed, tensor, n)
+    r = random_words(seed, tensor, n, first)
     return (((r % 65536) * 16 + 8) / 2.0**20, ((r // 65536) * 16 + 8) / 2.0**20)
 
 
-def adamw_step8(p, mc, ms, vc, vs, g, hp: O.AdamWHP, seed=None, tensor: int = 0):
+def adamw_step8(p, mc, ms, vc, vs, g, hp: O.AdamWHP, seed=None, tensor: int = 0, first: int = 0):
     """One AdamW step with 8-bit moments: the values of the codes, zs_oracle's fp32
-    step, and the new moments encoded. Returns (p, mc, ms, vc, vs, w)."""
+    step, and the new moments encoded. Returns (p, mc, ms, vc, vs, w). `first`: the place
+    in the tensor of the first element, a multiple of 256."""
     with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
         p2, m1, v1, w = O.adamw_step(p, state8_values(mc, ms, M), state8_values(vc, vs, V), g, hp)
-    rm, rv = (None, None) if seed is None else rounding_places(seed, tensor, len(m1))
+    rm, rv = (None, None) if seed is None else rounding_places(seed, tensor, len(m1), first)
     return (p2, *state8_encode(m1, M, rm), *state8_encode(v1, V, rv), w)
 
 

@@ -284,6 +284,49 @@ def test_adamw_multi_large_and_many():
         assert torch.equal(a, b)
 
 
+def test_adamw_multi_8bit_past_32_bits():
+    """A tensor of 2^32 + 5,000 elements (17 GB of p, 4 GB of each moment's codes):
+    windows at its start, around element 2^31 and 2^32 and at its end against the oracle;
+    p to the last bit (eps = 0 takes the exact operations), codes stochastic. The norm of
+    its gradients, a repeated block of 2^20, against that block's."""
+    dev = device()
+    n = (1 << 32) + 5000
+    block = W.as_bf16_bits(W.normal_f32(1 << 20, 1e-3, 77, dev))
+    g = torch.empty(n, dtype=torch.int16, device=dev)
+    whole = n >> 20
+    g[:whole << 20].view(whole, 1 << 20).copy_(block)
+    g[whole << 20:].copy_(block[:n - (whole << 20)])
+    p = torch.full((n,), 0.01, device=dev)
+    m = torch.randint(0, 256, (1 << 20,), dtype=torch.uint8, device=dev).repeat(whole + 1)[:n]
+    v = torch.randint(0, 256, (1 << 20,), dtype=torch.uint8, device=dev).repeat(whole + 1)[:n]
+    nb = -(-n // 256)
+    ms, vs = (torch.full((nb,), x, dtype=torch.uint8, device=dev) for x in (117, 107))
+    where = [(0, 4096), (1 << 31, 4096), ((1 << 32) - 2048, 4096), (n - n % 256 - 2048, 2048 + n % 256)]
+
+    def window(a, k):
+        b = slice(a // 256, -(-(a + k) // 256))
+        return [to_np(x).copy() for x in (p[a:a + k], m[a:a + k], ms[b], v[a:a + k], vs[b], g[a:a + k])]
+
+    before = [window(a, k) for a, k in where]
+    table = zs.MultiTable([p], [m.contiguous()], [v], [g], None, [ms], [vs])
+    m = table.tensors[1]
+    hp = dict(HP, eps=0.0)
+    zs.zs_adamw_multi(table, dict(step=4, **hp), seed=99)
+    torch.cuda.synchronize()
+    for (a, k), (p0, mc, m_s, vc, v_s, gg) in zip(where, before):
+        with np.errstate(all="ignore"):
+            want = F.adamw_step8(p0, mc, m_s, vc, v_s, O.bf16_widen(gg), O.AdamWHP(step=4, **hp), 99,
+                                 0, a)
+        got = window(a, k)
+        check_f32(got[0], want[0], f"p at {a}", exact=True)
+        for j, what in enumerate(("m codes", "m scales", "v codes", "v scales"), 1):
+            check_bits(got[j], want[j], f"{what} at {a}")
+    s, nc = norm_of(zs.MultiTable(grads=[g]))
+    part = F.sumsq([O.bf16_widen(to_np(block))])
+    tail = F.sumsq([O.bf16_widen(to_np(block[:n - (whole << 20)]))])
+    assert abs(float(s) - (whole * part + tail)) <= n * 2.0**-53 * (whole * part + tail)
+
+
 def test_adamw_multi_empty_and_side_stream():
     dev = device()
     zs.zs_adamw_multi(zs.MultiTable([], [], [], [], device=dev), dict(step=1, **HP))

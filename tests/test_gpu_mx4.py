@@ -125,6 +125,29 @@ def test_gather_past_32_bits():
         check_bf16(to_np(flat[r * S:(r + 1) * S]), O.bf16_round(want), f"shard {r}", exact=True)
 
 
+def test_quantize_past_32_bits():
+    """A shard of 2^32 + 37 bf16 elements: windows at its start, around element 2^31 and
+    2^32 and at its end, quantised and gathered again."""
+    dev = device()
+    S = (1 << 32) + 37
+    block = W.as_bf16_bits(W.normal_f32(1 << 20, 0.02, 78, dev))
+    x = torch.empty(S, dtype=torch.int16, device=dev)
+    x[:S - 37].view(-1, 1 << 20).copy_(block)
+    x[S - 37:].copy_(block[5:42])
+    codes = torch.zeros(-(-S // 2), dtype=torch.uint8, device=dev)
+    scales = torch.zeros(-(-S // 32), dtype=torch.uint8, device=dev)
+    zs.zs_quantize_mx4(x, codes, scales)
+    flat = torch.zeros(S, dtype=torch.int16, device=dev)
+    zs.zs_gather_unit_mx4([codes], [scales], flat)
+    torch.cuda.synchronize()
+    for a, k in ((0, 4096), (1 << 31, 4096), ((1 << 32) - 2048, 2048 + 37)):
+        wc, ws = F.mx4_quantize(O.bf16_widen(to_np(x[a:a + k])))
+        check_bits(to_np(codes[a // 2:a // 2 + wc.size]), wc, f"codes at {a}")
+        check_bits(to_np(scales[a // 32:a // 32 + ws.size]), ws, f"scales at {a}")
+        want = F.mx4_values(wc, ws, k).astype(np.float32)
+        check_bf16(to_np(flat[a:a + k]), O.bf16_round(want), f"values at {a}", exact=True)
+
+
 def test_step_quantize_gather_together():
     """A rank's working shards as a run uses them: each rank steps its shard, its bf16
     working shard is quantised, and the unit is gathered from the 4-bit shards; then the
