@@ -14,18 +14,8 @@ namespace {
 __device__ __forceinline__ float bf16_lo(uint32_t word) { return __uint_as_float(word << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t word) { return __uint_as_float(word & 0xffff0000u); }
 
-// fp32 -> bf16 bits, IEEE round to nearest, ties to even. Adding 0x7fff plus
-// the kept low bit carries into the kept half exactly when the dropped half
-// is above one half, or equal to it with an odd kept half. NaNs keep sign
-// and high payload and are made quiet.
-__device__ __forceinline__ uint32_t f32_to_bf16(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const uint32_t rounded = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-    return ((u & 0x7fffffffu) > 0x7f800000u) ? ((u >> 16) | 0x40u) : rounded;
-}
-
-// Two values' bf16 bits in one word, by gfx950's conversion instruction: the same
-// rounding in half an instruction a value, NaNs quiet.
+// Two values' bf16 bits in one word, rounded to nearest, ties to even, NaNs made quiet: by
+// gfx950's conversion instruction, half an instruction a value.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));

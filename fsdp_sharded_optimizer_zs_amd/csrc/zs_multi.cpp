@@ -20,7 +20,8 @@ struct zs_multi {
     int32_t state;
     int32_t dtype;
     std::vector<MultiChunk> chunks;
-    std::vector<Range> grads;  // what the gradients cover: sorted, disjoint
+    std::vector<Range> grads;    // what the gradients cover: sorted, disjoint
+    std::vector<Range> written;  // what the step writes, likewise
 };
 
 namespace {
@@ -62,7 +63,8 @@ void add_chunks(const zs_multi_tensor& x, int32_t t, int32_t state, int es,
         return base ? const_cast<char*>(static_cast<const char*>(base)) + bytes : nullptr;
     };
     int64_t end = ZS_MULTI_CHUNK;  // of the present chunk
-    if (state == ZS_STATE_F32) end -= int64_t(reinterpret_cast<uintptr_t>(x.p) / 4 % 64);
+    if (state == ZS_STATE_F32 && x.numel > ZS_MULTI_CHUNK)
+        end -= int64_t(reinterpret_cast<uintptr_t>(x.p) / 4 % 64);
     for (int64_t i = 0; i < x.numel; i = end, end += ZS_MULTI_CHUNK) {
         MultiChunk c{};
         if (state != ZS_STATE_NONE) {
@@ -113,13 +115,10 @@ zs_status check_tensors(const zs_multi_tensor* ts, int32_t T, int32_t state, int
     return ZS_OK;
 }
 
-// No written range may meet another one or a gradient. Sorted, two written ranges meet
-// only if two neighbours do, and a gradient can only meet the last one that starts
-// before its end.
-zs_status check_alias(const zs_multi_tensor* ts, int32_t T, int32_t state, int es) {
-    const char* who = "zs_multi_create";
-    if (state == ZS_STATE_NONE) return ZS_OK;
+// The ranges that the step writes, sorted.
+std::vector<Owned> owned_ranges(const zs_multi_tensor* ts, int32_t T, int32_t state) {
     std::vector<Owned> own;
+    if (state == ZS_STATE_NONE) return own;
     own.reserve(size_t(T) * 6);
     for (int32_t t = 0; t < T; ++t) {
         const zs_multi_tensor& x = ts[t];
@@ -136,6 +135,13 @@ zs_status check_alias(const zs_multi_tensor* ts, int32_t T, int32_t state, int e
     }
     std::sort(own.begin(), own.end(),
               [](const Owned& a, const Owned& b) { return a.r.lo < b.r.lo; });
+    return own;
+}
+
+// No written range may meet another one or a gradient. Two written ranges meet only if
+// two neighbours do, and a gradient can only meet the last one that starts before its end.
+zs_status check_alias(const zs_multi_tensor* ts, int32_t T, int es, const std::vector<Owned>& own) {
+    const char* who = "zs_multi_create";
     for (size_t i = 1; i < own.size(); ++i)
         if (own[i - 1].r.hi > own[i].r.lo)
             return fail(ZS_EALIAS, "%s: %s of tensor %d overlaps %s of tensor %d", who, own[i].name,
@@ -152,11 +158,8 @@ zs_status check_alias(const zs_multi_tensor* ts, int32_t T, int32_t state, int e
     return ZS_OK;
 }
 
-// The union of the gradients' ranges (gradients may overlap each other).
-std::vector<Range> grad_ranges(const zs_multi_tensor* ts, int32_t T, int es) {
-    std::vector<Range> r;
-    for (int32_t t = 0; t < T; ++t)
-        if (ts[t].numel > 0) r.push_back(range_of(ts[t].g, ts[t].numel, es));
+// The union of ranges: sorted, disjoint, those that touch joined.
+std::vector<Range> merged(std::vector<Range> r) {
     std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     size_t n = 0;
     for (size_t i = 0; i < r.size(); ++i) {
@@ -165,6 +168,13 @@ std::vector<Range> grad_ranges(const zs_multi_tensor* ts, int32_t T, int es) {
     }
     r.resize(n);
     return r;
+}
+
+// Whether x meets one of them.
+bool meets(const std::vector<Range>& sorted, const Range& x) {
+    auto it = std::lower_bound(sorted.begin(), sorted.end(), x.hi,
+                               [](const Range& r, uintptr_t hi) { return r.lo < hi; });
+    return it != sorted.begin() && (it - 1)->hi > x.lo;
 }
 
 // The checks that the moment conversions share.
@@ -190,12 +200,19 @@ ZS_EXPORT zs_status zs_multi_create(const zs_multi_tensor* tensors, int32_t T, i
     if (T > 0 && tensors == nullptr) return fail(ZS_EINVAL, "%s: tensors is NULL", who);
     try {
         zs_status st = check_tensors(tensors, T, state, es);
-        if (st == ZS_OK) st = check_alias(tensors, T, state, es);
+        if (st != ZS_OK) return st;
+        const std::vector<Owned> own = owned_ranges(tensors, T, state);
+        st = check_alias(tensors, T, es, own);
         if (st != ZS_OK) return st;
         int64_t n = T;  // at most: a shortened first chunk can add one
         for (int32_t t = 0; t < T; ++t) n += ceil_div(tensors[t].numel, ZS_MULTI_CHUNK);
-        std::unique_ptr<zs_multi> m(new zs_multi{kMagic, state, dtype, {}, {}});
-        m->grads = grad_ranges(tensors, T, es);
+        std::unique_ptr<zs_multi> m(new zs_multi{kMagic, state, dtype, {}, {}, {}});
+        std::vector<Range> g, w;
+        for (int32_t t = 0; t < T; ++t)
+            if (tensors[t].numel > 0) g.push_back(range_of(tensors[t].g, tensors[t].numel, es));
+        for (const Owned& o : own) w.push_back(o.r);
+        m->grads = merged(std::move(g));
+        m->written = merged(std::move(w));
         m->chunks.reserve(size_t(n));
         for (int32_t t = 0; t < T; ++t) add_chunks(tensors[t], t, state, es, &m->chunks);
         *out = m.release();
@@ -234,6 +251,8 @@ ZS_EXPORT zs_status zs_adamw_multi(const zs_multi* multi, const void* image, con
     st = check_hp(hp, who);
     if (st != ZS_OK) return st;
     if (!aligned(grad_scale, 4)) return fail(ZS_EINVAL, "%s: grad_scale not 4-byte aligned", who);
+    if (grad_scale != nullptr && meets(multi->written, range_of(grad_scale, 1, 4)))
+        return fail(ZS_EALIAS, "%s: grad_scale lies in an array that the step writes", who);
     MultiArgs a;
     bool stoch = false;
     a.rbc2s = 0.0f;
@@ -324,12 +343,9 @@ ZS_EXPORT zs_status zs_grad_norm(const zs_multi* multi, const void* image, doubl
         for (int b = a + 1; b < 3; ++b)
             if (overlap(out[a], out[b]))
                 return fail(ZS_EALIAS, "%s: sumsq, norm_coef and workspace overlap", who);
-    for (const Range& o : out) {
-        auto it = std::lower_bound(multi->grads.begin(), multi->grads.end(), o.hi,
-                                   [](const Range& g, uintptr_t hi) { return g.lo < hi; });
-        if (it != multi->grads.begin() && (it - 1)->hi > o.lo)
+    for (const Range& o : out)
+        if (meets(multi->grads, o))
             return fail(ZS_EALIAS, "%s: an output or the workspace overlaps a gradient", who);
-    }
     return hip_status(launch_norm(image_of(*multi, image), multi->dtype, max_norm, sumsq, norm_coef,
                                   static_cast<NormWorkspace*>(workspace), stream),
                       who);

@@ -3,7 +3,7 @@
 //
 // Both stream once over their data and are bound by HBM: the quantiser reads 2 or 4
 // bytes an element and writes 0.53, the gather reads 0.53 and writes 2 or 4. A lane
-// takes 8 consecutive elements at a time, one 32-bit word of codes, and kUnroll such
+// takes 8 consecutive elements at a time, one 32-bit word of codes, and kMx4Unroll such
 // groups, a workgroup apart, whose loads are all ahead of their use; 4 lanes share a
 // block of 32 and its scale byte.
 //

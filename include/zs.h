@@ -710,7 +710,8 @@ typedef struct {
  *   grad_scale  device pointer to one float, or NULL; read when the kernel runs
  *               (zs_grad_norm's clip factor, a loss scale's inverse)
  *   round       host pointer, or NULL: to nearest
- * Errors: ZS_EINVAL. Tables without elements enqueue nothing.
+ * Errors: ZS_EINVAL, ZS_EALIAS (grad_scale lies in an array that the step
+ * writes). Tables without elements enqueue nothing.
  */
 zs_status zs_adamw_multi(const zs_multi* multi, const void* image, const zs_adamw_hp* hp,
                          const float* grad_scale, const zs_round_opts* round, hipStream_t stream);

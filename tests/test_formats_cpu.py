@@ -346,6 +346,8 @@ def test_adamw_multi_refuses(lib, no_gpu):
                 dict(weight_decay=INF)):
         assert call(h_=hp(**bad)) == zs.ZS_EINVAL
     assert call(scale=A + 1) == zs.ZS_EINVAL
+    for at in (A, A + 3996, A + STEP + 996, A + 2 * STEP, A + 3 * STEP + 1996, A + 5 * STEP):
+        assert call(scale=at) == zs.ZS_EALIAS, at - A              # p, m, v, w_out, m_scale
     assert call(opts=B.zs_round_opts(2, 0, 0)) == zs.ZS_EINVAL
     assert call(opts=B.zs_round_opts(1, 1, 0)) == zs.ZS_EINVAL
     grads = make(lib, [B.zs_multi_tensor(g=A, numel=5)], state=zs.ZS_STATE_NONE)
