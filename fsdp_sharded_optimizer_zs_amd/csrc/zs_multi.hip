@@ -373,6 +373,51 @@ __device__ __forceinline__ uint32_t pack_v(const float (&x)[4], int s, const uin
            __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);
 }
 
+// Order the wavefront's LDS accesses before and after this point.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// HBM is written in 64-byte sectors, and one that two store instructions share is written
+// twice. The blocks of the 8-bit moments fix which elements a wavefront has, so that p and
+// w_out of a tensor off the sectors would share one between every two quarters. Their new
+// values go through the wavefront's slot of LDS instead and leave from the first sector
+// boundary on (element `head`), the few before it and after the last four one by one.
+__device__ __forceinline__ bool off_sectors(const void* p) {
+    return (reinterpret_cast<uintptr_t>(p) & 63) != 0;
+}
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p) {
+    return int((64 - (reinterpret_cast<uintptr_t>(p) & 63)) & 63) / int(sizeof(T));
+}
+__device__ __forceinline__ void store_staged(const MultiChunk& t, const float* slot, int lane) {
+    const int hp = head_of(t.p);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        const int i = hp + q * kQuarter + 4 * lane;
+        const float x[4] = {slot[i], slot[i + 1], slot[i + 2], slot[i + 3]};
+        if (q < kQ - 1 || i + 4 <= kWaveElems) store_f32<true>(t.p, 0, i, 4, x);
+    }
+    const int rp = (kWaveElems - hp) & 3;  // past the last four
+    const int ip = lane < hp ? lane : kWaveElems - rp + lane - 32;
+    if (lane < hp || (lane >= 32 && lane < 32 + rp)) *element<g_f32>(t.p, 0, ip) = slot[ip];
+    if (!t.w_out) return;
+    const int hw = head_of(t.w_out);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        const int i = hw + q * kQuarter + 4 * lane;
+        const float x[4] = {slot[i], slot[i + 1], slot[i + 2], slot[i + 3]};
+        if (q < kQ - 1 || i + 4 <= kWaveElems) store_bf16<true>(t.w_out, 0, i, 4, x);
+    }
+    const int rw = (kWaveElems - hw) & 3;
+    const int iw = lane < hw ? lane : kWaveElems - rw + lane - 32;
+    if (lane < hw || (lane >= 32 && lane < 32 + rw))
+        *element<g_u16>(t.w_out, 0, iw) = uint16_t(pack_bf16(slot[iw], 0.0f));
+}
+constexpr int kSlot = kWaveElems + 32;  // floats: a head's lanes read past the last element
+
 // Largest old scale bytes that step8_wave takes: B1 * 2^(s - 15) and B2 * 2^(s - 31)
 // have to be finite (moments below 2^16 and 2^32; others, and NaN blocks, go by quarters).
 constexpr int kMostM = 142, kMostV = 158;
@@ -410,7 +455,8 @@ __device__ __forceinline__ void load8_wave(const MultiChunk& t, int i, int n, Lo
 template <bool STOCH, bool ALL>
 __device__ __forceinline__ void step8_wave(const MultiChunk& t, Loaded8& d, int i, int n, int lane,
                                            const MultiArgs& a, float mult, uint32_t key, int* lm,
-                                           int* lv) {
+                                           int* lv, float* slot) {
+    const bool staged = ALL && (off_sectors(t.p) || (t.w_out && off_sectors(t.w_out)));
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
         if (!ALL && q * kQuarter >= n) break;
@@ -446,10 +492,20 @@ __device__ __forceinline__ void step8_wave(const MultiChunk& t, Loaded8& d, int 
             *lm = sm;
             *lv = sv;
         }
-        store_f32<ALL>(t.p, q, i, live, d.p[q]);
-        if (t.w_out) store_bf16<ALL>(t.w_out, q, i, live, d.p[q]);
+        if (staged) {
+            reinterpret_cast<f32x4*>(slot)[q * 64 + lane] =
+                f32x4{d.p[q][0], d.p[q][1], d.p[q][2], d.p[q][3]};
+        } else {
+            store_f32<ALL>(t.p, q, i, live, d.p[q]);
+            if (t.w_out) store_bf16<ALL>(t.w_out, q, i, live, d.p[q]);
+        }
         store_codes<ALL>(t.m, q, i, live, wm);
         store_codes<ALL>(t.v, q, i, live, wv);
+    }
+    if (staged) {
+        wave_sync();
+        store_staged(t, slot, lane);
+        wave_sync();
     }
 }
 
@@ -493,6 +549,7 @@ __global__ __launch_bounds__(kThreads) void multi32_kernel(
 template <int DT, bool STOCH, bool EXACT>
 __global__ __launch_bounds__(kThreads) void multi8_kernel(
     const MultiChunk* __restrict__ chunks, int64_t n_chunks, MultiArgs a) {
+    __shared__ __attribute__((aligned(16))) float slots[kWaves][kSlot];
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const float mult = a.grad_scale ? *a.grad_scale : 1.0f;
@@ -516,11 +573,13 @@ __global__ __launch_bounds__(kThreads) void multi8_kernel(
             if (n >= kWaveElems) {
                 load8_wave<DT, true>(t, i, n, d);
                 done = __all(lm <= kMostM && lv <= kMostV);
-                if (done) step8_wave<STOCH, true>(t, d, i, n, lane, a, mult, key, &lm, &lv);
+                if (done)
+                    step8_wave<STOCH, true>(t, d, i, n, lane, a, mult, key, &lm, &lv, slots[wave]);
             } else {
                 load8_wave<DT, false>(t, i, n, d);
                 done = __all(lm <= kMostM && lv <= kMostV);
-                if (done) step8_wave<STOCH, false>(t, d, i, n, lane, a, mult, key, &lm, &lv);
+                if (done)
+                    step8_wave<STOCH, false>(t, d, i, n, lane, a, mult, key, &lm, &lv, nullptr);
             }
         }
         if (!done) {
