@@ -22,11 +22,10 @@ inline int64_t norm_grid(int64_t n_chunks) {
     return b < 1 ? 1 : (b < kNormGrid ? b : kNormGrid);
 }
 
-// 4-bit quantisation: one workgroup per tile of kMx4Unroll groups of 8 elements a lane.
-constexpr int kMx4Unroll = 4;
+// 4-bit quantisation: one workgroup per tile of 32 elements a lane.
+constexpr int kMx4Tile = kBlockThreads * 32;
 inline int64_t quantize_mx4_grid(int64_t S) {
-    const int64_t tile = int64_t(kBlockThreads) * 8 * kMx4Unroll;
-    return grid_blocks(S / tile + (S % tile != 0), 1);
+    return grid_blocks(S / kMx4Tile + (S % kMx4Tile != 0), 1);
 }
 
 // Gather from 4-bit shards: the same tiles, a row of the grid per shard (the whole grid
