@@ -22,16 +22,18 @@ inline int64_t norm_grid(int64_t n_chunks) {
     return b < 1 ? 1 : (b < kNormGrid ? b : kNormGrid);
 }
 
-// 4-bit quantisation: one workgroup per tile of 32 elements a lane.
-constexpr int kMx4Tile = kBlockThreads * 32;
-inline int64_t quantize_mx4_grid(int64_t S) {
-    return grid_blocks(S / kMx4Tile + (S % kMx4Tile != 0), 1);
+// 4-bit quantisation of values of es bytes: one workgroup per tile of kMx4Groups 16-byte
+// groups of values a lane.
+constexpr int kMx4Groups = 2;
+inline int64_t quantize_mx4_grid(int64_t S, int es) {
+    const int64_t tile = int64_t(kBlockThreads) * (16 / es) * kMx4Groups;
+    return grid_blocks(S / tile + (S % tile != 0), 1);
 }
 
 // Gather from 4-bit shards: the same tiles, a row of the grid per shard (the whole grid
 // under the cap).
-inline int64_t gather_mx4_grid(int64_t S, int D) {
-    const int64_t b = quantize_mx4_grid(S), cap = kMaxGrid / D;
+inline int64_t gather_mx4_grid(int64_t S, int es, int D) {
+    const int64_t b = quantize_mx4_grid(S, es), cap = kMaxGrid / D;
     return b < cap ? b : cap;
 }
 

@@ -4,9 +4,11 @@
 // Both stream once over their data and are bound by HBM: the quantiser reads 2 or 4
 // bytes an element and writes 0.53, the gather reads 0.53 and writes 2 or 4. A lane takes
 // 16 bytes of values at a time (8 bf16 or 4 fp32), so that a wavefront's accesses to them
-// are one run of 1 KiB, and 32 elements in such groups, whose loads are all ahead of their
-// use; 4 or 8 lanes share a block of 32 and its scale byte. (With 8 fp32 values a lane, two
-// stores of alternate 16-byte pieces, the gather to fp32 ran at 2.8 TB/s.)
+// are one run of 1 KiB, and two such groups, a workgroup apart, whose loads are both ahead
+// of their use; 4 or 8 lanes share a block of 32 and its scale byte. (A unit of 202M elements
+// gathered to bf16 / fp32: 79 / 149 us; one group 112 / 185, three 82 / 143, four or eight
+// 84 / 172, each 7-20% slower or more at odd shard lengths; 8 fp32 values a lane, two stores
+// of alternate 16-byte pieces, 330.)
 //
 // Two elements are converted by one instruction of gfx950 (v_cvt_scalef32_pk_*_fp4),
 // which takes 2^(s-127) as a float. For s = 0 that float would be subnormal, and s = 255
@@ -25,9 +27,8 @@ namespace zs {
 namespace {
 
 constexpr int kThreads = kBlockThreads;
-constexpr int kBlock = 32;         // elements of a scale byte
-constexpr int kLaneElems = 32;     // elements a lane takes of a tile
-static_assert(kMx4Tile == kThreads * kLaneElems, "the grid counts tiles of a workgroup");
+constexpr int kBlock = 32;   // elements of a scale byte
+constexpr int U = kMx4Groups;  // groups a lane takes of a tile
 
 #define ZS_GLOBAL __attribute__((address_space(1)))
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -71,7 +72,7 @@ struct Group<ZS_F32> {
     uint32_t w[4];
 };
 template <int DT>
-constexpr int kUnroll = kLaneElems / Group<DT>::E;
+constexpr int kTile = kThreads * Group<DT>::E * U;  // elements of a workgroup's tile
 
 // Element i of an array of values.
 template <int DT>
@@ -207,18 +208,18 @@ __device__ __forceinline__ uint32_t encode(const Group<DT>& x, int* scale) {
     return w;
 }
 
-// A bf16 shard of 25.3M elements: 12.4 us, 5.2 TB/s with the launch's start and end, one of
-// 202M 81 us, 6.3 TB/s.
+// A bf16 shard of 25.3M elements: 12 us, 5.2 TB/s with the launch's start and end; one of
+// 202M 78 us, 6.6 TB/s (fp32 151 us, 6.1), at an odd address 90.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restrict__ src, int64_t S,
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
-    constexpr int E = Group<DT>::E, U = kUnroll<DT>, kStep = kThreads * E;
+    constexpr int E = Group<DT>::E, kStep = kThreads * E;
     const bool first = threadIdx.x % (kBlock / E) == 0;  // of the lanes of a block
-    for (int64_t base = blockIdx.x * int64_t(kMx4Tile); base < S;
-         base += gridDim.x * int64_t(kMx4Tile)) {
+    for (int64_t base = blockIdx.x * int64_t(kTile<DT>); base < S;
+         base += gridDim.x * int64_t(kTile<DT>)) {
         const int64_t i0 = base + int64_t(threadIdx.x) * E;
-        if (base + kMx4Tile <= S) {
+        if (base + kTile<DT> <= S) {
             Group<DT> x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) x[u] = load_group<DT>(src, i0 + u * kStep);
@@ -288,26 +289,27 @@ __device__ __forceinline__ Group<DT> decode(uint32_t w, int s) {
     return x;
 }
 
-// A unit of 202M elements from 8 shards to bf16: 84 us, 6.1 TB/s.
+// A unit of 202M elements from 8 shards to bf16: 79 us, 6.5 TB/s; from shards of odd length
+// 85. To fp32 149 us, 6.2 TB/s.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void gather_mx4_kernel(PtrPack codes, PtrPack scales,
                                                               int64_t S, void* __restrict__ flat) {
-    constexpr int E = Group<DT>::E, U = kUnroll<DT>, kStep = kThreads * E;
+    constexpr int E = Group<DT>::E, kStep = kThreads * E;
     const int r = int(blockIdx.y);
     const g_u8* cs = global<const g_u8>(codes.p[r]);
     const g_u8* ss = global<const g_u8>(scales.p[r]);
     const int64_t slot = int64_t(r) * S;
-    for (int64_t base = blockIdx.x * int64_t(kMx4Tile); base < S;
-         base += gridDim.x * int64_t(kMx4Tile)) {
+    for (int64_t base = blockIdx.x * int64_t(kTile<DT>); base < S;
+         base += gridDim.x * int64_t(kTile<DT>)) {
         const int64_t i0 = base + int64_t(threadIdx.x) * E;
-        if (base + kMx4Tile <= S) {
+        if (base + kTile<DT> <= S) {
             uint32_t w[U];
             int s[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t i = i0 + u * kStep;
                 typedef const typename Group<DT>::Codes C;
-                w[u] = *reinterpret_cast<C*>(cs + i / 2);
+                w[u] = __builtin_nontemporal_load(reinterpret_cast<C*>(cs + i / 2));
                 s[u] = ss[i / kBlock];
             }
 #pragma unroll
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(kThreads) void gather_mx4_kernel(PtrPack codes, Ptr
 
 hipError_t launch_quantize_mx4(const void* src, int dtype, int64_t S, uint8_t* codes,
                                uint8_t* scales, hipStream_t stream) {
-    const dim3 grid(unsigned(quantize_mx4_grid(S)));
+    const dim3 grid(unsigned(quantize_mx4_grid(S, dtype == ZS_F32 ? 4 : 2)));
     if (dtype == ZS_BF16)
         hipLaunchKernelGGL((quantize_kernel<ZS_BF16>), grid, dim3(kThreads), 0, stream, src, S,
                            codes, scales);
@@ -345,7 +347,7 @@ hipError_t launch_quantize_mx4(const void* src, int dtype, int64_t S, uint8_t* c
 
 hipError_t launch_gather_mx4(const PtrPack& codes, const PtrPack& scales, int D, int64_t S,
                              int dtype, void* flat, hipStream_t stream) {
-    const dim3 grid(unsigned(gather_mx4_grid(S, D)), unsigned(D));
+    const dim3 grid(unsigned(gather_mx4_grid(S, dtype == ZS_F32 ? 4 : 2, D)), unsigned(D));
     if (dtype == ZS_BF16)
         hipLaunchKernelGGL((gather_mx4_kernel<ZS_BF16>), grid, dim3(kThreads), 0, stream, codes,
                            scales, S, flat);
