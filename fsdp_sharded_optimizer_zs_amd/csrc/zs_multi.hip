@@ -604,27 +604,28 @@ __global__ __launch_bounds__(kThreads) void multi8_kernel(
 
 // ------------------------------------------------------------- conversions
 
-// kQ blocks of 256 elements per wavefront, all loads first: 202M codes to bf16 in 97 us,
-// 6.3 TB/s (one block a wavefront: 200).
-template <bool SIGNED>
+// N blocks of 256 elements per wavefront, all loads first. 202M codes to bf16, N = 4: 97 us,
+// 6.3 TB/s (one block: 200, two: 103, eight: 97); to fp32, N = 2: 166, 6.1 TB/s (four: 180);
+// fp32 to codes, N = 2: 158, 6.4 TB/s (four: 166, eight: 170).
+template <bool SIGNED, int N>
 __global__ __launch_bounds__(kThreads) void encode8_kernel(const float* __restrict__ x, int64_t S,
                                                            uint8_t* __restrict__ codes,
                                                            uint8_t* __restrict__ scales) {
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const uint32_t none[4] = {};
-    for (int64_t base = (int64_t(blockIdx.x) * kWaves + wave) * kWaveElems; base < S;
-         base += int64_t(gridDim.x) * kWaves * kWaveElems) {
-        const int n = int(S - base < kWaveElems ? S - base : kWaveElems);
-        float y[kQ][4];
+    for (int64_t base = (int64_t(blockIdx.x) * kWaves + wave) * (N * kQuarter); base < S;
+         base += int64_t(gridDim.x) * kWaves * (N * kQuarter)) {
+        const int n = int(S - base < (N * kQuarter) ? S - base : (N * kQuarter));
+        float y[N][4];
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
+        for (int q = 0; q < N; ++q) {
             const int live = live_of(q * kQuarter + 4 * lane, n);
             load_f32<false>(x + base, q, 4 * lane, live, y[q]);
         }
         int mine = 0;  // lane q: the scale byte of quarter q
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
+        for (int q = 0; q < N; ++q) {
             const int live = live_of(q * kQuarter + 4 * lane, n);
             if constexpr (!SIGNED) {
 #pragma unroll
@@ -636,31 +637,31 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const float* __restri
                                encode4<SIGNED, false>(y[q], s, none));
             if (lane == q) mine = s;
         }
-        if (lane * kQuarter < n && lane < kQ)
+        if (lane * kQuarter < n && lane < N)
             *element<g_u8>(scales + base / kQuarter, 0, lane) = uint8_t(mine);
     }
 }
 
-template <bool SIGNED, int DT>
+template <bool SIGNED, int DT, int N>
 __global__ __launch_bounds__(kThreads) void decode8_kernel(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales,
                                                            int64_t S, void* __restrict__ out) {
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    for (int64_t base = (int64_t(blockIdx.x) * kWaves + wave) * kWaveElems; base < S;
-         base += int64_t(gridDim.x) * kWaves * kWaveElems) {
-        const int n = int(S - base < kWaveElems ? S - base : kWaveElems);
+    for (int64_t base = (int64_t(blockIdx.x) * kWaves + wave) * (N * kQuarter); base < S;
+         base += int64_t(gridDim.x) * kWaves * (N * kQuarter)) {
+        const int n = int(S - base < (N * kQuarter) ? S - base : (N * kQuarter));
         int mine = 0;
-        if (lane * kQuarter < n && lane < kQ)
+        if (lane * kQuarter < n && lane < N)
             mine = *element<const g_u8>(scales + base / kQuarter, 0, lane);
-        uint32_t w[kQ];
+        uint32_t w[N];
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
+        for (int q = 0; q < N; ++q) {
             const int live = live_of(q * kQuarter + 4 * lane, n);
             w[q] = load_codes<false>(codes + base, q, 4 * lane, live);
         }
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
+        for (int q = 0; q < N; ++q) {
             const int live = live_of(q * kQuarter + 4 * lane, n);
             float x[4];
             decode4<SIGNED>(w[q], __builtin_amdgcn_readlane(mine, q), x);
@@ -840,31 +841,33 @@ hipError_t launch_multi(const MultiImage& im, int state, int dtype, MultiArgs a,
 
 hipError_t launch_encode8(const float* x, int64_t S, bool is_signed, uint8_t* codes,
                           uint8_t* scales, hipStream_t stream) {
-    const dim3 grid(unsigned(state8_grid(S)));
+    const dim3 grid(unsigned(state8_grid(S, 2)));
     if (is_signed)
-        hipLaunchKernelGGL((encode8_kernel<true>), grid, dim3(kThreads), 0, stream, x, S, codes,
+        hipLaunchKernelGGL((encode8_kernel<true, 2>), grid, dim3(kThreads), 0, stream, x, S, codes,
                            scales);
     else
-        hipLaunchKernelGGL((encode8_kernel<false>), grid, dim3(kThreads), 0, stream, x, S, codes,
+        hipLaunchKernelGGL((encode8_kernel<false, 2>), grid, dim3(kThreads), 0, stream, x, S, codes,
                            scales);
     return hipGetLastError();
 }
 
+namespace {
+template <bool SIGNED>
+void launch_decode(const uint8_t* codes, const uint8_t* scales, int64_t S, int dtype, void* out,
+                   hipStream_t stream) {
+    if (dtype == ZS_F32)
+        hipLaunchKernelGGL((decode8_kernel<SIGNED, ZS_F32, 2>), dim3(unsigned(state8_grid(S, 2))),
+                           dim3(kThreads), 0, stream, codes, scales, S, out);
+    else
+        hipLaunchKernelGGL((decode8_kernel<SIGNED, ZS_BF16, 4>), dim3(unsigned(state8_grid(S, 4))),
+                           dim3(kThreads), 0, stream, codes, scales, S, out);
+}
+}  // namespace
+
 hipError_t launch_decode8(const uint8_t* codes, const uint8_t* scales, int64_t S, bool is_signed,
                           int dtype, void* out, hipStream_t stream) {
-    const dim3 grid(unsigned(state8_grid(S)));
-    if (is_signed && dtype == ZS_F32)
-        hipLaunchKernelGGL((decode8_kernel<true, ZS_F32>), grid, dim3(kThreads), 0, stream, codes,
-                           scales, S, out);
-    else if (is_signed)
-        hipLaunchKernelGGL((decode8_kernel<true, ZS_BF16>), grid, dim3(kThreads), 0, stream, codes,
-                           scales, S, out);
-    else if (dtype == ZS_F32)
-        hipLaunchKernelGGL((decode8_kernel<false, ZS_F32>), grid, dim3(kThreads), 0, stream, codes,
-                           scales, S, out);
-    else
-        hipLaunchKernelGGL((decode8_kernel<false, ZS_BF16>), grid, dim3(kThreads), 0, stream, codes,
-                           scales, S, out);
+    is_signed ? launch_decode<true>(codes, scales, S, dtype, out, stream)
+              : launch_decode<false>(codes, scales, S, dtype, out, stream);
     return hipGetLastError();
 }
 

@@ -6,9 +6,10 @@
 
 namespace zs {
 
-// Conversions of 8-bit moments: one wavefront per 4 blocks of 256 elements.
-inline int64_t state8_grid(int64_t S) {
-    return grid_blocks(S / 1024 + (S % 1024 != 0), kBlockThreads / 64);
+// Conversions of 8-bit moments: one wavefront per `blocks` blocks of 256 elements.
+inline int64_t state8_grid(int64_t S, int blocks) {
+    const int64_t per = int64_t(blocks) * 256;
+    return grid_blocks(S / per + (S % per != 0), kBlockThreads / 64);
 }
 
 // The norm over a table's chunks: workgroups of 16 wavefronts, 4 to a chunk, at most 2 on

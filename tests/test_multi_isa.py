@@ -85,7 +85,8 @@ using namespace zs;
 int main() {
     long long a, b;
     while (std::scanf("%lld %lld", &a, &b) == 2)
-        std::printf("%lld %lld %lld %lld %lld %lld\n", (long long)state8_grid(a),
+        std::printf("%lld %lld %lld %lld %lld %lld %lld\n", (long long)state8_grid(a, 4),
+                    (long long)state8_grid(a, 2),
                     (long long)norm_grid(a), (long long)quantize_mx4_grid(a, 2),
                     (long long)quantize_mx4_grid(a, 4), (long long)gather_mx4_grid(a, 2, int(b)),
                     (long long)gather_mx4_grid(a, 4, int(b)));
@@ -108,8 +109,8 @@ def test_grids_are_legal_and_cover_the_work(tmp_path):
     out = subprocess.run([str(tmp_path / "d")], input="".join("%d %d\n" % c for c in cases),
                          capture_output=True, text=True, check=True).stdout.split("\n")
     for (s, D), line in zip(cases, out):
-        state8, norm, *mx4 = (int(x) for x in line.split())
-        for blocks, units, per in ((state8, s, 4096), (mx4[0], s, 4096), (mx4[1], s, 2048)):
+        wide, narrow, norm, *mx4 = (int(x) for x in line.split())
+        for blocks, units, per in ((wide, s, 4096), (narrow, s, 2048), (mx4[0], s, 4096), (mx4[1], s, 2048)):
             assert 1 <= blocks <= MAXG and (blocks == MAXG or blocks * per >= units)
         assert 1 <= norm <= 512 and (norm == 512 or norm * 4 >= s)
         for gather, per in ((mx4[2], 4096), (mx4[3], 2048)):     # the grid is gather x D
