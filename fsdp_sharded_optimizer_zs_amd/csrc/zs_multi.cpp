@@ -52,10 +52,11 @@ MultiImage image_of(const zs_multi& m, const void* image) {
 
 // The chunks of one tensor, its arrays offset to each one's first element. With fp32
 // moments the first chunk of a tensor that starts inside a cache line is shortened so that
-// the others start 64 elements' lines together (256 bytes of p, and 128 of a bf16 w_out and
-// g laid out alike): a wavefront's stores then cover whole lines. (1,000 ragged tensors end
+// the others start where p is at a multiple of 64 elements, and so other arrays laid out
+// alike: a wavefront's stores then cover whole lines. (1,000 ragged tensors end
 // to end, 58M elements, fp32 gradients: 307 us against 377 with every chunk off the lines.)
-// 8-bit moments cannot move off their blocks of 256.
+// 8-bit moments cannot move off their blocks of 256, and the norm, which only reads, gains
+// nothing (135 against 131 us on 2,000 ragged tensors).
 void add_chunks(const zs_multi_tensor& x, int32_t t, int32_t state, int es,
                 std::vector<MultiChunk>* out) {
     const int ms = state == ZS_STATE_F32 ? 4 : 1;
