@@ -50,13 +50,12 @@ MultiImage image_of(const zs_multi& m, const void* image) {
     return MultiImage{static_cast<const MultiChunk*>(image), int64_t(m.chunks.size())};
 }
 
-// The chunks of one tensor, its arrays offset to each one's first element. With fp32
-// moments the first chunk of a tensor that starts inside a cache line is shortened so that
-// the others start where p is at a multiple of 64 elements, and so other arrays laid out
-// alike: a wavefront's stores then cover whole lines. (1,000 ragged tensors end
-// to end, 58M elements, fp32 gradients: 307 us against 377 with every chunk off the lines.)
-// 8-bit moments cannot move off their blocks of 256, and the norm, which only reads, gains
-// nothing (135 against 131 us on 2,000 ragged tensors).
+// The chunks of one tensor, its arrays offset to each one's first element. The first chunk
+// of a tensor that starts inside a cache line is shortened so that the others start where p
+// (without a step: g) is at a multiple of 64 elements, and so are arrays laid out alike: a
+// wavefront then covers whole lines. (1,000 ragged tensors end to end, 58M elements, fp32
+// gradients and moments: 307 us against 377 with every chunk off the lines; the norm of
+// 2,000: 130 against 131.) 8-bit moments cannot move off their blocks of 256.
 void add_chunks(const zs_multi_tensor& x, int32_t t, int32_t state, int es,
                 std::vector<MultiChunk>* out) {
     const int ms = state == ZS_STATE_F32 ? 4 : 1;
@@ -64,8 +63,11 @@ void add_chunks(const zs_multi_tensor& x, int32_t t, int32_t state, int es,
         return base ? const_cast<char*>(static_cast<const char*>(base)) + bytes : nullptr;
     };
     int64_t end = ZS_MULTI_CHUNK;  // of the present chunk
-    if (state == ZS_STATE_F32 && x.numel > ZS_MULTI_CHUNK)
-        end -= int64_t(reinterpret_cast<uintptr_t>(x.p) / 4 % 64);
+    if (state != ZS_STATE_8BIT && x.numel > ZS_MULTI_CHUNK) {
+        const uintptr_t place = state == ZS_STATE_F32 ? reinterpret_cast<uintptr_t>(x.p) / 4
+                                                      : reinterpret_cast<uintptr_t>(x.g) / es;
+        end -= int64_t(place % 64);
+    }
     for (int64_t i = 0; i < x.numel; i = end, end += ZS_MULTI_CHUNK) {
         MultiChunk c{};
         if (state != ZS_STATE_NONE) {

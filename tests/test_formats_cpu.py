@@ -280,6 +280,18 @@ def test_fp32_chunks_cover_a_tensor_and_start_on_lines(lib, no_gpu, n, off):
         assert k == 0 or p % 256 == 0
         at += live
     assert at == n
+    # gradients only: where g is at a multiple of 64 elements
+    h = make(lib, [B.zs_multi_tensor(g=A + 2 * off, numel=n)], state=zs.ZS_STATE_NONE)
+    lib.zs_multi_image(h, ctypes.byref(img), ctypes.byref(nbytes))
+    raw = ctypes.string_at(img.value, nbytes.value)
+    at = 0
+    for k in range(0, len(raw), 80):
+        g = np.frombuffer(raw[k + 48:k + 56], np.uint64).tolist()[0]
+        first, _, live = np.frombuffer(raw[k + 56:k + 68], np.uint32).tolist()
+        assert first == at and 1 <= live <= 4096 and g == A + 2 * off + 2 * at
+        assert k == 0 or g % 128 == 0
+        at += live
+    assert at == n
 
 
 @pytest.mark.parametrize("kw,status", [
