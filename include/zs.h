@@ -681,8 +681,9 @@ typedef struct {
  * 2^-24 (|p * DEC| + |p'|) of the formula's value for these m' and v', the same in every
  * run (with EPS * BC2S < 2^-38 or a beta in (0, 2^-60), p' is the fp32 step's, bit for
  * bit).
- * Blocks of 256 elements, counted from the tensor's
- * first element, share a scale byte s, and a code c stands for
+ *
+ * The codes: blocks of 256 elements, counted from the tensor's first element, share a
+ * scale byte s, and a code c stands for
  *   m:  +-float_of_bits((c & 127) << 20) * 2^(s - 15)     (sign in bit 7)
  *   v:    float_of_bits(c << 20)         * 2^(s - 31)
  * -- a float with 3 bits of mantissa and 4 (m) or 5 (v) of exponent, whose
