@@ -678,8 +678,8 @@ typedef struct {
  * v' before they are encoded). There p' = p * DEC - SS * (m' / den) is held to a bound
  * instead of an operation order, since roots and divisions rounded to the last bit
  * would cost more than the memory traffic: within 2^-21 |SS * (m' / den)| +
- * 2^-24 (|p * DEC| + |p'|) of the formula's value for these m' and v', the same in every
- * run (with EPS * BC2S < 2^-38 or a beta in (0, 2^-60), p' is the fp32 step's, bit for
+ * 2^-24 (|p * DEC| + |p'|) + 2^-149 of the formula's value for these m' and v', the same
+ * in every run (with EPS * BC2S < 2^-38 or a beta in (0, 2^-60), p' is the fp32 step's, bit for
  * bit).
  *
  * The codes: blocks of 256 elements, counted from the tensor's first element, share a
