@@ -705,6 +705,18 @@ def _enqueue(f, ref, stream, *args) -> None:
         _check(status)
 
 
+class _MultiHandle:
+    """Owner of one zs_multi: freed with the last table that refers to it (a
+    table copied with copy.copy shares it)."""
+
+    def __init__(self, multi):
+        self._multi = multi
+
+    def __del__(self):
+        if _lib is not None:
+            _lib.zs_multi_destroy(self._multi)
+
+
 class MultiTable:
     """The tensors of zs_adamw_multi and zs_grad_norm, checked once by the
     library: gradients (all bf16 or all fp32) and, for the step, parameters p
@@ -721,7 +733,6 @@ class MultiTable:
                  v_scale: Sequence = None, device=None):
         import numpy as np
         torch = _torch()
-        self._multi = None
         grads = list(grads)
         T = len(grads)
         lists = dict(p=p, m=m, v=v, m_scale=m_scale, v_scale=v_scale, w_out=w)
@@ -771,7 +782,7 @@ class MultiTable:
         lib = load()
         _check(lib.zs_multi_create(rows.ctypes.data_as(ctypes.POINTER(zs_multi_tensor)), T,
                                    self.state, code, ctypes.byref(multi)))
-        self._multi = multi
+        self._multi, self._owner = multi, _MultiHandle(multi)
         host, nbytes = ctypes.c_void_p(), ctypes.c_int64()
         _check(lib.zs_multi_image(multi, ctypes.byref(host), ctypes.byref(nbytes)))
         device = every[0].device if every else device
@@ -783,11 +794,6 @@ class MultiTable:
             self._dev = self.image.get_device()
             self._home = torch._C._cuda_getCurrentRawStream(self._dev)
         self._ref = every[0] if every else None
-
-    def __del__(self):
-        if getattr(self, "_multi", None) is not None and _lib is not None:
-            _lib.zs_multi_destroy(self._multi)
-            self._multi = None
 
     def _image(self, stream):
         """Address of the device image, which stays allocated until the work on
