@@ -46,6 +46,11 @@ zs_status check_multi(const char* who, const zs_multi* multi, const void* image)
     return ZS_OK;
 }
 
+// The device image of a table: the kernels read it while they write.
+Range image_range(const zs_multi& m, const void* image) {
+    return range_of(image, int64_t(m.chunks.size() * sizeof(MultiChunk)), 1);
+}
+
 MultiImage image_of(const zs_multi& m, const void* image) {
     return MultiImage{static_cast<const MultiChunk*>(image), int64_t(m.chunks.size())};
 }
@@ -256,6 +261,8 @@ ZS_EXPORT zs_status zs_adamw_multi(const zs_multi* multi, const void* image, con
     if (!aligned(grad_scale, 4)) return fail(ZS_EINVAL, "%s: grad_scale not 4-byte aligned", who);
     if (grad_scale != nullptr && meets(multi->written, range_of(grad_scale, 1, 4)))
         return fail(ZS_EALIAS, "%s: grad_scale lies in an array that the step writes", who);
+    if (!multi->chunks.empty() && meets(multi->written, image_range(*multi, image)))
+        return fail(ZS_EALIAS, "%s: image overlaps an array that the step writes", who);
     MultiArgs a;
     bool stoch = false;
     a.rbc2s = 0.0f;
@@ -349,6 +356,9 @@ ZS_EXPORT zs_status zs_grad_norm(const zs_multi* multi, const void* image, doubl
     for (const Range& o : out)
         if (meets(multi->grads, o))
             return fail(ZS_EALIAS, "%s: an output or the workspace overlaps a gradient", who);
+    for (const Range& o : out)
+        if (overlap(image_range(*multi, image), o))
+            return fail(ZS_EALIAS, "%s: an output or the workspace overlaps image", who);
     return hip_status(launch_norm(image_of(*multi, image), multi->dtype, max_norm, sumsq, norm_coef,
                                   static_cast<NormWorkspace*>(workspace), stream),
                       who);

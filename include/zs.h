@@ -711,8 +711,8 @@ typedef struct {
  *   grad_scale  device pointer to one float, or NULL; read when the kernel runs
  *               (zs_grad_norm's clip factor, a loss scale's inverse)
  *   round       host pointer, or NULL: to nearest
- * Errors: ZS_EINVAL, ZS_EALIAS (grad_scale lies in an array that the step
- * writes). Tables without elements enqueue nothing.
+ * Errors: ZS_EINVAL, ZS_EALIAS (grad_scale or image lies in an array that the
+ * step writes). Tables without elements enqueue nothing.
  */
 zs_status zs_adamw_multi(const zs_multi* multi, const void* image, const zs_adamw_hp* hp,
                          const float* grad_scale, const zs_round_opts* round, hipStream_t stream);
@@ -775,7 +775,7 @@ zs_status zs_state8_decode(const uint8_t* codes, const uint8_t* scales, int64_t 
  *                 graphs) need one each
  * A table without elements gives 0, 0 and 1.
  * Errors: ZS_EINVAL, ZS_EALIAS (outputs and workspace overlap, or one of them a
- * gradient).
+ * gradient or the image).
  */
 zs_status zs_grad_norm(const zs_multi* multi, const void* image, double max_norm, double* sumsq,
                        float* norm_coef, void* workspace, hipStream_t stream);
