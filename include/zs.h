@@ -757,7 +757,12 @@ zs_status zs_state8_decode(const uint8_t* codes, const uint8_t* scales, int64_t 
  * brings it down to max_norm.
  *
  *   sumsq[0]     = sum of g * g over every element, in fp64 (exact products;
- *                  the order of the sum depends on the table alone)
+ *                  the order of the sum depends on the table alone: on
+ *                  the tensors' sizes and, for each of more than
+ *                  ZS_MULTI_CHUNK elements, on the place of g
+ *                  (ZS_STATE_NONE) or p (ZS_STATE_F32) modulo 64 elements.
+ *                  Equal gradients at other places, or in a table of another
+ *                  state, may give other last bits)
  *   norm_coef[0] = float(sqrt(sumsq))
  *   norm_coef[1] = float(c) for c = max_norm / (sqrt(sumsq) + 1e-6) < 1, else 1
  *                  (NaN if the sum is NaN; 0 if it is infinite; always 1 when
