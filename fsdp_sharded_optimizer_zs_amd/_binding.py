@@ -815,7 +815,10 @@ def zs_adamw_multi(table: MultiTable, hp, grad_scale=None, seed: int = None,
     device tensor of one element that multiplies every gradient (the clip
     factor norm_coef[1:] of zs_grad_norm), read when the kernel runs. seed:
     8-bit moments are rounded stochastically with random numbers of this seed
-    (a new one each step) instead of to nearest."""
+    (a new one each step) instead of to nearest. Beside 8-bit moments p is held
+    to the formula within 2^-21 of its update and half an ulp each of p * DEC and
+    of itself; with a very small or huge eps (a very small one perhaps in early
+    steps only) it is the fp32 step's bit for bit, at a lower rate: include/zs.h."""
     lib = load()
     h = ctypes.byref(_hp(hp))
     ref, scale, opts = table._ref, None, None

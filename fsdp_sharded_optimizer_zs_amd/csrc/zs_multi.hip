@@ -292,10 +292,12 @@ __device__ __forceinline__ void step32_wave(const MultiChunk& t, int i, int n,
 // operations, each correctly rounded. Otherwise the root and the two quotients are
 // the hardware's one-step approximations and a product with 1 / BC2S: 10 issue slots
 // instead of about 50, of which HBM leaves about 100 an element. Their errors (root and
-// reciprocal 1 ulp, four roundings) stay within 2^-21 of the update. It needs
-// EPS * BC2S >= 2^-38: then the roots that the hardware may flush (of subnormals, so at
-// most 2^-63 / BC2S of the divisor) are below half an ulp of EPS, and the divisor and its
-// reciprocal are normal numbers.
+// reciprocal one ulp, 1 / BC2S, divisor and product half of one: 7 * 2^-24) stay within
+// 2^-21 of the update, but for an m' / den in the subnormals, which is off by 2^-150 as in
+// the fp32 step. It needs EPS * BC2S >= 2^-38: then the roots that the hardware may flush (of
+// subnormals, so at most 2^-63 / BC2S of the divisor) are below half an ulp of EPS. And it
+// needs EPS <= 2^125: the hardware gives 0 for a subnormal reciprocal, and beside EPS the
+// divisor has at most 2^64 / BC2S < 2^91, so that it stays below 2^126.
 template <bool EXACT>
 __device__ __forceinline__ float new_p(float p, float m1, float v1, const MultiArgs& a) {
     if constexpr (EXACT) {
@@ -834,7 +836,8 @@ hipError_t launch_multi(const MultiImage& im, int state, int dtype, MultiArgs a,
     a.rbc2s = float(1.0 / double(a.k.bc2s));
     // when the update's approximations hold (new_p), and B1 and B2 can be scaled exactly
     const auto scales = [](float b) { return b == 0.0f || b >= 0x1p-60f; };
-    const bool exact = !(a.k.eps * a.k.bc2s >= 0x1p-38f && scales(a.k.b1) && scales(a.k.b2));
+    const bool exact = !(a.k.eps * a.k.bc2s >= 0x1p-38f && a.k.eps <= 0x1p125f &&
+                         scales(a.k.b1) && scales(a.k.b2));
     if (dtype == ZS_BF16) launch_dtype<ZS_BF16>(im, state, a, stoch, exact, stream);
     else launch_dtype<ZS_F32>(im, state, a, stoch, exact, stream);
     return hipGetLastError();

@@ -678,9 +678,11 @@ typedef struct {
  * v' before they are encoded). There p' = p * DEC - SS * (m' / den) is held to a bound
  * instead of an operation order, since roots and divisions rounded to the last bit
  * would cost more than the memory traffic: within 2^-21 |SS * (m' / den)| +
- * 2^-24 (|p * DEC| + |p'|) + 2^-149 of the formula's value for these m' and v', the same
- * in every run (with EPS * BC2S < 2^-38 or a beta in (0, 2^-60), p' is the fp32 step's, bit for
- * bit).
+ * 2^-24 (|p * DEC| + |p'|) + (1 + SS / 2) 2^-149 of the formula's value for these m' and
+ * v' wherever m' / den and p' are in fp32's range, the same in every run. With EPS * BC2S <
+ * 2^-38, EPS > 2^125 or a beta in (0, 2^-60), p' is the fp32 step's, bit for bit; BC2S grows
+ * with the step, so with a very small EPS early steps may be of that kind and later ones not
+ * (none is with EPS = 1e-8 and 1 - beta2 > 1.4e-7).
  *
  * The codes: blocks of 256 elements, counted from the tensor's first element, share a
  * scale byte s, and a code c stands for
