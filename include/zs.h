@@ -737,15 +737,18 @@ zs_status zs_state8_layout(const int64_t* numels, int32_t T, int64_t* offsets_ou
  * zs_state8_encode, zs_state8_decode -- fp32 moments to 8-bit codes, rounded to
  * nearest (starting 8-bit moments from a 32-bit run or a checkpoint), and codes to
  * the values they stand for (checkpoints through zs_shard_save, re-sharding).
- * Encoding what was decoded gives the same values (but for blocks whose largest
- * magnitude is below 2^-126).
+ * Encoding what was decoded gives the same values where the blocks of 256 hold the
+ * same elements (but for blocks whose largest magnitude is below 2^-126). Shards of
+ * other lengths have other blocks, whose values are rounded once more: by at most half
+ * a code, 2^-4 of the value or half of the new block's smallest step (v: all of it).
  *
  *   x       device, S floats; for ZS_STATE8_V a negative one counts as NaN
  *   kind    ZS_STATE8_M or ZS_STATE8_V
  *   codes   device, S bytes;  scales  device, ceil(S / 256) bytes
  *   dtype   ZS_F32 (every value exact) or ZS_BF16 (exact down to 2^-133)
  *   out     device, S elements of dtype
- * Errors: ZS_EINVAL, ZS_EALIAS (any two arrays overlap), ZS_EUNSUPPORTED.
+ * Errors: ZS_EINVAL, ZS_EALIAS (x overlaps codes or scales, or these each other;
+ * out overlaps codes or scales), ZS_EUNSUPPORTED.
  */
 zs_status zs_state8_encode(const float* x, int64_t S, int32_t kind, uint8_t* codes,
                            uint8_t* scales, hipStream_t stream);
