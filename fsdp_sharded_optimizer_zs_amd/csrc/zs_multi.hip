@@ -41,10 +41,6 @@ typedef ZS_GLOBAL float g_f32;
 typedef ZS_GLOBAL uint16_t g_u16;
 typedef ZS_GLOBAL uint8_t g_u8;
 
-template <typename G, typename P>
-__device__ __forceinline__ G* global(P* p) {
-    return reinterpret_cast<G*>(reinterpret_cast<uintptr_t>(p));
-}
 // Element q * kQuarter + i of an array whose base scalar registers hold: i is the lane's
 // own 32-bit offset and the quarter's goes into the instruction.
 template <typename G>
@@ -441,7 +437,8 @@ __device__ __forceinline__ void load8_wave(const MultiChunk& t, int i, int n, Lo
         load_f32<ALL>(t.p, q, i, live, d.p[q]);
     }
     // keeps the loads here, in flight beside the scale bytes, ahead of the branch that
-    // waits for those
+    // waits for those (of a whole wavefront; the up to three elements that a lane has left
+    // over at a tensor's end are put together one by one, with a wait for each)
     asm volatile("" ::: "memory");
 }
 
@@ -736,7 +733,8 @@ __device__ __forceinline__ bool arrive(NormWorkspace* ws) {
 // share, and it has arrived there once the wait for it is over; the count goes up after
 // that wait, so that whoever sees the whole count sees every sum.
 //
-// Bound by HBM: 108M fp32 gradients in 2,000 tensors 131 us, 6.6 TB/s; 3.3M bf16 ones 6.0 us
+// Bound by HBM: 217M fp32 gradients in 2,000 tensors 131 us, 6.6 TB/s, as bf16 75 us, 5.8, and
+// 202M bf16 ones in 9 tensors 68 us, 6.0 (8 bytes a lane and load); 3.3M bf16 ones 6.0 us
 // a call (a second launch for the final sum: 12.4). One count for all workgroups 137; 2048
 // smaller workgroups 140 and, on the 3.3M, 13.8; a release with the count, which writes back
 // and invalidates an XCD's whole L2 for every workgroup, 227 and 20.
@@ -811,9 +809,16 @@ void launch32(const MultiImage& im, const MultiArgs& a, hipStream_t stream) {
 
 // Chunks of a step with fp32 moments that is taken to stay in the memory-side cache
 // (256 MiB) between two steps: at up to 18 bytes an element of state, working copy and
-// gradient, 1,800 chunks are at most 133 MB, which leaves room for what runs in between.
-// 3.3M parameters (801 chunks) step in 16.4 us by ordinary accesses against 19.3; 202M in
-// 1050 against 945. With 8-bit moments the gain is 5% or none.
+// gradient, 1,800 chunks are at most 133 MB. By ordinary accesses against non-temporal ones,
+// bf16 gradients, and in between a pass over M MB of other data that reads and writes it:
+//   chunks        M = 0         128           192          256          512
+//      200           -         6 |  7 us     6 |  7      13 |  7         -
+//      800       15 | 17      15 | 21       15 | 20      32 | 21      28 | 21
+//    1,800       27 | 36      33 | 39       44 | 39      60 | 39      48 | 39
+//    3,200       45 | 62 and 82 | 65 with 512; 4,800: 77 | 91 and 112 | 94; 8,000: 171 | 150
+// It pays while step and other data fit the cache together (the rule's assumption: small
+// models, several lists a step) and costs 5 to 21 us where more lies between two steps.
+// With 8-bit moments the gain is 5% or none.
 constexpr int64_t kCachedChunks = 1800;
 
 template <int DT>
