@@ -1,0 +1,439 @@
+"""Operators around an 8-bit unit and a clipped shard step, their plain forms and their cases.
+
+Five operators:
+
+gather8     a matrix of a unit, from the unit's D shards to 8-bit floating point with a scale for
+            each 128 x 128 block, as it is and transposed, and the values that both then stand for
+fwd8        a linear layer's forward pass: activations to 8 bits with a scale for each 128 elements
+            of a row, and their product with the 8-bit weights
+bwd8        its backward pass: the input's gradient, and the weight's gradient written into the
+            unit's flat gradient, from the output's gradient and the input in 8 bits
+reducenorm  a shard's D gradient contributions to their mean, its sum of squares and clip factor
+clipstep    the shard step of several buckets with the gradient clipped by its global norm
+
+The formulas, in the notation of the library's header. 8-bit floating point: e4m3 (largest 448) or
+e5m2 (largest 57344) codes, of blocks that share one scale byte s for 2^(s - 127). With u the fp32
+bits of a block's largest magnitude, s = max(1, ((u + 0x1fffff) >> 23) - E), E = 8 or 15, so that
+no code overflows (255, a block of NaN, if the magnitude is not finite); a code is x * 2^(127 - s)
+rounded to nearest even. Products: y = x W^T, dx = dy W, dW = dy^T x over the values that the codes
+stand for, blocks of x and dy along what the product sums over. The reduced gradient:
+g = (((c_0 + c_1) + ...) + c_{D-1}) * fp32(1 / D), every operation rounded to 32 bits; norm =
+sqrt(sum of g g over every bucket), clip = min(1, max_norm / (norm + 1e-6)), and AdamW on g * clip.
+"""
+import math
+
+import torch
+
+own = False
+
+HP = dict(lr=3e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=100)
+BLOCK = 128
+OPS = ("gather8", "fwd8", "bwd8", "reducenorm", "clipstep")
+MOST = 4096 * 11008 * 4096  # products of the largest case
+
+E4M3, E5M2 = "e4m3", "e5m2"
+MANT = {E4M3: 3, E5M2: 2}
+EMIN = {E4M3: -6, E5M2: -14}    # exponent of the smallest normal code
+ETOP = {E4M3: 8, E5M2: 15}      # exponent of the largest one, 1.75 * 2^ETOP
+
+
+def listed():
+    return [
+        # the first feed-forward matrix of the small GPT's unit, which starts off any alignment
+        dict(name="gather8 gpt ff D4", op="gather8", D=4, dt="bf16", rows=1024, cols=256,
+             offset=394_753, S=820_352),
+        # a decoder block's gate matrix from 8 ranks' shards, across 2 of their borders
+        dict(name="gather8 block gate D8", op="gather8", D=8, dt="bf16", rows=11_008, cols=4096,
+             offset=67_108_864, S=25_297_920),
+        # one new token: the weights' bytes are all there is
+        dict(name="fwd8 one token", op="fwd8", M=1, N=11_008, K=4096, dt="bf16"),
+        # the small GPT's feed-forward on four sequences
+        dict(name="fwd8 gpt", op="fwd8", M=2048, N=256, K=1024, dt="bf16"),
+        # ragged everywhere
+        dict(name="fwd8 odd", op="fwd8", M=777, N=1001, K=1500, dt="f32"),
+        # a decoder block's gate matrix on 4096 tokens
+        dict(name="fwd8 block", op="fwd8", M=4096, N=11_008, K=4096, dt="bf16"),
+        # the small GPT's feed-forward, the weight's gradient as a bf16 contribution
+        dict(name="bwd8 gpt bf16", op="bwd8", M=2048, N=1024, K=256, g=E4M3, dw="bf16"),
+        # a decoder block's gate matrix, gradients in e5m2, the weight's gradient in fp32
+        dict(name="bwd8 block e5m2 fp32", op="bwd8", M=4096, N=11_008, K=4096, g=E5M2, dw="f32"),
+        # the small GPT's shard at D = 4
+        dict(name="reducenorm gpt D4 bf16", op="reducenorm", D=4, S=820_352, dt="bf16", max_norm=1.0),
+        # a decoder block's shard at D = 8
+        dict(name="reducenorm block D8 bf16", op="reducenorm", D=8, S=25_297_920, dt="bf16",
+             max_norm=1.0),
+        # the small GPT's whole shard step
+        dict(name="clipstep gpt D4 bf16", op="clipstep", D=4, buckets=1, S=820_352, root=0, dt="bf16",
+             max_norm=0.1),
+        # two decoder blocks and an odd fp32-reduced root of the same rank
+        dict(name="clipstep blocks D8 bf16", op="clipstep", D=8, buckets=2, S=25_297_920,
+             root=1_000_003, dt="bf16", max_norm=1.0),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return min(hi, int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))
+
+
+def draw(rng):
+    op = rng.choice(OPS)
+    if op == "gather8":
+        D, rows, cols = rng.choice((1, 2, 3, 4, 8, 16, 64)), _log_int(rng, 1, 11_008), _log_int(rng, 1, 4096)
+        before, after = _log_int(rng, 1, 1 << 22) - 1, _log_int(rng, 1, 1 << 22) - 1
+        return dict(op=op, D=D, dt=rng.choice(("bf16", "f32")), rows=rows, cols=cols, offset=before,
+                    S=-(-(before + rows * cols + after) // D))
+    if op in ("fwd8", "bwd8"):
+        most = MOST if op == "fwd8" else MOST // 2
+        while True:
+            few = op == "fwd8" and rng.random() < 0.4  # a few tokens, as in serving
+            M = _log_int(rng, 1, 32) if few else _log_int(rng, 1, 8192)
+            # mostly matrices, now and then next to nothing
+            N, K = (_log_int(rng, *((1, 16) if rng.random() < 0.1 else (17, 11_008))) for _ in range(2))
+            if M * N * K <= most:
+                break
+        if op == "fwd8":
+            return dict(op=op, M=M, N=N, K=K, dt=rng.choice(("bf16", "f32")))
+        return dict(op=op, M=M, N=N, K=K, g=rng.choice((E4M3, E5M2)), dw=rng.choice(("bf16", "f32")))
+    D, dt = rng.choice((1, 2, 3, 4, 8, 16, 32)), rng.choice(("bf16", "f32"))
+    case = dict(op=op, D=D, dt=dt, max_norm=rng.choice((0.1, 1.0, 1000.0)))
+    if op == "reducenorm":
+        return dict(case, S=_log_int(rng, 1, min(25_000_000, 100_000_000 // D)))
+    n = _log_int(rng, 1, 6)
+    most = min(48_000_000, 150_000_000 // D) // (n + 1)
+    return dict(case, buckets=n, S=_log_int(rng, 1, most), root=_log_int(rng, 1, most))
+
+
+def sizes_of(case):
+    """Elements of each bucket of a rank: one a block, and the root's if there is one."""
+    return case["buckets"] * [case["S"]] + ([case["root"]] if case["root"] else [])
+
+
+def _width(dt):
+    return 2 if dt == "bf16" else 4
+
+
+def work(case):
+    """Bytes: each input read once, each output written once (8-bit codes of weights at 1 byte,
+    the values of gathered codes in bf16 as returned). flops: the formulas' operations."""
+    op = case["op"]
+    if op == "gather8":
+        n = case["rows"] * case["cols"]
+        return dict(bytes=n * (_width(case["dt"]) + 2 + 4), flops=6 * n)
+    if op == "fwd8":
+        M, N, K = case["M"], case["N"], case["K"]
+        return dict(bytes=M * K * _width(case["dt"]) + N * K + 2 * M * N, flops=2 * M * N * K)
+    if op == "bwd8":
+        M, N, K = case["M"], case["N"], case["K"]
+        return dict(bytes=2 * M * N + 4 * M * K + N * K * (1 + _width(case["dw"])), flops=4 * M * N * K)
+    S = case["S"] if op == "reducenorm" else sum(sizes_of(case))
+    D = case["D"]
+    if op == "reducenorm":
+        return dict(bytes=S * (D * _width(case["dt"]) + 4), flops=(D + 3) * S)
+    # the mean has to be whole before it is clipped: written once and read once
+    return dict(bytes=S * (D * _width(case["dt"]) + 8 + 26), flops=(D + 18) * S)
+
+
+# ---------------------------------------------------------------- inputs
+
+
+def _normal(shape, std, gen):
+    return torch.randn(shape, generator=gen, device="cuda").mul_(std)
+
+
+def _activations(rows, cols, gen):
+    """Rows of one size, a few columns of which are much larger than the others."""
+    return _normal((rows, cols), 1.0, gen) * _normal((cols,), 1.0, gen).exp_()
+
+
+def _gradients(rows, cols, gen):
+    """Rows (tokens) of very different sizes."""
+    return _normal((rows, cols), 1e-4, gen) * _normal((rows, 1), 1.5, gen).exp_()
+
+
+def _typed(x, dt):
+    return x.bfloat16() if dt == "bf16" else x
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    op = case["op"]
+    st = dict(case=case)
+    if op == "gather8":
+        rows, cols = case["rows"], case["cols"]
+        st["shards"] = [_typed(_normal(case["S"], 0.02, gen), case["dt"]) for _ in range(case["D"])]
+        st["out"] = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+        st["out_t"] = torch.zeros(cols, rows, dtype=torch.bfloat16, device="cuda")
+        if own:
+            import fsdp_sharded_optimizer_zs_amd as zs
+            st["w"] = zs.F8Matrix.empty(rows, cols, block_rows=BLOCK, device="cuda")
+            st["w_t"] = zs.F8Matrix.empty(cols, rows, block_rows=BLOCK, device="cuda")
+        return st
+    if op in ("fwd8", "bwd8"):
+        M, N, K = case["M"], case["N"], case["K"]
+        w = _normal((N, K), 0.02, gen)
+        x = _activations(M, K, gen)
+        st["x"] = _typed(x, case["dt"] if op == "fwd8" else "bf16")
+        st["w"], st["ws"] = _stored(w)
+        if op == "fwd8":
+            st["y"] = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+        else:
+            st["w_t"], st["ws_t"] = _stored(w.t().contiguous())
+            st["dy"] = _gradients(M, N, gen).bfloat16()
+            st["dx"] = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+            # the unit's flat gradient, with a norm's weights before this matrix
+            st["flat"] = torch.zeros(N * K + 2 * K, device="cuda",
+                                     dtype=torch.bfloat16 if case["dw"] == "bf16" else torch.float32)
+            st["dw"] = st["flat"][K:K + N * K].view(N, K)
+        if own:
+            import fsdp_sharded_optimizer_zs_amd as zs
+            st["W"] = zs.F8Matrix(st["w"], st["ws"], N, K, block_rows=BLOCK)
+            st["g"] = zs.ZS_E5M2 if case.get("g") == E5M2 else zs.ZS_E4M3
+            if op == "fwd8":
+                need = zs.zs_linear_f8_workspace(M, N, K)
+            else:
+                st["Wt"] = zs.F8Matrix(st["w_t"], st["ws_t"], K, N, block_rows=BLOCK)
+                need = zs.zs_linear_f8_backward_workspace(M, N, K)
+            st["workspace"] = torch.zeros(need, dtype=torch.uint8, device="cuda")
+        return st
+    sizes = [case["S"]] if op == "reducenorm" else sizes_of(case)
+    st["contribs"] = [[_typed(_normal(S, 1e-3, gen), case["dt"]) for _ in range(case["D"])] for S in sizes]
+    st["g"] = [torch.zeros(S, device="cuda") for S in sizes]
+    st["sumsq"] = torch.zeros(1, dtype=torch.float64, device="cuda")
+    st["norm_coef"] = torch.zeros(2, device="cuda")
+    if op == "clipstep":
+        st["p"] = [_normal(S, 0.02, gen) for S in sizes]
+        st["m"] = [_normal(S, 3e-4, gen) for S in sizes]
+        st["v"] = [_normal(S, 1e-3, gen).square_() for S in sizes]
+        st["w"] = [torch.zeros(S, dtype=torch.bfloat16, device="cuda") for S in sizes]
+    if own:
+        import fsdp_sharded_optimizer_zs_amd as zs
+        st["workspace"] = torch.zeros(zs.ZS_NORM_WORKSPACE, dtype=torch.uint8, device="cuda")
+    return st
+
+
+# ---------------------------------------------------------------- one pass
+
+
+def run(st):
+    op = st["case"]["op"]
+    if own:
+        return _own(st, op)
+    return dict(gather8=_gather8, fwd8=_fwd8, bwd8=_bwd8, reducenorm=_reducenorm, clipstep=_clipstep)[op](st)
+
+
+def _own(st, op):
+    import fsdp_sharded_optimizer_zs_amd as zs
+    case = st["case"]
+    if op == "gather8":
+        zs.zs_gather_matrix_f8(st["shards"], case["offset"], st["w"], st["w_t"])
+        zs.zs_dequantize_f8(st["w"], st["out"])
+        zs.zs_dequantize_f8(st["w_t"], st["out_t"])
+        return dict(w=st["out"], w_t=st["out_t"])
+    if op == "fwd8":
+        zs.zs_linear_f8(st["x"], st["W"], st["y"], st["workspace"])
+        return st["y"]
+    if op == "bwd8":
+        zs.zs_linear_f8_backward(st["dy"], st["x"], st["Wt"], st["dx"], st["dw"], st["workspace"],
+                                 grad_type=st["g"])
+        return dict(dx=st["dx"], dw=st["dw"])
+    for k, (c, g) in enumerate(zip(st["contribs"], st["g"])):
+        zs.zs_reduce_shard_norm(c, g, st["sumsq"], st["workspace"], accumulate=k > 0)
+    zs.zs_clip_coef([st["sumsq"]], case["max_norm"], st["norm_coef"])
+    if op == "reducenorm":
+        return dict(g=st["g"][0], sumsq=st["sumsq"], norm_coef=st["norm_coef"])
+    for k, g in enumerate(st["g"]):
+        zs.zs_adamw_step_clip(st["p"][k], st["m"][k], st["v"][k], st["w"][k], [g], HP, st["norm_coef"][1:])
+    return dict(p=st["p"], m=st["m"], v=st["v"], w=st["w"], norm_coef=st["norm_coef"])
+
+
+def _pow2(e):
+    """2^e in fp32 for whole numbers e in [-126, 127], exactly."""
+    return ((e.int() + 127) << 23).view(torch.float32)
+
+
+def _ceil(n, k=BLOCK):
+    return -(-n // k) * k
+
+
+def _quantized(x, kind, block_rows):
+    """Codes' values (before the scale) and scale bytes of a matrix, whose blocks are
+    block_rows x 128; padded to whole blocks."""
+    rows, cols = x.shape
+    R, C = _ceil(rows, block_rows), _ceil(cols)
+    pad = torch.zeros(R, C, device=x.device)
+    pad[:rows, :cols] = x
+    blocks = pad.view(R // block_rows, block_rows, C // BLOCK, BLOCK)
+    u = blocks.abs().amax((1, 3)).view(torch.int32)
+    s = ((u.long() + 0x1FFFFF) >> 23) - ETOP[kind]
+    s = torch.where(u >= 0x7F800000, 255, s.clamp(min=1)).int()
+    y = blocks * _pow2(127 - s.clamp(max=253))[:, None, :, None]
+    e = ((y.abs().view(torch.int32) >> 23) - 127).clamp(min=EMIN[kind])
+    step = _pow2(e - MANT[kind])
+    return (torch.round(y / step) * step).view(R, C), s
+
+
+def _values(x, kind, block_rows=1):
+    """What the 8-bit form of a matrix stands for, in fp32."""
+    q, s = _quantized(x.float(), kind, block_rows)
+    two = torch.where(s == 255, float("nan"), _pow2(s.clamp(max=254) - 127))
+    two = two.repeat_interleave(block_rows, 0).repeat_interleave(BLOCK, 1)
+    return (q * two)[: x.shape[0], : x.shape[1]]
+
+
+def _stored(w):
+    """Codes (e4m3, rows padded to whole blocks) and scale bytes (rows padded to 4) of weights."""
+    q, s = _quantized(w, E4M3, BLOCK)
+    bits = q.abs().view(torch.int32)
+    code = torch.where(bits < (121 << 23), (q.abs() * 512).int(), (bits >> 20) - (120 << 3))
+    code = (code | (torch.signbit(q).int() << 7)).to(torch.uint8)[: w.shape[0]].contiguous()
+    scales = torch.ones(s.shape[0], _ceil(s.shape[1], 4), dtype=torch.uint8, device=w.device)
+    scales[:, : s.shape[1]] = s
+    return code, scales
+
+
+def _loaded(codes, scales, rows, cols):
+    """Values of stored weights in fp32."""
+    table = torch.tensor([_e4m3(c) for c in range(256)], device=codes.device)
+    two = _pow2(scales.int() - 127).repeat_interleave(BLOCK, 0)[:rows].repeat_interleave(BLOCK, 1)
+    return table[codes[:, :cols].int()] * two[:, :cols]
+
+
+def _e4m3(c):
+    e, f = (c >> 3) & 15, c & 7
+    mag = math.ldexp(f / 8, -6) if e == 0 else math.ldexp(1 + f / 8, e - 7)
+    return (math.nan if c & 127 == 127 else mag) * (-1 if c >= 128 else 1)
+
+
+def _gather8(st):
+    case = st["case"]
+    n = case["rows"] * case["cols"]
+    flat = torch.cat(st["shards"])[case["offset"]:case["offset"] + n].view(case["rows"], case["cols"])
+    v = _values(flat, E4M3, BLOCK)
+    st["out"].copy_(v)
+    st["out_t"].copy_(v.t())
+    return dict(w=st["out"], w_t=st["out_t"])
+
+
+def _fwd8(st):
+    case = st["case"]
+    x = _values(st["x"], E4M3)
+    st["y"].copy_(x @ _loaded(st["w"], st["ws"], case["N"], case["K"]).t())
+    return st["y"]
+
+
+def _bwd8(st):
+    case = st["case"]
+    dy = _values(st["dy"], case["g"])
+    st["dx"].copy_(dy @ _loaded(st["w"], st["ws"], case["N"], case["K"]))
+    dy_t = _values(st["dy"].t(), case["g"])
+    x_t = _values(st["x"].t(), E4M3)
+    st["dw"].copy_(dy_t @ x_t.t())
+    return dict(dx=st["dx"], dw=st["dw"])
+
+
+def _reduced(st):
+    total = None
+    for c, g in zip(st["contribs"], st["g"]):
+        s = c[0].float()
+        for x in c[1:]:
+            s = s + x.float()
+        g.copy_(s * torch.full((1,), 1.0 / len(c), device=s.device))
+        sq = g.double().square().sum()
+        total = sq if total is None else total + sq
+    norm = total.sqrt()
+    c = st["case"]["max_norm"] / (norm + 1e-6)
+    st["sumsq"].copy_(total)
+    st["norm_coef"].copy_(torch.stack([norm, torch.where(c >= 1, 1.0, c)]))
+
+
+def _reducenorm(st):
+    _reduced(st)
+    return dict(g=st["g"][0], sumsq=st["sumsq"], norm_coef=st["norm_coef"])
+
+
+def _clipstep(st):
+    _reduced(st)
+    b1t, b2t = HP["beta1"] ** HP["step"], HP["beta2"] ** HP["step"]
+    for p, m, v, w, g in zip(st["p"], st["m"], st["v"], st["w"], st["g"]):
+        g = g * st["norm_coef"][1]
+        m.copy_(m * HP["beta1"] + g * (1.0 - HP["beta1"]))
+        v.copy_(v * HP["beta2"] + (g * g) * (1.0 - HP["beta2"]))
+        bc2s = torch.full((1,), math.sqrt(1.0 - b2t), device=v.device)
+        den = v.sqrt() / bc2s + HP["eps"]
+        p.copy_(p * (1.0 - HP["lr"] * HP["weight_decay"]) - (m / den) * (HP["lr"] / (1.0 - b1t)))
+        w.copy_(p)
+    return dict(p=st["p"], m=st["m"], v=st["v"], w=st["w"], norm_coef=st["norm_coef"])
+
+
+# ---------------------------------------------------------------- the definitions in 64 bits
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    op = case["op"]
+    if op == "gather8":
+        flat = torch.cat([s.double() for s in st["shards"]])
+        w = flat[case["offset"]:][: case["rows"] * case["cols"]].view(case["rows"], case["cols"])
+        v = _nearby(w, E4M3, BLOCK)
+        return dict(w=v, w_t=v.t().contiguous())
+    if op in ("fwd8", "bwd8"):
+        w = _table(st["w"], st["ws"])[: case["N"], : case["K"]]
+        if op == "fwd8":
+            return torch.mm(_nearby(st["x"].double(), E4M3, 1), w.t().contiguous())
+        dy, x = st["dy"].double(), st["x"].double()
+        dy_t = _nearby(dy.t().contiguous(), case["g"], 1)
+        x_t = _nearby(x.t().contiguous(), E4M3, 1)
+        return dict(dx=torch.mm(_nearby(dy, case["g"], 1), w), dw=torch.mm(dy_t, x_t.t().contiguous()))
+    g = [sum(x.double() for x in c) / len(c) for c in st["contribs"]]
+    total = sum(float(x.dot(x)) for x in g)
+    norm = math.sqrt(total)
+    clip = min(1.0, case["max_norm"] / (norm + 1e-6))
+    norm_coef = torch.tensor([norm, clip], dtype=torch.float64)
+    if op == "reducenorm":
+        return dict(g=g[0], sumsq=torch.tensor([total], dtype=torch.float64), norm_coef=norm_coef)
+    b1, b2, t = HP["beta1"], HP["beta2"], HP["step"]
+    out = dict(p=[], m=[], v=[], w=[], norm_coef=norm_coef)
+    for k, x in enumerate(g):
+        m = b1 * st["m"][k].double() + (1 - b1) * clip * x
+        v = b2 * st["v"][k].double() + (1 - b2) * (clip * x) ** 2
+        hat = (m / (1 - b1 ** t)) / ((v / (1 - b2 ** t)).sqrt() + HP["eps"])
+        p = st["p"][k].double() * (1 - HP["lr"] * HP["weight_decay"]) - HP["lr"] * hat
+        for name, value in zip("pmvw", (p, m, v, p)):
+            out[name].append(value)
+    return out
+
+
+def _two(e):
+    """2^e from a table of powers."""
+    table = torch.tensor([math.ldexp(1.0, k) for k in range(-400, 401)], device="cuda",
+                         dtype=torch.float64)
+    return table[(e + 400).long()]
+
+
+def _nearby(x, kind, block_rows):
+    """Values of the 8-bit format next to x, under the smallest power of two that brings its
+    block's largest magnitude to the largest code's, in 64-bit arithmetic."""
+    rows, cols = x.shape
+    x = torch.nn.functional.pad(x, (0, -cols % BLOCK, 0, -rows % block_rows))
+    tiles = x.unflatten(1, (-1, BLOCK)).unflatten(0, (-1, block_rows))
+    top = tiles.abs().amax((1, 3), keepdim=True)
+    part, e = torch.frexp(top)
+    # top = part * 2^e <= 1.75 * 2^(ETOP + k) for the smallest k
+    k = (e.long() - 1 - ETOP[kind] + (part > 0.875).long()).clamp(min=1 - 127)
+    y = tiles / _two(k)
+    binade = torch.frexp(y.abs().clamp(min=math.ldexp(1.0, EMIN[kind])))[1].long() - 1
+    step = _two(binade - MANT[kind])
+    q = torch.round(y / step) * step * _two(k)
+    return q.flatten(2, 3).flatten(0, 1)[:rows, :cols].contiguous()
+
+
+def _table(codes, scales):
+    """Values of e4m3 codes as numbers: sign, 4 bits of exponent, 3 behind the point."""
+    c = codes.long()
+    field, part = (c // 8) % 16, (c % 8).double() / 8
+    mag = torch.where(field > 0, (1 + part) * _two(field - 7), part * _two(field * 0 - 6))
+    mag = torch.where(c >= 128, -mag, mag)
+    at = torch.arange(codes.shape[0], device="cuda") // BLOCK
+    return mag.unflatten(1, (-1, BLOCK)).mul(
+        _two(scales[at, : codes.shape[1] // BLOCK].long() - 127)[:, :, None]).flatten(1, 2)
