@@ -238,8 +238,9 @@ def _own(st, op):
                                  grad_type=st["g"])
         return dict(dx=st["dx"], dw=st["dw"])
     for k, (c, g) in enumerate(zip(st["contribs"], st["g"])):
-        zs.zs_reduce_shard_norm(c, g, st["sumsq"], st["workspace"], accumulate=k > 0)
-    zs.zs_clip_coef([st["sumsq"]], case["max_norm"], st["norm_coef"])
+        # the norm of what has been reduced so far: after the last bucket, of the whole gradient
+        zs.zs_reduce_shard_norm(c, g, case["max_norm"], st["sumsq"], st["norm_coef"], st["workspace"],
+                                accumulate=k > 0)
     if op == "reducenorm":
         return dict(g=st["g"][0], sumsq=st["sumsq"], norm_coef=st["norm_coef"])
     for k, g in enumerate(st["g"]):
