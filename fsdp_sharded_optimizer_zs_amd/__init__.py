@@ -17,6 +17,10 @@ from ._binding import (  # noqa: F401
     zs_stream_ceiling_timed, MultiTable, zs_adamw_multi, zs_grad_norm, zs_clip_coef,
     zs_state8_layout, zs_state8_encode, zs_state8_decode, zs_quantize_mx4, zs_gather_unit_mx4,
     ZS_STATE_NONE, ZS_STATE_F32, ZS_STATE_8BIT, ZS_STATE8_M, ZS_STATE8_V, ZS_NORM_WORKSPACE,
+    zs_reduce_shard_norm, zs_adamw_step_clip, F8Matrix, zs_f8_layout, zs_quantize_f8,
+    zs_gather_matrix_f8, zs_dequantize_f8, zs_matmul_f8, zs_matmul_f8_workspace,
+    zs_linear_f8, zs_linear_f8_workspace, zs_linear_f8_backward,
+    zs_linear_f8_backward_workspace, ZS_E4M3, ZS_E5M2,
 )
 
 __all__ = [
@@ -31,4 +35,8 @@ __all__ = [
     "zs_state8_encode", "zs_state8_decode", "zs_quantize_mx4", "zs_gather_unit_mx4",
     "ZS_STATE_NONE", "ZS_STATE_F32", "ZS_STATE_8BIT", "ZS_STATE8_M", "ZS_STATE8_V",
     "ZS_NORM_WORKSPACE",
+    "zs_reduce_shard_norm", "zs_adamw_step_clip", "F8Matrix", "zs_f8_layout",
+    "zs_quantize_f8", "zs_gather_matrix_f8", "zs_dequantize_f8", "zs_matmul_f8",
+    "zs_matmul_f8_workspace", "zs_linear_f8", "zs_linear_f8_workspace",
+    "zs_linear_f8_backward", "zs_linear_f8_backward_workspace", "ZS_E4M3", "ZS_E5M2",
 ]

@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(HERE, "libzs.so")
 
 ZS_OK, ZS_EINVAL, ZS_EALIAS, ZS_EHIP, ZS_EUNSUPPORTED, ZS_EIO = 0, 1, 2, 3, 4, 5
 ZS_BF16, ZS_F32 = 1, 2
+ZS_E4M3, ZS_E5M2 = 3, 4
 ZS_MAX_D = 64
 
 
@@ -61,6 +62,12 @@ class zs_multi_tensor(ctypes.Structure):
 class zs_round_opts(ctypes.Structure):
     _fields_ = [("stochastic", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("seed", ctypes.c_uint64)]
+
+
+class zs_f8_matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32)]
 
 
 class zs_shard_info(ctypes.Structure):
@@ -137,6 +144,25 @@ def load() -> ctypes.CDLL:
                 "zs_multi_create": (i32, [P(zs_multi_tensor), i32, i32, i32, P(vp)]),
                 "zs_multi_image": (i32, [vp, P(vp), P(i64)]),
                 "zs_multi_destroy": (i32, [vp]),
+                "zs_reduce_shard_norm": (i32, [P(vp), i32, P(zs_reduce_opts), i32, i64, vp,
+                                               ctypes.c_double, vp, vp, i32, vp, vp]),
+                "zs_adamw_step_clip": (i32, [vp, vp, vp, vp, i64, P(vp), i32, P(zs_reduce_opts),
+                                             i32, P(zs_adamw_hp), vp, vp]),
+                "zs_f8_layout": (i32, [i64, i64, i32, P(i64), P(i64)]),
+                "zs_quantize_f8": (i32, [vp, i32, i64, P(zs_f8_matrix), P(zs_f8_matrix), vp]),
+                "zs_gather_matrix_f8": (i32, [P(vp), i32, i64, i32, i64, P(zs_f8_matrix),
+                                              P(zs_f8_matrix), vp]),
+                "zs_dequantize_f8": (i32, [P(zs_f8_matrix), i32, vp, i64, vp]),
+                "zs_matmul_f8": (i32, [P(zs_f8_matrix), P(zs_f8_matrix), i32, vp, i64, i32, vp,
+                                       vp]),
+                "zs_matmul_f8_workspace": (i32, [i64, i64, i64, P(i64)]),
+                "zs_linear_f8": (i32, [vp, i32, i64, i64, i32, P(zs_f8_matrix), i32, vp, i64, vp,
+                                       vp]),
+                "zs_linear_f8_workspace": (i32, [i64, i64, i64, P(i64)]),
+                "zs_linear_f8_backward": (i32, [vp, i64, vp, i64, i32, i64, i64, i64, i32,
+                                                P(zs_f8_matrix), i32, vp, i64, i32, vp, i64, i32,
+                                                vp, vp]),
+                "zs_linear_f8_backward_workspace": (i32, [i64, i64, i64, P(i64)]),
                 "zs_adamw_multi": (i32, [vp, vp, P(zs_adamw_hp), vp, P(zs_round_opts), vp]),
                 "zs_state8_layout": (i32, [P(i64), i32, P(i64)]),
                 "zs_state8_encode": (i32, [vp, i64, i32, vp, vp, vp]),
@@ -942,6 +968,260 @@ def zs_gather_unit_mx4(codes: Sequence, scales: Sequence, flat_out, stream=None)
     _same_device((flat_out, codes[0], scales[0]), "zs_gather_unit_mx4")
     _enqueue(load().zs_gather_unit_mx4, flat_out, stream, *arrays, D, S, code,
              flat_out.data_ptr())
+
+
+# ------------------------------------------- the clipped step of one shard
+def zs_reduce_shard_norm(contribs: Sequence, grad_out, max_norm: float, sumsq, norm_coef, workspace,
+                         accumulate: bool = False, replicas: int = 1,
+                         round_to_reduce_dtype: bool = False, scale: float = 0.0,
+                         stream=None) -> None:
+    """zs_reduce_shard_ex, and the sum of the squares of grad_out in sumsq (float64,
+    1 element), added to what it holds with accumulate: the buckets of a step in
+    turn. norm_coef (float32, 2) or None = its root and the factor that clips it to
+    max_norm, after the last bucket what zs_adamw_step_clip takes. workspace as
+    zs_grad_norm."""
+    torch = _torch()
+    contribs = list(contribs)
+    S = grad_out.numel()
+    _typed(grad_out, "grad_out", torch.float32)
+    code = _contributions(contribs, S)
+    _typed(sumsq, "sumsq", torch.float64, 1)
+    _typed(workspace, "workspace", torch.uint8)
+    if workspace.numel() < ZS_NORM_WORKSPACE:
+        raise ValueError(f"workspace must hold {ZS_NORM_WORKSPACE} bytes")
+    side = [grad_out, sumsq, workspace]
+    if norm_coef is not None:
+        _typed(norm_coef, "norm_coef", torch.float32, 2)
+        side.append(norm_coef)
+    _same_device(contribs + side, "zs_reduce_shard_norm")
+    opts = zs_reduce_opts(int(replicas), 1 if round_to_reduce_dtype else 0, float(scale))
+    _enqueue(load().zs_reduce_shard_norm, grad_out, stream, _ptr_array(contribs),
+             _groups(contribs, replicas), ctypes.byref(opts), code, S, grad_out.data_ptr(),
+             float(max_norm), sumsq.data_ptr(),
+             None if norm_coef is None else norm_coef.data_ptr(), 1 if accumulate else 0,
+             workspace.data_ptr())
+
+
+def zs_adamw_step_clip(p, m, v, w_out, contribs: Sequence, hp, grad_scale, replicas: int = 1,
+                       round_to_reduce_dtype: bool = False, scale: float = 0.0,
+                       keep_working_shard: bool = False, stream=None) -> None:
+    """zs_adamw_step_ex on the reduced gradient times grad_scale, a float32 device
+    tensor of one element (the clip factor norm_coef[1:] of zs_reduce_shard_norm or
+    zs_clip_coef), read when the kernel runs."""
+    torch = _torch()
+    contribs = list(contribs)
+    S = p.numel()
+    for name, t in (("p", p), ("m", m), ("v", v)):
+        _typed(t, name, torch.float32, S)
+    _dev(w_out, "w_out")
+    if _dtype_code(w_out) != ZS_BF16 or w_out.numel() != S:
+        raise ValueError("w_out must be bf16 bits with S elements")
+    code = _contributions(contribs, S)
+    _typed(grad_scale, "grad_scale", torch.float32, 1)
+    _same_device([p, m, v, w_out, grad_scale] + contribs, "zs_adamw_step_clip")
+    opts = zs_reduce_opts(int(replicas), 1 if round_to_reduce_dtype else 0, float(scale),
+                          ZS_W_KEEP if keep_working_shard else ZS_W_STREAM, 0)
+    _enqueue(load().zs_adamw_step_clip, p, stream, p.data_ptr(), m.data_ptr(), v.data_ptr(),
+             w_out.data_ptr(), S, _ptr_array(contribs), _groups(contribs, replicas),
+             ctypes.byref(opts), code, ctypes.byref(_hp(hp)), grad_scale.data_ptr())
+
+
+def _contributions(contribs, S) -> int:
+    """The element type of contributions of S elements each."""
+    if not contribs:
+        return ZS_F32
+    code = _dtype_code(contribs[0])
+    for i, c in enumerate(contribs):
+        _dev(c, f"contribs[{i}]")
+        if c.numel() != S or _dtype_code(c) != code:
+            raise ValueError("contributions must share one dtype and hold S elements")
+    return code
+
+
+# ---------------------------------------------------------- 8-bit matrices
+def zs_f8_layout(rows: int, cols: int, block_rows: int = 1) -> Tuple[int, int]:
+    """(bytes of codes, bytes of scales) of a matrix in 8-bit floating point."""
+    codes, scales = ctypes.c_int64(), ctypes.c_int64()
+    _check(load().zs_f8_layout(int(rows), int(cols), int(block_rows), ctypes.byref(codes),
+                               ctypes.byref(scales)))
+    return codes.value, scales.value
+
+
+class F8Matrix:
+    """A rows x cols matrix in block-scaled 8-bit floating point: its codes and
+    scale bytes (contiguous uint8 device tensors, in the layout of zs_f8_layout:
+    rows of 128 * ceil(cols / 128) codes and of 4 * ceil(cols / 512) scales, one
+    row of scales for each block_rows rows), their type (ZS_E4M3 or ZS_E5M2) and
+    block_rows (1 or 128)."""
+
+    def __init__(self, codes, scales, rows: int, cols: int, type: int = ZS_E4M3,
+                 block_rows: int = 1):
+        uint8 = _torch().uint8
+        n_codes, n_scales = zs_f8_layout(rows, cols, block_rows)
+        _typed(codes, "codes", uint8, n_codes)
+        _typed(scales, "scales", uint8, n_scales)
+        _same_device((codes, scales), "F8Matrix")
+        self.codes, self.scales = codes, scales
+        self.rows, self.cols, self.type, self.block_rows = int(rows), int(cols), int(type), int(block_rows)
+        self.device = codes.device
+        self._as_parameter_ = ctypes.pointer(zs_f8_matrix(
+            codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, self.type, self.block_rows))
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, type: int = ZS_E4M3, block_rows: int = 1,
+              device="cuda") -> "F8Matrix":
+        """A matrix to be written: its buffers are allocated, not filled."""
+        torch = _torch()
+        codes, scales = (torch.empty(n, dtype=torch.uint8, device=device)
+                         for n in zs_f8_layout(rows, cols, block_rows))
+        return cls(codes, scales, rows, cols, type, block_rows)
+
+
+def _matrix(t, what: str, rows: int = None, cols: int = None):
+    """A device matrix whose rows are contiguous: (its element type, row stride)."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device (cuda/HIP) tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a matrix with contiguous rows")
+    if rows is not None and tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{what} must be {rows} x {cols}")
+    # a matrix of one row has any stride, and may have one below its columns
+    return _dtype_code(t), t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _quantized_shape(out, out_t):
+    if out is None and out_t is None:
+        raise ValueError("need out, out_t or both")
+    return (out.rows, out.cols) if out is not None else (out_t.cols, out_t.rows)
+
+
+def zs_quantize_f8(x, out: F8Matrix = None, out_t: F8Matrix = None, stream=None) -> None:
+    """x (a bf16 or float32 matrix, its rows contiguous) to 8 bits: as it is (out),
+    transposed (out_t, whose blocks run along x's columns) or both from one read."""
+    code, ld = _matrix(x, "x", *_quantized_shape(out, out_t))
+    _same_device([x] + [o for o in (out, out_t) if o is not None], "zs_quantize_f8")
+    _enqueue(load().zs_quantize_f8, x, stream, x.data_ptr(), code, ld, out, out_t)
+
+
+def zs_gather_matrix_f8(shards: Sequence, offset: int, out: F8Matrix = None, out_t: F8Matrix = None,
+                        stream=None) -> None:
+    """Elements [offset, offset + rows * cols) of the unit that D shards (bf16 or
+    float32, S elements each) hold, as a rows x cols matrix in 8 bits: as it is
+    (out), transposed (out_t) or both."""
+    shards = list(shards)
+    if not shards:
+        raise ValueError("need at least one shard")
+    _quantized_shape(out, out_t)
+    S = shards[0].numel()
+    code = _contributions(shards, S)
+    _same_device(shards + [o for o in (out, out_t) if o is not None], "zs_gather_matrix_f8")
+    _enqueue(load().zs_gather_matrix_f8, shards[0], stream, _ptr_array(shards), len(shards), S, code,
+             int(offset), out, out_t)
+
+
+def zs_dequantize_f8(x: F8Matrix, out, stream=None) -> None:
+    """out (a bf16 or float32 matrix, its rows contiguous) = the values of x."""
+    code, ld = _matrix(out, "out", x.rows, x.cols)
+    _same_device((x, out), "zs_dequantize_f8")
+    _enqueue(load().zs_dequantize_f8, out, stream, x, code, out.data_ptr(), ld)
+
+
+def _f8_workspace(f, M, N, K) -> int:
+    n = ctypes.c_int64()
+    _check(f(int(M), int(N), int(K), ctypes.byref(n)))
+    return n.value
+
+
+def zs_matmul_f8_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of workspace of zs_matmul_f8 for a of M x K and b of N x K (may be 0)."""
+    return _f8_workspace(load().zs_matmul_f8_workspace, M, N, K)
+
+
+def zs_linear_f8_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of workspace of zs_linear_f8 for x of M x K and w of N x K."""
+    return _f8_workspace(load().zs_linear_f8_workspace, M, N, K)
+
+
+def zs_linear_f8_backward_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of workspace of zs_linear_f8_backward for dy of M x N and x of M x K."""
+    return _f8_workspace(load().zs_linear_f8_backward_workspace, M, N, K)
+
+
+def _workspace(workspace, need: int):
+    """Address of a workspace of at least `need` bytes."""
+    if need == 0 and workspace is None:
+        return None
+    if workspace is None:
+        raise ValueError(f"workspace must hold {need} bytes")
+    _typed(workspace, "workspace", _torch().uint8)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    return workspace.data_ptr()
+
+
+def zs_matmul_f8(a: F8Matrix, b: F8Matrix, c, accumulate: bool = False, workspace=None,
+                 stream=None) -> None:
+    """c (M x N, bf16 or float32, its rows contiguous) = a b^T for a of M x K and b of
+    N x K, added to c with accumulate. workspace: uint8 device tensor of
+    zs_matmul_f8_workspace(M, N, K) bytes, zeroed once; one for each of calls that may
+    run at the same time. In bf16 the sum is formed by the 8-bit matrix instructions,
+    in float32 in 32 bits throughout (slower): include/zs.h."""
+    code, ld = _matrix(c, "c", a.rows, b.rows)
+    if a.cols != b.cols:
+        raise ValueError("a and b must have the same number of columns")
+    ws = _workspace(workspace, zs_matmul_f8_workspace(a.rows, b.rows, a.cols))
+    _same_device([a, b, c] + ([] if workspace is None else [workspace]), "zs_matmul_f8")
+    _enqueue(load().zs_matmul_f8, c, stream, a, b, code, c.data_ptr(), ld, 1 if accumulate else 0, ws)
+
+
+def zs_linear_f8(x, w: F8Matrix, y, workspace, type: int = ZS_E4M3, stream=None) -> None:
+    """y (M x N, bf16 or float32) = Q(x) w^T: x (M x K, bf16 or float32) quantised to
+    8-bit codes of `type` with a scale for each 128 elements of a row, times the 8-bit
+    weights w (N x K). workspace: uint8 device tensor of zs_linear_f8_workspace(M, N, K)
+    bytes, zeroed once; one for each of calls that may run at the same time."""
+    code, ldx = _matrix(x, "x")
+    if x.shape[1] != w.cols:
+        raise ValueError(f"x must have {w.cols} columns")
+    M = x.shape[0]
+    y_code, ldy = _matrix(y, "y", M, w.rows)
+    ws = _workspace(workspace, zs_linear_f8_workspace(M, w.rows, w.cols))
+    _same_device((x, w, y, workspace), "zs_linear_f8")
+    _enqueue(load().zs_linear_f8, y, stream, x.data_ptr(), code, M, ldx, int(type), w, y_code,
+             y.data_ptr(), ldy, ws)
+
+
+def zs_linear_f8_backward(dy, x, w_t: F8Matrix, dx, dw, workspace, grad_type: int = ZS_E4M3,
+                          accumulate: bool = False, stream=None) -> None:
+    """The gradients of zs_linear_f8 from dy (M x N): dx (M x K) = Q(dy) w with w given
+    transposed (w_t, K x N), and dw (N x K, usually a view into a unit's flat gradient) =
+    Q(dy^T) Q(x^T)^T, added to dw with accumulate. dx (with it w_t) or dw (with it x) may
+    be None. grad_type: of dy's codes. dy and x: bf16 or both float32."""
+    code, lddy = _matrix(dy, "dy")
+    M, N = dy.shape
+    if dx is None and dw is None:
+        raise ValueError("need dx, dw or both")
+    K = dx.shape[1] if dx is not None else dw.shape[1]
+    args = dict(x=(None, 0), dx=(ZS_BF16, None, 0), dw=(ZS_BF16, None, 0))
+    used = [dy, workspace]
+    if dx is not None:
+        dx_code, ld = _matrix(dx, "dx", M, K)
+        if w_t is None or (w_t.rows, w_t.cols) != (K, N):
+            raise ValueError(f"w_t must be {K} x {N}")
+        args["dx"] = (dx_code, dx.data_ptr(), ld)
+        used += [dx, w_t]
+    if dw is not None:
+        dw_code, ld = _matrix(dw, "dw", N, K)
+        x_code, ldx = _matrix(x, "x", M, K)
+        if x_code != code:
+            raise TypeError("dy and x must share one element type")
+        args["dw"] = (dw_code, dw.data_ptr(), ld)
+        args["x"] = (x.data_ptr(), ldx)
+        used += [x, dw]
+    ws = _workspace(workspace, zs_linear_f8_backward_workspace(M, N, K))
+    _same_device(used, "zs_linear_f8_backward")
+    _enqueue(load().zs_linear_f8_backward, dy, stream, dy.data_ptr(), lddy, *args["x"], code, M, N, K,
+             int(grad_type), w_t if dx is not None else None, *args["dx"], *args["dw"],
+             1 if accumulate else 0, ws)
 
 
 ZS_PROBE_READ, ZS_PROBE_WRITE, ZS_PROBE_COPY, ZS_PROBE_TRIAD = 0, 1, 2, 3

@@ -5,13 +5,15 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzs.so")
 SOURCES = ("zs_api.cpp", "zs_pipeline.cpp", "zs_ckpt.cpp", "zs_host.cpp", "zs_step.hip",
            "zs_move.hip", "zs_diag.hip", "zs_static.hip", "zs_multi.cpp", "zs_multi.hip",
-           "zs_mx4.hip")
+           "zs_mx4.hip", "zs_f8.cpp", "zs_f8_quant.hip", "zs_f8_gemm.hip")
 
 # -ffp-contract=off: no fused multiply-add in the step's arithmetic;
 # correctly rounded fp32 divide and sqrt (the HIP default, stated);
@@ -32,16 +34,28 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the HIP toolchain is required to build libzs")
 
 
-def build(out: str = LIB, defines: tuple = (), verbose: bool = False) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + FLAGS + ["-D" + d for d in defines] + ["-x", "hip"] + srcs + ["-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("hipcc failed building %s" % out)
+    return subprocess.run(cmd, capture_output=True, text=True)
+
+
+def build(out: str = LIB, defines: tuple = (), verbose: bool = False) -> str:
+    """Compile every source, a few at a time, and link them."""
+    tmp = out + ".tmp%d" % os.getpid()
+    flags = [f for f in FLAGS if f != "-shared"] + ["-D" + d for d in defines]
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, s + ".o") for s in SOURCES]
+        cmds = [[hipcc()] + flags + ["-c", "-x", "hip", os.path.join(CSRC, s), "-o", o]
+                for s, o in zip(SOURCES, objects)]
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            runs = list(pool.map(lambda c: _run(c, verbose), cmds))
+        if all(r.returncode == 0 for r in runs):
+            runs.append(_run([hipcc()] + FLAGS + objects + ["-o", tmp], verbose))
+    for r in runs:
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("hipcc failed building %s" % out)
     os.replace(tmp, out)
     return out
 

@@ -181,7 +181,7 @@ using namespace zs;
 
 ZS_EXPORT const char* zs_last_error(void) { return g_last_error.c_str(); }
 
-ZS_EXPORT int32_t zs_abi_version(void) { return 202; }
+ZS_EXPORT int32_t zs_abi_version(void) { return 203; }
 
 ZS_EXPORT zs_status zs_unit_layout(const int64_t* numels, int32_t T, int32_t D,
                                    int64_t* offsets_out, int64_t* n_out, int64_t* n_pad_out,
@@ -296,7 +296,7 @@ zs_status check_groups(const char* who, int32_t nd, const zs_reduce_opts* opts, 
 
 zs_status reduce_common(const char* who, const void* const* contribs, int32_t nd,
                         const zs_reduce_opts* opts, int32_t dtype, int64_t S, float* grad_out,
-                        hipStream_t stream) {
+                        hipStream_t stream, const NormJob* norm = nullptr) {
     const int es = elem_size(dtype);
     if (es == 0) return fail(ZS_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
     int R;
@@ -306,6 +306,10 @@ zs_status reduce_common(const char* who, const void* const* contribs, int32_t nd
     zs_status st = check_groups(who, nd, opts, &R, &rnd, &inv_n, &keep_w);
     if (st != ZS_OK) return st;
     if (!size_ok(S, 4)) return fail(ZS_EINVAL, "%s: S = %lld out of range", who, (long long)S);
+    if (S == 0 && norm != nullptr)  // the sum is written all the same
+        return hip_status(launch_reduce(PtrPack{}, nd, R, rnd, dtype, 0, inv_n, nullptr, true,
+                                        stream, norm),
+                          who);
     if (S == 0) return ok();
     if (grad_out == nullptr) return fail(ZS_EINVAL, "%s: grad_out is NULL", who);
     if (!aligned(grad_out, 4)) return fail(ZS_EINVAL, "%s: grad_out not 4-byte aligned", who);
@@ -320,13 +324,28 @@ zs_status reduce_common(const char* who, const void* const* contribs, int32_t nd
             return fail(ZS_EALIAS, "%s: grad_out overlaps contribution %d", who, k);
         al = al && aligned(cp.p[k], 16);
     }
-    return hip_status(launch_reduce(cp, nd, R, rnd, dtype, S, inv_n, grad_out, al, stream), who);
+    if (norm != nullptr) {
+        const Range side[3] = {range_of(norm->sumsq, 1, 8),
+                               range_of(norm->norm_coef, norm->norm_coef ? 2 : 0, 4),
+                               range_of(norm->ws, ZS_NORM_WORKSPACE, 1)};
+        for (const Range& o : side) {
+            if (overlap(out, o))
+                return fail(ZS_EALIAS, "%s: grad_out overlaps sumsq, norm_coef or workspace", who);
+            for (int k = 0; k < n; ++k)
+                if (overlap(o, range_of(cp.p[k], S, es)))
+                    return fail(ZS_EALIAS, "%s: sumsq, norm_coef or workspace overlaps contribution %d",
+                                who, k);
+        }
+    }
+    return hip_status(launch_reduce(cp, nd, R, rnd, dtype, S, inv_n, grad_out, al, stream, norm),
+                      who);
 }
 
 zs_status adamw_common(const char* who, float* p, float* m, float* v, uint16_t* w_out, int64_t S,
                        const void* const* contribs, int32_t nd, const zs_reduce_opts* opts,
                        int32_t dtype, const zs_adamw_hp* hp, hipStream_t stream,
-                       hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr) {
+                       hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr,
+                       const float* grad_scale = nullptr) {
     const int es = elem_size(dtype);
     if (es == 0) return fail(ZS_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
     int R;
@@ -361,11 +380,15 @@ zs_status adamw_common(const char* who, float* p, float* m, float* v, uint16_t* 
                 return fail(ZS_EALIAS, "%s: contribution %d overlaps %s", who, k, names[a]);
         al = al && aligned(cp.p[k], 16);
     }
+    for (int a = 0; a < 4; ++a)
+        if (grad_scale != nullptr && overlap(range_of(grad_scale, 1, 4), rs[a]))
+            return fail(ZS_EALIAS, "%s: grad_scale lies in %s", who, names[a]);
     AdamConsts k = adam_consts(*hp, n);
     k.inv_n = inv_n;
     k.keep_w = keep_w;
     return hip_status(
-        launch_adamw(p, m, v, w_out, S, cp, nd, R, rnd, dtype, k, al, stream, ev_start, ev_stop),
+        launch_adamw(p, m, v, w_out, S, cp, nd, R, rnd, dtype, k, al, stream, ev_start, ev_stop,
+                     grad_scale),
         who);
 }
 
@@ -407,6 +430,39 @@ ZS_EXPORT zs_status zs_adamw_step_timed(float* p, float* m, float* v, uint16_t* 
         return fail(ZS_EINVAL, "%s: start or stop event is NULL", who);
     if (start == stop) return fail(ZS_EINVAL, "%s: start and stop are the same event", who);
     return adamw_common(who, p, m, v, w_out, S, contribs, D, opts, dtype, hp, stream, start, stop);
+}
+
+ZS_EXPORT zs_status zs_reduce_shard_norm(const void* const* contribs, int32_t D,
+                                         const zs_reduce_opts* opts, int32_t dtype, int64_t S,
+                                         float* grad_out, double max_norm, double* sumsq,
+                                         float* norm_coef, int32_t accumulate, void* workspace,
+                                         hipStream_t stream) {
+    const char* who = "zs_reduce_shard_norm";
+    if (!(max_norm > 0.0)) return fail(ZS_EINVAL, "%s: max_norm must be > 0", who);
+    if (accumulate != 0 && accumulate != 1)
+        return fail(ZS_EINVAL, "%s: accumulate must be 0 or 1", who);
+    if (!sumsq || !workspace) return fail(ZS_EINVAL, "%s: sumsq or workspace is NULL", who);
+    if (!aligned(sumsq, 8) || !aligned(norm_coef, 4) || !aligned(workspace, 16))
+        return fail(ZS_EINVAL, "%s: sumsq, norm_coef or workspace misaligned", who);
+    const Range rs = range_of(sumsq, 1, 8), rn = range_of(norm_coef, norm_coef ? 2 : 0, 4),
+                rw = range_of(workspace, ZS_NORM_WORKSPACE, 1);
+    if (overlap(rs, rn) || overlap(rs, rw) || overlap(rn, rw))
+        return fail(ZS_EALIAS, "%s: sumsq, norm_coef and workspace overlap", who);
+    const NormJob norm{max_norm, sumsq, norm_coef, accumulate,
+                       static_cast<NormWorkspace*>(workspace)};
+    return reduce_common(who, contribs, D, opts, dtype, S, grad_out, stream, &norm);
+}
+
+ZS_EXPORT zs_status zs_adamw_step_clip(float* p, float* m, float* v, uint16_t* w_out, int64_t S,
+                                       const void* const* contribs, int32_t D,
+                                       const zs_reduce_opts* opts, int32_t dtype,
+                                       const zs_adamw_hp* hp, const float* grad_scale,
+                                       hipStream_t stream) {
+    const char* who = "zs_adamw_step_clip";
+    if (grad_scale == nullptr || !aligned(grad_scale, 4))
+        return fail(ZS_EINVAL, "%s: grad_scale is NULL or misaligned", who);
+    return adamw_common(who, p, m, v, w_out, S, contribs, D, opts, dtype, hp, stream, nullptr,
+                        nullptr, grad_scale);
 }
 
 ZS_EXPORT zs_status zs_gather_unit(const void* const* shards, int32_t D, int64_t S,

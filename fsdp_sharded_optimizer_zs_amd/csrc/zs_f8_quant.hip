@@ -1,0 +1,513 @@
+// Block-scaled 8-bit matrices for gfx950: quantisation of a bf16 or fp32 matrix (as it is
+// and transposed, from one read), the same of a matrix that lies in a unit's shards, and
+// the values that codes stand for.
+//
+// All stream once over their data. A workgroup of 4 wavefronts takes a 128 x 128 tile, so
+// that the blocks of both forms are whole in it. Lane l of wavefront w holds 8 columns
+// (from 8 (l % 16) on) of the rows 64 h + 16 w + 4 (l / 16) + i, h < 2, i < 4: 16 lanes cover
+// 256 bytes of a bf16 row, a row's block of 128 is the 16 lanes of a DPP row, and the 4
+// rows i of a column are one word of transposed codes. Those words are exchanged through
+// LDS (16 KiB) so that the transpose leaves in 16-byte pieces of whole 128-byte runs too.
+
+#include "zs_f8.h"
+#include "zs_math.h"
+
+#pragma clang fp contract(off)
+
+namespace zs {
+namespace {
+
+constexpr int kThreads = kBlockThreads;
+constexpr int kT = kF8Block;  // side of a tile
+
+#define ZS_GLOBAL __attribute__((address_space(1)))
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// vectors at element alignment: a matrix may start at any element of a unit
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+typedef ZS_GLOBAL f32x4_u g_f32x4;
+typedef ZS_GLOBAL u32x4_u g_u32x4;
+typedef ZS_GLOBAL u32x4 g_u32x4a;
+typedef ZS_GLOBAL u32x2 g_u32x2a;
+typedef ZS_GLOBAL uint32_t g_u32a;
+typedef ZS_GLOBAL uint8_t g_u8;
+typedef ZS_GLOBAL uint16_t g_u16;
+typedef ZS_GLOBAL float g_f32;
+
+template <typename G, typename P>
+__device__ __forceinline__ G* global(P* p) {
+    return reinterpret_cast<G*>(reinterpret_cast<uintptr_t>(p));
+}
+
+// 8 neighbouring elements of a row.
+template <int DT>
+struct Eight;
+template <>
+struct Eight<ZS_BF16> {
+    uint32_t w[4];  // pairs
+};
+template <>
+struct Eight<ZS_F32> {
+    float f[8];
+};
+
+template <int DT>
+__device__ __forceinline__ Eight<DT> load8(const void* base, int64_t i) {
+    Eight<DT> x;
+    if constexpr (DT == ZS_BF16) {
+        const u32x4 h = __builtin_nontemporal_load(
+            reinterpret_cast<const g_u32x4*>(global<const g_u16>(base) + i));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.w[k] = h[k];
+    } else {
+        const g_f32x4* p = reinterpret_cast<const g_f32x4*>(global<const g_f32>(base) + i);
+        const f32x4 a = __builtin_nontemporal_load(p), b = __builtin_nontemporal_load(p + 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.f[k] = a[k], x.f[4 + k] = b[k];
+    }
+    return x;
+}
+template <int DT>
+__device__ __forceinline__ void load1(const void* base, int64_t i, int e, Eight<DT>& x) {
+    if constexpr (DT == ZS_BF16)
+        x.w[e / 2] |= uint32_t(global<const g_u16>(base)[i]) << (16 * (e & 1));
+    else
+        x.f[e] = global<const g_f32>(base)[i];
+}
+
+// A matrix in memory, row r from element r * ldx on.
+struct Strided {
+    const void* x;
+    int64_t ldx;
+    template <int DT>
+    __device__ __forceinline__ Eight<DT> get(int64_t r, int64_t c, int live) const {
+        if (live >= 8) return load8<DT>(x, r * ldx + c);
+        Eight<DT> v{};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < live) load1<DT>(x, r * ldx + c + e, e, v);
+        return v;
+    }
+};
+
+// A matrix in a unit's shards: the shard of an element by a product with 1 / S in fp64
+// (elements are below 2^53, so that it is off by at most one, which is put right).
+struct Sharded {
+    const F8Shards* s;
+    int64_t cols;
+    __device__ __forceinline__ int shard_of(int64_t f, int64_t* at) const {
+        int r = int(double(f) * s->inv_s);
+        int64_t i = f - int64_t(r) * s->S;
+        if (i < 0) --r, i += s->S;
+        if (i >= s->S) ++r, i -= s->S;
+        *at = i;
+        return r;
+    }
+    template <int DT>
+    __device__ __forceinline__ Eight<DT> get(int64_t r, int64_t c, int live) const {
+        int64_t i;
+        int k = shard_of(s->offset + r * cols + c, &i);
+        if (live >= 8 && i + 8 <= s->S) return load8<DT>(s->shards.p[k], i);
+        Eight<DT> v{};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e < live) load1<DT>(s->shards.p[k], i, e, v);
+            // every shard ends at a multiple of S: the next element is the next one's first
+            if (++i >= s->S) {
+                i = 0;
+                if (e + 1 < live) ++k;
+            }
+        }
+        return v;
+    }
+};
+
+// Largest magnitudes as fp32 bits (unsigned numbers: infinity and NaN above every number).
+__device__ __forceinline__ uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 mags(uint32_t w) {
+    return __builtin_bit_cast(u16x2, w & 0x7fff7fffu);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t top_bits(const Eight<DT>& x) {
+    if constexpr (DT == ZS_BF16) {
+        u16x2 u = __builtin_elementwise_max(mags(x.w[0]), mags(x.w[1]));
+        u = __builtin_elementwise_max(u, __builtin_elementwise_max(mags(x.w[2]), mags(x.w[3])));
+        return uint32_t(u[0] > u[1] ? u[0] : u[1]) << 16;
+    } else {
+        uint32_t u = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u = max_u(u, __float_as_uint(x.f[k]) & 0x7fffffffu);
+        return u;
+    }
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with(uint32_t u) {
+    return max_u(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), CTRL, 0xf, 0xf, true)));
+}
+// Over the 16 lanes of a DPP row.
+__device__ __forceinline__ uint32_t row_max(uint32_t u) {
+    u = max_with<0xb1>(u);     // quad_perm 1,0,3,2
+    u = max_with<0x4e>(u);     // quad_perm 2,3,0,1
+    u = max_with<0x141>(u);    // row_half_mirror
+    return max_with<0x140>(u); // row_mirror
+}
+// Over lanes l % 16 = const.
+__device__ __forceinline__ uint32_t col_max(uint32_t u) {
+    u = max_u(u, __shfl_xor(u, 16, 64));
+    return max_u(u, __shfl_xor(u, 32, 64));
+}
+
+__device__ __forceinline__ int scale_of(uint32_t u, int type) {
+    const int s = int((u + 0x1fffffu) >> 23) - (type == ZS_E4M3 ? 8 : 15);
+    return u >= 0x7f800000u ? 255 : (s > 1 ? s : 1);
+}
+
+// Two codes into half `HI` of a word: gfx950 converts with the scale in one instruction.
+// Blocks of s = 1 hold magnitudes that may be subnormal and are scaled by ldexp first.
+template <int TYPE, bool HI>
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, float a, float b, float two) {
+    const s16x2 old = __builtin_bit_cast(s16x2, w);
+    if constexpr (TYPE == ZS_E4M3)
+        return __builtin_bit_cast(uint32_t,
+                                  __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(old, a, b, two, HI));
+    else
+        return __builtin_bit_cast(uint32_t,
+                                  __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(old, a, b, two, HI));
+}
+template <int TYPE, bool HI>
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, uint32_t pair, float two) {
+    const s16x2 old = __builtin_bit_cast(s16x2, w);
+    const bf16x2 h = __builtin_bit_cast(bf16x2, pair);
+    if constexpr (TYPE == ZS_E4M3)
+        return __builtin_bit_cast(uint32_t,
+                                  __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(old, h, two, HI));
+    else
+        return __builtin_bit_cast(uint32_t,
+                                  __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(old, h, two, HI));
+}
+
+// 4 codes of values given as pairs of bf16 or as floats, under scale byte s.
+template <int TYPE>
+__device__ __forceinline__ uint32_t four_codes(float a, float b, float c, float d, int s) {
+    if (s == 255) return 0;
+    float two = __uint_as_float(uint32_t(s) << 23);
+    if (s == 1) {
+        a = __builtin_ldexpf(a, 126), b = __builtin_ldexpf(b, 126);
+        c = __builtin_ldexpf(c, 126), d = __builtin_ldexpf(d, 126);
+        two = 1.0f;
+    }
+    return two_codes<TYPE, true>(two_codes<TYPE, false>(0u, a, b, two), c, d, two);
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t four_codes(uint32_t ab, uint32_t cd, int s) {
+    if (s <= 1 || s == 255)
+        return four_codes<TYPE>(bf16_lo(ab), bf16_hi(ab), bf16_lo(cd), bf16_hi(cd), s);
+    const float two = __uint_as_float(uint32_t(s) << 23);
+    return two_codes<TYPE, true>(two_codes<TYPE, false>(0u, ab, two), cd, two);
+}
+
+// The scale byte of block `block` of row `row`, and, beside the last one, the bytes 1 that
+// fill the row: lane k < 4 writes byte block + k.
+__device__ __forceinline__ void put_scale(const F8Out& o, int64_t row, int64_t block,
+                                          int64_t blocks, int k, int s) {
+    if (k == 0 || (block + 1 == blocks && block + k < o.lds))
+        global<g_u8>(o.scales)[row * o.lds + block + k] = uint8_t(k == 0 ? s : 1);
+}
+
+struct Shared {
+    uint32_t codes[kT * kT / 4];
+    uint32_t top[4][kT];
+    uint32_t whole[4];
+};
+
+// One tile. BR = 1: a block for each row (column, transposed) of the tile, BR = 128: one.
+template <int DT, int BR, class Src>
+__device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int64_t tr,
+                                           int64_t tc, Shared& sh) {
+    const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
+    const int cg = lane & 15, rq = lane >> 4;
+    const int64_t r0 = tr * kT, c = tc * kT + 8 * cg;
+    const int64_t blocks_c = f8_ceil(q.cols, kT), blocks_r = f8_ceil(q.rows, kT);
+    const int live = q.cols - c >= 8 ? 8 : (q.cols > c ? int(q.cols - c) : 0);
+    Eight<DT> x[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = r0 + 64 * h + 16 * wave + 4 * rq + i;
+            if (r < q.rows && live > 0) x[h][i] = src.template get<DT>(r, c, live);
+            else x[h][i] = Eight<DT>{};
+        }
+    uint32_t whole = 0;
+    if constexpr (BR == 128) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) whole = max_u(whole, top_bits<DT>(x[h][i]));
+        whole = col_max(row_max(whole));
+        if (lane == 0) sh.whole[wave] = whole;
+        __syncthreads();
+        whole = max_u(max_u(sh.whole[0], sh.whole[1]), max_u(sh.whole[2], sh.whole[3]));
+    }
+    if (q.out.codes != nullptr) {
+        const int type = q.out.type;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = r0 + 64 * h + 16 * wave + 4 * rq + i;
+                const int s = scale_of(BR == 128 ? whole : row_max(top_bits<DT>(x[h][i])), type);
+                u32x2 w;
+                const Eight<DT>& v = x[h][i];
+                if constexpr (DT == ZS_BF16) {
+                    if (type == ZS_E4M3)
+                        w = u32x2{four_codes<ZS_E4M3>(v.w[0], v.w[1], s),
+                                  four_codes<ZS_E4M3>(v.w[2], v.w[3], s)};
+                    else
+                        w = u32x2{four_codes<ZS_E5M2>(v.w[0], v.w[1], s),
+                                  four_codes<ZS_E5M2>(v.w[2], v.w[3], s)};
+                } else {
+                    if (type == ZS_E4M3)
+                        w = u32x2{four_codes<ZS_E4M3>(v.f[0], v.f[1], v.f[2], v.f[3], s),
+                                  four_codes<ZS_E4M3>(v.f[4], v.f[5], v.f[6], v.f[7], s)};
+                    else
+                        w = u32x2{four_codes<ZS_E5M2>(v.f[0], v.f[1], v.f[2], v.f[3], s),
+                                  four_codes<ZS_E5M2>(v.f[4], v.f[5], v.f[6], v.f[7], s)};
+                }
+                if (r < q.rows) {
+                    *global<g_u32x2a>(q.out.codes + r * q.out.ld + c) = w;
+                    if (BR == 1 && cg < 4) put_scale(q.out, r, tc, blocks_c, cg, s);
+                }
+            }
+        if (BR == 128 && threadIdx.x < 4)
+            put_scale(q.out, tr, tc, blocks_c, int(threadIdx.x), scale_of(whole, type));
+    }
+    if (q.out_t.codes == nullptr) return;
+    const int type = q.out_t.type;
+    int st[8];
+    if constexpr (BR == 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t u = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (DT == ZS_BF16)
+                        u = max_u(u, (x[h][i].w[e / 2] << (e & 1 ? 0 : 16)) & 0x7fff0000u);
+                    else
+                        u = max_u(u, __float_as_uint(x[h][i].f[e]) & 0x7fffffffu);
+                }
+            u = col_max(u);
+            if (rq == 0) sh.top[wave][8 * cg + e] = u;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int k = 8 * cg + e;
+            st[e] = scale_of(max_u(max_u(sh.top[0][k], sh.top[1][k]),
+                                   max_u(sh.top[2][k], sh.top[3][k])), type);
+        }
+        if (wave == 0 && rq == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (e < live) put_scale(q.out_t, c + e, tr, blocks_r, k, st[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) st[e] = scale_of(whole, type);
+        if (threadIdx.x < 4)
+            put_scale(q.out_t, tc, tr, blocks_r, int(threadIdx.x), scale_of(whole, type));
+    }
+    // word (column, 4 rows): the 16-byte pieces of a column's 128 are permuted by its number
+    // over 8, so that the 16 columns that a wavefront writes at once fall on other banks
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t w;
+            if constexpr (DT == ZS_BF16) {
+                const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
+                const uint32_t ab = __builtin_amdgcn_perm(x[h][1].w[e / 2], x[h][0].w[e / 2], sel);
+                const uint32_t cd = __builtin_amdgcn_perm(x[h][3].w[e / 2], x[h][2].w[e / 2], sel);
+                w = type == ZS_E4M3 ? four_codes<ZS_E4M3>(ab, cd, st[e])
+                                    : four_codes<ZS_E5M2>(ab, cd, st[e]);
+            } else {
+                const float a = x[h][0].f[e], b = x[h][1].f[e], d = x[h][2].f[e], f = x[h][3].f[e];
+                w = type == ZS_E4M3 ? four_codes<ZS_E4M3>(a, b, d, f, st[e])
+                                    : four_codes<ZS_E5M2>(a, b, d, f, st[e]);
+            }
+            const int piece = (4 * h + wave) ^ (cg & 7);
+            sh.codes[(8 * cg + e) * 32 + 4 * piece + rq] = w;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int col = 32 * k + int(threadIdx.x) / 8, piece = int(threadIdx.x) % 8;
+        if (tc * kT + col < q.cols) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(
+                &sh.codes[col * 32 + 4 * (piece ^ ((col >> 3) & 7))]);
+            *global<g_u32x4a>(q.out_t.codes + (tc * kT + col) * q.out_t.ld + r0 + 16 * piece) = w;
+        }
+    }
+}
+
+template <int BR>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(F8Quant q) {
+    __shared__ Shared sh;
+    const uint32_t tiles_c = uint32_t(f8_ceil(q.cols, kT));
+    const uint32_t tiles = tiles_c * uint32_t(f8_ceil(q.rows, kT));  // checked: below 2^31
+    const Strided src{q.x, q.ldx};
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        if (q.dtype == ZS_BF16) quant_tile<ZS_BF16, BR>(q, src, t / tiles_c, t % tiles_c, sh);
+        else quant_tile<ZS_F32, BR>(q, src, t / tiles_c, t % tiles_c, sh);
+        __syncthreads();
+    }
+}
+
+template <int DT, int BR>
+__global__ __launch_bounds__(kThreads) void gather_kernel(F8Quant q, F8Shards s) {
+    __shared__ Shared sh;
+    const uint32_t tiles_c = uint32_t(f8_ceil(q.cols, kT));
+    const uint32_t tiles = tiles_c * uint32_t(f8_ceil(q.rows, kT));  // checked: below 2^31
+    const Sharded src{&s, q.cols};
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        quant_tile<DT, BR>(q, src, t / tiles_c, t % tiles_c, sh);
+        __syncthreads();
+    }
+}
+
+// Value of a code under scale byte s, as fp32.
+template <int TYPE>
+__device__ __forceinline__ f32x2 two_values(uint32_t w, bool hi) {
+    if constexpr (TYPE == ZS_E4M3)
+        return hi ? __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true)
+                  : __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false);
+    else
+        return hi ? __builtin_amdgcn_cvt_pk_f32_bf8(int(w), true)
+                  : __builtin_amdgcn_cvt_pk_f32_bf8(int(w), false);
+}
+
+// Tiles of 64 x 128; a lane takes the codes of 16 bytes of values (8 bf16 or 4 fp32), so
+// that a wavefront's store covers whole runs of its rows.
+template <int TYPE, int DT>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int shift,
+    int64_t rows, int64_t cols, int64_t ld, int64_t lds, void* __restrict__ out, int64_t ldo) {
+    constexpr int E = DT == ZS_BF16 ? 8 : 4, kLanes = kT / E, kRows = kThreads / kLanes;
+    constexpr int kTileRows = 64;
+    const uint32_t tiles_c = uint32_t(f8_ceil(cols, kT));
+    const uint32_t tiles = tiles_c * uint32_t(f8_ceil(rows, kTileRows));
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t tr = t / tiles_c, tc = t % tiles_c;
+        const int64_t c = tc * kT + E * (int(threadIdx.x) % kLanes);
+        uint32_t w[kTileRows / kRows][E / 4];
+        int s[kTileRows / kRows];
+#pragma unroll
+        for (int k = 0; k < kTileRows / kRows; ++k) {
+            const int64_t r = tr * kTileRows + k * kRows + int(threadIdx.x) / kLanes;
+            if (r >= rows) continue;
+            const g_u32a* p = global<const g_u32a>(codes + r * ld + c);
+#pragma unroll
+            for (int j = 0; j < E / 4; ++j) w[k][j] = p[j];
+            s[k] = global<const g_u8>(scales)[(r >> shift) * lds + tc];
+        }
+#pragma unroll
+        for (int k = 0; k < kTileRows / kRows; ++k) {
+            const int64_t r = tr * kTileRows + k * kRows + int(threadIdx.x) / kLanes;
+            if (r >= rows || c >= cols) continue;
+            float y[E];
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) {
+                const f32x2 v = two_values<TYPE>(w[k][j / 2], j & 1);
+                y[2 * j] = v[0], y[2 * j + 1] = v[1];
+            }
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                y[j] = __builtin_ldexpf(y[j], s[k] - 127);
+                if (s[k] == 255) y[j] = __uint_as_float(0x7fc00000u);
+            }
+            const int64_t at = r * ldo + c;
+            if (c + E <= cols) {
+                if constexpr (DT == ZS_BF16)
+                    __builtin_nontemporal_store(
+                        u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                              pack_bf16(y[6], y[7])},
+                        reinterpret_cast<g_u32x4*>(global<g_u16>(out) + at));
+                else
+                    __builtin_nontemporal_store(
+                        f32x4{y[0], y[1], y[2], y[3]},
+                        reinterpret_cast<g_f32x4*>(global<g_f32>(out) + at));
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    if (c + j >= cols) continue;
+                    if constexpr (DT == ZS_BF16)
+                        global<g_u16>(out)[at + j] = uint16_t(pack_bf16(y[j], 0.0f));
+                    else
+                        global<g_f32>(out)[at + j] = y[j];
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_quantize_f8(const F8Quant& q, int block_rows, hipStream_t stream) {
+    const dim3 grid(unsigned(f8_tile_grid(f8_tiles(q.rows, q.cols))));
+    if (block_rows == 1)
+        hipLaunchKernelGGL((quantize_kernel<1>), grid, dim3(kThreads), 0, stream, q);
+    else
+        hipLaunchKernelGGL((quantize_kernel<128>), grid, dim3(kThreads), 0, stream, q);
+    return hipGetLastError();
+}
+
+hipError_t launch_gather_f8(const F8Quant& q, const F8Shards& src, int block_rows,
+                            hipStream_t stream) {
+    const dim3 grid(unsigned(f8_tile_grid(f8_tiles(q.rows, q.cols))));
+    if (q.dtype == ZS_BF16) {
+        if (block_rows == 1)
+            hipLaunchKernelGGL((gather_kernel<ZS_BF16, 1>), grid, dim3(kThreads), 0, stream, q, src);
+        else
+            hipLaunchKernelGGL((gather_kernel<ZS_BF16, 128>), grid, dim3(kThreads), 0, stream, q,
+                               src);
+    } else {
+        if (block_rows == 1)
+            hipLaunchKernelGGL((gather_kernel<ZS_F32, 1>), grid, dim3(kThreads), 0, stream, q, src);
+        else
+            hipLaunchKernelGGL((gather_kernel<ZS_F32, 128>), grid, dim3(kThreads), 0, stream, q,
+                               src);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_dequantize_f8(const uint8_t* codes, const uint8_t* scales, int block_rows,
+                                int64_t rows, int64_t cols, int type, int dtype, void* out,
+                                int64_t ldo, hipStream_t stream) {
+    const int64_t ld = f8_ld(cols), lds = f8_lds(cols);
+    const int shift = block_rows == 1 ? 0 : 7;
+    const dim3 grid(unsigned(f8_tile_grid(f8_ceil(rows, 64) * f8_ceil(cols, kT))));
+    const auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, codes, scales, shift, rows,
+                           cols, ld, lds, out, ldo);
+    };
+    if (type == ZS_E4M3) {
+        if (dtype == ZS_BF16) go(dequantize_kernel<ZS_E4M3, ZS_BF16>);
+        else go(dequantize_kernel<ZS_E4M3, ZS_F32>);
+    } else {
+        if (dtype == ZS_BF16) go(dequantize_kernel<ZS_E5M2, ZS_BF16>);
+        else go(dequantize_kernel<ZS_E5M2, ZS_F32>);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace zs

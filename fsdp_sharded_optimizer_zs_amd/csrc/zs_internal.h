@@ -109,9 +109,20 @@ const DeviceInfo& device_info();
 hipError_t launch_adamw(float* p, float* m, float* v, uint16_t* w, int64_t S,
                         const PtrPack& contribs, int nd, int R, bool rnd, int dtype,
                         const AdamConsts& k, bool aligned, hipStream_t stream,
-                        hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr);
+                        hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr,
+                        const float* grad_scale = nullptr);
+// With norm, the reduce also sums the squares of what it writes.
+struct NormWorkspace;
+struct NormJob {
+    double max_norm;
+    double* sumsq;
+    float* norm_coef;  // or nullptr
+    int accumulate;
+    NormWorkspace* ws;
+};
 hipError_t launch_reduce(const PtrPack& contribs, int nd, int R, bool rnd, int dtype, int64_t S,
-                         float inv_n, float* out, bool aligned, hipStream_t stream);
+                         float inv_n, float* out, bool aligned, hipStream_t stream,
+                         const NormJob* norm = nullptr);
 hipError_t launch_pack(const zs_tensor_ref* d_table, int T, int64_t N, int es,
                        int D, const PtrPack& shards, int64_t S, hipStream_t stream);
 // in_place: bit r set when shard r already sits in its slot (not copied).

@@ -11,6 +11,7 @@
 
 #include "zs_multi.h"
 #include "zs_math.h"
+#include "zs_norm.h"
 
 #pragma clang fp contract(off)
 
@@ -679,51 +680,6 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const uint8_t* __rest
 // counts itself in at the end, and additions to one address take about 12 ns apiece.
 constexpr int kNormWaves = kNormThreads / 64;
 
-// Sum over a workgroup of the norm, in a fixed order, valid in thread 0.
-__device__ __forceinline__ double block_sum(double x, double* slot) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_down(x, d, 64);
-    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = x;
-    __syncthreads();
-    double s = 0.0;
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int w = 0; w < kNormWaves; ++w) s += slot[w];
-    }
-    return s;
-}
-
-__device__ __forceinline__ void write_clip(double sum, double max_norm, float* norm_coef) {
-    const double norm = __builtin_sqrt(sum);
-    norm_coef[0] = float(norm);
-    float c = 1.0f;
-    if (!__builtin_isinf(max_norm)) {
-        const double d = max_norm / (norm + 1e-6);
-        c = d >= 1.0 ? 1.0f : float(d);
-    }
-    norm_coef[1] = c;
-}
-
-// Counts this workgroup in; true for the last one of the grid. Workgroups count in
-// groups (b mod kNormGroups), the last of each group for the group, so that the counts on
-// one address are few; each count is put back to 0 by the last that adds to it.
-__device__ __forceinline__ uint32_t count(uint32_t* n) {
-    return __hip_atomic_fetch_add(n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
-}
-__device__ __forceinline__ void clear(uint32_t* n) {
-    __hip_atomic_store(n, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ bool arrive(NormWorkspace* ws) {
-    const unsigned group = blockIdx.x % kNormGroups;
-    const unsigned groups = gridDim.x < kNormGroups ? gridDim.x : kNormGroups;
-    const unsigned members = (gridDim.x - group + kNormGroups - 1) / kNormGroups;
-    if (count(&ws->arrived[group].n) != members) return false;
-    clear(&ws->arrived[group].n);
-    if (count(&ws->groups.n) != groups) return false;
-    clear(&ws->groups.n);
-    return true;
-}
-
 // Sum of squares, in fp64, where the product of two fp32 numbers is exact and no square
 // over- or underflows. Workgroup b takes kNormChunks chunks at a time; the one that
 // arrives last adds all partial sums, in their order, and leaves the count at 0 for the
@@ -766,7 +722,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] = __builtin_fma(double(x[q][e]), double(x[q][e]), s[e]);
     }
-    const double mine = block_sum((s[0] + s[1]) + (s[2] + s[3]), slot);
+    const double mine = block_sum<kNormWaves>((s[0] + s[1]) + (s[2] + s[3]), slot);
     if (threadIdx.x == 0) {
         __hip_atomic_store(&ws->partial[blockIdx.x], mine, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
@@ -778,7 +734,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(
     double sum = 0.0;
     for (unsigned k = threadIdx.x; k < gridDim.x; k += kNormThreads)
         sum += __hip_atomic_load(&ws->partial[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sum = block_sum(sum, slot);
+    sum = block_sum<kNormWaves>(sum, slot);
     if (threadIdx.x == 0) {
         *sumsq = sum;
         write_clip(sum, max_norm, norm_coef);

@@ -23,6 +23,15 @@ inline int64_t norm_grid(int64_t n_chunks) {
     return b < 1 ? 1 : (b < kNormGrid ? b : kNormGrid);
 }
 
+// The reduce with its result's norm: workgroups of 8 wavefronts, one wavefront per group of
+// `tiles` 512-element tiles (not aligned: one lane per element), at most one workgroup for
+// each partial sum of the workspace.
+inline int64_t reduce_norm_grid(int64_t S, int tiles, bool aligned) {
+    const int64_t per = aligned ? int64_t(8) * tiles * 512 : 512;
+    const int64_t b = S / per + (S % per != 0);
+    return b < 1 ? 1 : (b < kNormGrid ? b : kNormGrid);
+}
+
 // 4-bit quantisation of values of es bytes: one workgroup per tile of kMx4Groups 16-byte
 // groups of values a lane.
 constexpr int kMx4Groups = 2;

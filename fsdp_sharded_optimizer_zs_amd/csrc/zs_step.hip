@@ -32,7 +32,7 @@
 
 #include <hip/hip_ext.h>
 
-#include "zs_internal.h"
+#include "zs_norm.h"
 
 #pragma clang fp contract(off)
 
@@ -291,6 +291,25 @@ struct HybridSum {
     }
 };
 
+// A reduce whose result is multiplied by a factor on the device (a clip factor, the
+// inverse of a loss scale): one more product, rounded on its own. The factor is one
+// scalar load per tile group, from the cache after the first.
+template <class Sum>
+struct Clipped {
+    Sum sum;
+    const float* factor;
+    __device__ __forceinline__ void vec(const PtrPack& c, int64_t tile, int lane,
+                                        float (&g)[kVec]) const {
+        sum.vec(c, tile, lane, g);
+        const float f = *factor;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) g[e] = g[e] * f;
+    }
+    __device__ __forceinline__ float one(const PtrPack& c, int64_t i) const {
+        return sum.one(c, i) * *factor;
+    }
+};
+
 // One AdamW element, in the fixed order, every operation rounded on its own.
 __device__ __forceinline__ void adamw1(float& p, float& m, float& v, float g,
                                        const AdamConsts& k) {
@@ -466,12 +485,12 @@ __global__ __launch_bounds__(kThreads) void adamw_scalar_kernel(
     }
 }
 
-// The reduced gradient of TP adjacent tiles from tile0, stored in the split map.
+// The reduced gradient of TP adjacent tiles from tile0, stored in the split map and left
+// in g.
 template <int DT, int TP, class Sum>
 __device__ __forceinline__ void reduce_tiles(f32x4* __restrict__ o4, const PtrPack& c,
                                              const Sum& sum, int64_t tile0, int lane,
-                                             f32x4* slot) {
-    float g[TP][kVec];
+                                             f32x4* slot, float (&g)[TP][kVec]) {
 #pragma unroll
     for (int u = 0; u < TP; ++u) sum.vec(c, tile0 + u, lane, g[u]);
     if constexpr (DT == ZS_BF16) {
@@ -497,8 +516,10 @@ __global__ __launch_bounds__(kThreads) ZS_WAVES void reduce_vec_kernel(float* __
     const int64_t stride = int64_t(gridDim.x) * kWaves;
     f32x4* o4 = reinterpret_cast<f32x4*>(out);
     const int64_t ngroups = S / (TP * kTile);
-    for (int64_t q = int64_t(blockIdx.x) * kWaves + wave; q < ngroups; q += stride)
-        reduce_tiles<DT, TP>(o4, c, sum, q * TP, lane, xpose[wave]);
+    for (int64_t q = int64_t(blockIdx.x) * kWaves + wave; q < ngroups; q += stride) {
+        float g[TP][kVec];
+        reduce_tiles<DT, TP>(o4, c, sum, q * TP, lane, xpose[wave], g);
+    }
     if (blockIdx.x == gridDim.x - 1) {
         for (int64_t t = ngroups * TP * kTile + threadIdx.x; t < S; t += kThreads)
             out[t] = sum.one(c, t);
@@ -513,10 +534,71 @@ __global__ __launch_bounds__(kThreads) void reduce_scalar_kernel(float* __restri
         out[t] = sum.one(c, t);
 }
 
+// The reduce with the sum of the squares of what it writes, in fp64 (exact products): the
+// square costs no read of its own, where a norm over the written gradient would read it
+// again (4 bytes an element beside D * 2 + 4). Workgroups of 8 wavefronts, at most one
+// for each partial sum of the workspace, which is also what fills the chip at 2 wavefronts
+// a SIMD; their sums are joined as the norm over many tensors joins its own. Elements past
+// the last whole tile group go to the last workgroup; with buffers that are not 16-byte
+// aligned (TP = 0) every workgroup takes elements, one a lane.
+constexpr int kJoinThreads = 512;
+template <int DT, class Sum, int TP>
+__global__ __launch_bounds__(kJoinThreads) ZS_WAVES void reduce_norm_kernel(
+    float* __restrict__ out, int64_t S, PtrPack c, Sum sum, double max_norm, int accumulate,
+    NormWorkspace* ws, double* sumsq, float* norm_coef) {
+    constexpr int W = kJoinThreads / kWave, kTP = TP > 0 ? TP : 1;
+    __shared__ f32x4 xpose[W][kTile / 4];
+    __shared__ double slot[W];
+    __shared__ bool last;
+    const int lane = int(threadIdx.x) % kWave;
+    const int wave = int(threadIdx.x) / kWave;
+    double s[2] = {0.0, 0.0};
+    int64_t first = int64_t(blockIdx.x) * kJoinThreads;
+    int64_t step = int64_t(gridDim.x) * kJoinThreads;
+    if constexpr (TP > 0) {
+        f32x4* o4 = reinterpret_cast<f32x4*>(out);
+        const int64_t ngroups = S / (TP * kTile);
+        for (int64_t q = int64_t(blockIdx.x) * W + wave; q < ngroups; q += int64_t(gridDim.x) * W) {
+            float g[kTP][kVec];
+            reduce_tiles<DT, kTP>(o4, c, sum, q * TP, lane, xpose[wave], g);
+#pragma unroll
+            for (int u = 0; u < kTP; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    s[e & 1] = __builtin_fma(double(g[u][e]), double(g[u][e]), s[e & 1]);
+        }
+        first = blockIdx.x == gridDim.x - 1 ? ngroups * TP * kTile : S;
+        step = kJoinThreads;
+    }
+    for (int64_t t = first + threadIdx.x; t < S; t += step) {
+        const float g = sum.one(c, t);
+        out[t] = g;
+        s[0] = __builtin_fma(double(g), double(g), s[0]);
+    }
+    const double mine = block_sum<W>(s[0] + s[1], slot);
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(&ws->partial[blockIdx.x], mine, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        last = arrive(ws);
+    }
+    __syncthreads();
+    if (!last) return;
+    double total = 0.0;
+    for (unsigned k = threadIdx.x; k < gridDim.x; k += kJoinThreads)
+        total += __hip_atomic_load(&ws->partial[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    total = block_sum<W>(total, slot);
+    if (threadIdx.x == 0) {
+        if (accumulate) total = *sumsq + total;
+        *sumsq = total;
+        if (norm_coef != nullptr) write_clip(total, max_norm, norm_coef);
+    }
+}
+
 // ---------------------------------------------------------------- dispatch
 
-// What one launch computes: the AdamW step (out == nullptr) or the reduce
-// alone into out.
+// What one launch computes: the reduce with its norm (norm != nullptr), else the AdamW
+// step (out == nullptr) or the reduce alone into out.
 struct Job {
     float* p;
     float* m;
@@ -528,6 +610,7 @@ struct Job {
     bool aligned;
     hipEvent_t ev_start;  // with ev_stop: recorded at the step kernel's own start and end
     hipEvent_t ev_stop;
+    const NormJob* norm;  // with out: also the sum of squares
 };
 
 template <int DT, class Sum>
@@ -536,7 +619,18 @@ hipError_t launch_job(const Job& j, const PtrPack& c, const Sum& sum, hipStream_
     static_assert(kThreads == kBlockThreads, "grid arithmetic assumes 256-thread workgroups");
     const unsigned tiled = unsigned(step_tiled_grid(j.S, TP));
     const unsigned scalar = unsigned(step_scalar_grid(j.S));
-    if (j.out == nullptr && j.ev_start != nullptr) {
+    if (j.norm != nullptr) {
+        const NormJob& n = *j.norm;
+        const unsigned grid = unsigned(reduce_norm_grid(j.S, TP, j.aligned));
+        if (j.aligned)
+            hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, TP>), dim3(grid), dim3(kJoinThreads),
+                               0, stream, j.out, j.S, c, sum, n.max_norm, n.accumulate, n.ws,
+                               n.sumsq, n.norm_coef);
+        else
+            hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, 0>), dim3(grid), dim3(kJoinThreads),
+                               0, stream, j.out, j.S, c, sum, n.max_norm, n.accumulate, n.ws,
+                               n.sumsq, n.norm_coef);
+    } else if (j.out == nullptr && j.ev_start != nullptr) {
         // timed: the runtime ties the two events to this dispatch's start and
         // end timestamps, with no marker packets around it
         if (j.aligned)
@@ -593,22 +687,43 @@ hipError_t dispatch(const Job& j, const PtrPack& c, int nd, int R, bool rnd, hip
         stream);
 }
 
+// The step with a factor on the device: the fold of one contribution (a gradient that was
+// reduced before, for its norm), and run-time folds, which batch their loads alike.
+template <int DT>
+hipError_t dispatch_clip(const Job& j, const PtrPack& c, int nd, int R, bool rnd,
+                         const float* factor, hipStream_t stream) {
+    const float inv_n = j.k.inv_n;
+    if (R == 1 && !rnd) {
+        if (nd == 1 && j.aligned)
+            return launch_job<DT>(j, c, Clipped<FlatSum<DT, 1>>{{nd, inv_n}, factor}, stream);
+        return launch_job<DT>(j, c, Clipped<FlatSum<DT, 0>>{{nd, inv_n}, factor}, stream);
+    }
+    return launch_job<DT>(j, c, Clipped<HybridSum<DT, 0>>{{nd, R, rnd ? 1 : 0, inv_n}, factor},
+                          stream);
+}
+
 }  // namespace
 
 hipError_t launch_adamw(float* p, float* m, float* v, uint16_t* w, int64_t S,
                         const PtrPack& contribs, int nd, int R, bool rnd, int dtype,
                         const AdamConsts& k, bool aligned, hipStream_t stream,
-                        hipEvent_t ev_start, hipEvent_t ev_stop) {
-    const Job j{p, m, v, w, nullptr, S, k, aligned, ev_start, ev_stop};
+                        hipEvent_t ev_start, hipEvent_t ev_stop, const float* grad_scale) {
+    const Job j{p, m, v, w, nullptr, S, k, aligned, ev_start, ev_stop, nullptr};
+    if (grad_scale != nullptr) {
+        if (dtype == ZS_BF16)
+            return dispatch_clip<ZS_BF16>(j, contribs, nd, R, rnd, grad_scale, stream);
+        return dispatch_clip<ZS_F32>(j, contribs, nd, R, rnd, grad_scale, stream);
+    }
     if (dtype == ZS_BF16) return dispatch<ZS_BF16>(j, contribs, nd, R, rnd, stream);
     return dispatch<ZS_F32>(j, contribs, nd, R, rnd, stream);
 }
 
 hipError_t launch_reduce(const PtrPack& contribs, int nd, int R, bool rnd, int dtype, int64_t S,
-                         float inv_n, float* out, bool aligned, hipStream_t stream) {
+                         float inv_n, float* out, bool aligned, hipStream_t stream,
+                         const NormJob* norm) {
     AdamConsts k{};
     k.inv_n = inv_n;
-    const Job j{nullptr, nullptr, nullptr, nullptr, out, S, k, aligned, nullptr, nullptr};
+    const Job j{nullptr, nullptr, nullptr, nullptr, out, S, k, aligned, nullptr, nullptr, norm};
     if (dtype == ZS_BF16) return dispatch<ZS_BF16>(j, contribs, nd, R, rnd, stream);
     return dispatch<ZS_F32>(j, contribs, nd, R, rnd, stream);
 }

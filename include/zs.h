@@ -26,9 +26,19 @@
  *                    AdamW over many tensors in one launch, moments in 32 or
  *                    in 8 bits; zs_state8_layout, zs_state8_encode and
  *                    zs_state8_decode lay out and convert the 8-bit moments
+ *   zs_quantize_f8, zs_gather_matrix_f8, zs_dequantize_f8
+ *                    matrices in 8-bit floating point with a scale for each
+ *                    block of 128 elements, also straight from a unit's shards
+ *   zs_matmul_f8, zs_linear_f8, zs_linear_f8_backward
+ *                    their products, and a linear layer's forward and backward
+ *                    pass over a unit's 8-bit weights
  *   zs_grad_norm, zs_clip_coef
  *                    the L2 norm over many gradient tensors and the factor
  *                    that clips it, left on the device for zs_adamw_multi
+ *   zs_reduce_shard_norm, zs_adamw_step_clip
+ *                    the shard's reduce with the norm of its result, and the
+ *                    step with the gradient multiplied by a clip factor that
+ *                    is on the device
  *   zs_quantize_mx4, zs_gather_unit_mx4
  *                    a shard in microscaled 4-bit floating point, and the
  *                    all-gather's rebuild of a unit from such shards
@@ -835,6 +845,194 @@ zs_status zs_quantize_mx4(const void* src, int32_t dtype, int64_t S, uint8_t* co
  */
 zs_status zs_gather_unit_mx4(const uint8_t* const* codes, const uint8_t* const* scales, int32_t D,
                              int64_t S, int32_t dtype, void* flat_out, hipStream_t stream);
+
+/*
+ * zs_reduce_shard_norm -- zs_reduce_shard_ex that also takes the sum of the
+ * squares of what it writes, in the same pass: the clipped step of a rank whose
+ * gradient is spread over the buckets of several units. Each bucket is reduced
+ * when its contributions are there; after the last one norm_coef is that of the
+ * whole gradient (one rank holding all of it: the D simulated ranks' shards; where
+ * several ranks hold parts, zs_clip_coef joins their sums).
+ *
+ *   grad_out[i]  = the bits of zs_reduce_shard_ex
+ *   sumsq[0]     = (accumulate ? sumsq[0] : 0) + sum of grad_out[i]^2, in fp64
+ *                  (exact products; the order of the sum depends on S and on whether
+ *                  every buffer is 16-byte aligned, on nothing else)
+ *   norm_coef[0], norm_coef[1] = of sumsq[0], as zs_grad_norm
+ *
+ *   contribs, D, opts, dtype, S, grad_out  as zs_reduce_shard_ex
+ *   max_norm     > 0, or infinity
+ *   sumsq        device, one double;  norm_coef  device, two floats, or NULL
+ *   accumulate   0 or 1: calls on one stream in turn add up
+ *   workspace    device, ZS_NORM_WORKSPACE bytes, as zs_grad_norm (and shared with
+ *                it, by calls that do not run at the same time)
+ * With S == 0 and accumulate == 0 the sum is 0 and is written.
+ * Errors: as zs_reduce_shard_ex and zs_grad_norm; ZS_EINVAL also when accumulate is
+ * not 0 or 1.
+ */
+zs_status zs_reduce_shard_norm(const void* const* contribs, int32_t D, const zs_reduce_opts* opts,
+                               int32_t dtype, int64_t S, float* grad_out, double max_norm,
+                               double* sumsq, float* norm_coef, int32_t accumulate,
+                               void* workspace, hipStream_t stream);
+
+/*
+ * zs_adamw_step_clip -- zs_adamw_step_ex whose gradient, the grad_out value of
+ * zs_reduce_shard_ex, is multiplied by *grad_scale (one fp32 product, rounded) before
+ * the update: bit for bit what zs_adamw_multi gives for the gradient grad_out.
+ * With one fp32 contribution, zs_reduce_shard_norm's grad_out, and norm_coef + 1 this
+ * is the clipped shard step; with the D contributions and the inverse of a loss scale
+ * no reduced gradient is stored.
+ *
+ *   grad_scale  device, one float, read when the kernel runs
+ * Other arguments and errors as zs_adamw_step_ex; ZS_EINVAL also when grad_scale is
+ * NULL or misaligned, ZS_EALIAS when it lies in p, m, v or w_out.
+ */
+zs_status zs_adamw_step_clip(float* p, float* m, float* v, uint16_t* w_out, int64_t S,
+                             const void* const* contribs, int32_t D, const zs_reduce_opts* opts,
+                             int32_t dtype, const zs_adamw_hp* hp, const float* grad_scale,
+                             hipStream_t stream);
+
+/*
+ * Block-scaled 8-bit floating point, in which a unit's matrices are multiplied.
+ * A matrix's element is a code of 8 bits times 2^(s - 127) with one scale byte s for
+ * each block of block_rows x 128 elements: 1 x 128 for activations and gradients
+ * (128 elements of a row, along what a product sums over), 128 x 128 for weights, whose
+ * transpose then has the same codes. Codes are e4m3 (sign, 4 bits of exponent, bias 7,
+ * 3 of mantissa; largest 448, no infinity) or e5m2 (5 bits, bias 15, 2; largest finite
+ * 57344). s = 255 marks a block of NaN. With u the fp32 bits of a block's largest
+ * magnitude,
+ *   s = 255 and all codes 0 if u >= 0x7f800000, else
+ *       max(1, ((u + 0x1fffff) >> 23) - 8 (e5m2: 15)),
+ * the smallest power of two under which the largest code holds that magnitude, and a
+ * code is x * 2^(127 - s) rounded to nearest, ties to even (signs are kept, of zeros
+ * too). Scales are powers of two, so that nothing but that one rounding is lost and the
+ * matrix cores apply them.
+ *
+ * Layout: row r's codes are bytes [r * ld, r * ld + cols), ld = 128 * ceil(cols / 128),
+ * followed by codes 0; the scale byte of its block c / 128 is byte
+ * (r / block_rows) * lds + c / 128, lds = 4 * ceil(cols / 512), and what fills a row of
+ * scale bytes is 1. Products read whole blocks: codes written by others must have the
+ * zeros too.
+ */
+#define ZS_E4M3 3
+#define ZS_E5M2 4
+
+typedef struct {
+    uint8_t* codes;      /* device, rows * ld bytes, 16-byte aligned                */
+    uint8_t* scales;     /* device, ceil(rows / block_rows) * lds bytes, 4-byte aligned */
+    int64_t rows;        /* 0 .. 2^31 - 1                                           */
+    int64_t cols;        /* 0 .. 2^22                                               */
+    int32_t type;        /* ZS_E4M3 or ZS_E5M2                                      */
+    int32_t block_rows;  /* 1 or 128                                                */
+} zs_f8_matrix;
+
+/* zs_f8_layout -- bytes of codes and of scales of a rows x cols matrix (host only). */
+zs_status zs_f8_layout(int64_t rows, int64_t cols, int32_t block_rows, int64_t* code_bytes,
+                       int64_t* scale_bytes);
+
+/*
+ * zs_quantize_f8 -- a matrix to that form, as it is, transposed, or both from one read.
+ *
+ *   x      device, rows x cols elements of dtype (ZS_BF16 or ZS_F32), row r from element
+ *          r * ldx on; ldx >= cols
+ *   out    host pointer, rows x cols, or NULL
+ *   out_t  host pointer, cols x rows, or NULL: the transpose, whose blocks run along x's
+ *          columns. At least one of both; they share block_rows, not the type
+ * Errors: ZS_EINVAL, ZS_EALIAS (x and the outputs overlap), ZS_EUNSUPPORTED.
+ */
+zs_status zs_quantize_f8(const void* x, int32_t dtype, int64_t ldx, const zs_f8_matrix* out,
+                         const zs_f8_matrix* out_t, hipStream_t stream);
+
+/*
+ * zs_gather_matrix_f8 -- one matrix of a unit, from the unit's D shards straight to that
+ * form: zs_gather_unit's elements [offset, offset + rows * cols) as a rows x cols matrix,
+ * and zs_quantize_f8 of it, without the flat unit in between.
+ *
+ *   shards  host array of D device pointers, each to S elements of dtype
+ *   offset  the matrix's first element in the flat unit (zs_unit_layout); the matrix ends
+ *           within the D * S elements
+ *   out, out_t  as zs_quantize_f8
+ * Errors: ZS_EINVAL, ZS_EALIAS, ZS_EUNSUPPORTED.
+ */
+zs_status zs_gather_matrix_f8(const void* const* shards, int32_t D, int64_t S, int32_t dtype,
+                              int64_t offset, const zs_f8_matrix* out, const zs_f8_matrix* out_t,
+                              hipStream_t stream);
+
+/*
+ * zs_dequantize_f8 -- the values that a matrix in that form stands for, rounded to dtype
+ * (to nearest even; exact but below 2^-126 and beyond the type's range).
+ *   out  device, rows x cols elements of dtype, row r from element r * ldo on
+ * Errors: ZS_EINVAL, ZS_EALIAS, ZS_EUNSUPPORTED.
+ */
+zs_status zs_dequantize_f8(const zs_f8_matrix* x, int32_t dtype, void* out, int64_t ldo,
+                           hipStream_t stream);
+
+/*
+ * zs_matmul_f8 -- C = A B^T, or C += A B^T, over the values of two matrices in that form:
+ *   c[m, n] = sum over k of a[m, k] * b[n, k]   (+ c[m, n] with accumulate)
+ * for a of M x K, b of N x K. Blocks of NaN make every element that reads them NaN.
+ *
+ * The sum is rounded to C's type once (with accumulate after adding C's old value, in
+ * fp32). For C in fp32 it is held in fp32 throughout. For C in bf16 the 8-bit matrix
+ * instructions form it: of 8 neighbouring products along K they drop what is below 2^-13
+ * of the largest one's leading power of two, and hold the rest in fp32. It is then off by
+ * at most 7 * 2^-13 of the sum of these largest products' magnitudes (on normal data by
+ * about 2^-16 of the result) before the rounding to bf16. The order of the sum depends on
+ * M, N, K and the types alone.
+ *
+ *   c          device, M x N elements of dtype, row m from element m * ldc on; what lies
+ *              between the rows is not written
+ *   accumulate 0 or 1
+ *   workspace  device, 16-byte aligned, zs_matmul_f8_workspace(M, N, K) bytes (NULL where
+ *              that is 0), zeroed by the caller before its first use; each call leaves it
+ *              ready for the next one, of any size it is large enough for. Calls that may
+ *              run at the same time (other streams, graphs) need one each
+ * With K = 0 the sum is 0. Errors: ZS_EINVAL, ZS_EALIAS (C or the workspace overlap an
+ * operand or each other), ZS_EUNSUPPORTED.
+ */
+zs_status zs_matmul_f8(const zs_f8_matrix* a, const zs_f8_matrix* b, int32_t dtype, void* c,
+                       int64_t ldc, int32_t accumulate, void* workspace, hipStream_t stream);
+zs_status zs_matmul_f8_workspace(int64_t M, int64_t N, int64_t K, int64_t* bytes);
+
+/*
+ * zs_linear_f8 -- a linear layer over 8-bit weights: y = Q(x) w^T with Q the quantiser of
+ * zs_quantize_f8 with 1 x 128 blocks, then zs_matmul_f8. For few rows (serving: one new
+ * token) in one launch, with the same results.
+ *
+ *   x     device, M x K elements of dtype, row stride ldx;  type  of its codes
+ *   w     N x K, block_rows 1 or 128 (a gathered matrix)
+ *   y     device, M x N elements of y_dtype, row stride ldy
+ *   workspace  as zs_matmul_f8, of zs_linear_f8_workspace(M, N, K) bytes
+ * Errors: as zs_quantize_f8 and zs_matmul_f8.
+ */
+zs_status zs_linear_f8(const void* x, int32_t dtype, int64_t M, int64_t ldx, int32_t type,
+                       const zs_f8_matrix* w, int32_t y_dtype, void* y, int64_t ldy,
+                       void* workspace, hipStream_t stream);
+zs_status zs_linear_f8_workspace(int64_t M, int64_t N, int64_t K, int64_t* bytes);
+
+/*
+ * zs_linear_f8_backward -- that layer's gradients from the output's gradient dy (M x N):
+ *   dx = Q(dy) w             (M x K), w given transposed: w_t, K x N
+ *   dw = Q(dy^T) Q(x^T)^T    (N x K), with accumulate dw += that
+ * Q quantises along what each product sums over: dy by rows for dx, dy and x by columns
+ * for dw. dw is usually a view into the unit's flat gradient, a contribution of
+ * zs_reduce_shard.
+ *
+ *   dy, x      device, elements of dtype, row strides lddy, ldx
+ *   dy_type    ZS_E4M3 or ZS_E5M2: of dy's codes (x's are e4m3)
+ *   w_t        NULL when dx is NULL
+ *   dx         device, elements of dx_dtype, row stride lddx; NULL: not computed
+ *   dw         device, elements of dw_dtype, row stride lddw; NULL: not computed (x may
+ *              then be NULL)
+ *   workspace  as zs_matmul_f8, of zs_linear_f8_backward_workspace(M, N, K) bytes
+ * Errors: as zs_quantize_f8 and zs_matmul_f8; ZS_EINVAL also when dx and dw are both NULL.
+ */
+zs_status zs_linear_f8_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                int32_t dtype, int64_t M, int64_t N, int64_t K, int32_t dy_type,
+                                const zs_f8_matrix* w_t, int32_t dx_dtype, void* dx, int64_t lddx,
+                                int32_t dw_dtype, void* dw, int64_t lddw, int32_t accumulate,
+                                void* workspace, hipStream_t stream);
+zs_status zs_linear_f8_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t* bytes);
 
 /* Text of the calling thread's most recent failure ("" if none). The pointer
  * stays valid until the thread's next call into the library. */
