@@ -38,7 +38,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
 typedef ZS_GLOBAL f32x4_u g_f32x4;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef ZS_GLOBAL u32x2_u g_u32x2;
+typedef ZS_GLOBAL u32x4_u g_u32x4;
 typedef ZS_GLOBAL uint8_t g_u8;
 typedef ZS_GLOBAL uint16_t g_u16;
 typedef ZS_GLOBAL uint32_t g_u32;
@@ -281,6 +284,277 @@ __global__ __launch_bounds__(kThreads) void matmul_kernel(F8Product p) {
     }
 }
 
+// ------------------------------------------------------------ the large product
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// 16 bytes a lane from base + offset to LDS, lane l's at lds + 16 l. Written as assembly so
+// that the compiler's own LDS reads do not wait for it; `arrived` and a barrier do. (The
+// instruction takes the LDS address from m0, one wait state after it is written.)
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((ZS_LDS const void*)(p)));
+}
+
+template <int N>
+__device__ __forceinline__ void arrived_but() {  // all but the last N loads
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// 256 x 256 of C by 2 x WN wavefronts, 128 x 256 / WN each.
+template <int WN, int TA, int TB, int DT>
+__global__ __launch_bounds__(128 * WN, 1) void matmul256_kernel(F8Product p) {
+    constexpr bool EXACT = DT == ZS_F32;
+    constexpr int T = 256, W = 2 * WN, NI = T / WN / 32;
+    // LDS: a ring of 4 half steps (64 codes of each row of both operands), and twice the
+    // scale bytes of 4 steps
+    constexpr int kHalfRow = 64, kOperand = T * kHalfRow, kHalf = 2 * kOperand;
+    constexpr int kScales = 4 * kHalf, kScale = 2 * T * 4;
+    constexpr int kLoads = T * 2 / 16 / W;  // of a half step, a wavefront
+    __shared__ __attribute__((aligned(16))) uint8_t big[kScales + 2 * kScale];
+    const int lane = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    // each XCD takes a run of tiles, 8 rows of tiles deep
+    const unsigned total = unsigned(p.tiles_m) * unsigned(p.tiles_n);
+    const unsigned xcd = blockIdx.x & 7u, q = total >> 3, rest = total & 7u;
+    const unsigned t = xcd * q + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
+    const unsigned deep = 8, band = t / (deep * p.tiles_n);
+    const unsigned rows = min(deep, unsigned(p.tiles_m) - band * deep);
+    const unsigned in = t - band * deep * p.tiles_n;
+    const int64_t m0 = int64_t(band * deep + in % rows) * T, n0 = int64_t(in / rows) * T;
+    const int wm = (wave & 1) * 128, wn = (wave >> 1) * (T / WN);
+
+    // What this lane loads: of each half step 16 bytes of kLoads rows, 16 * W apart, the first
+    // half of them of a and the others of b; and the scale bytes of a row.
+    const int64_t last_a = p.a.rows - 1 - m0, last_b = p.b.rows - 1 - n0;
+    uint32_t off[kLoads];
+    const int piece = ((lane & 3) ^ ((lane >> 4) & 3)) * 16;
+#pragma unroll
+    for (int k = 0; k < kLoads / 2; ++k) {
+        const int64_t r = 16 * (k * W + wave) + (lane >> 2);
+        off[k] = uint32_t((r < last_a ? r : last_a) * p.a.ld) + piece;
+        off[k + kLoads / 2] = uint32_t((r < last_b ? r : last_b) * p.b.ld) + piece;
+    }
+    const uint8_t* const codes_a = p.a.codes + m0 * p.a.ld;
+    const uint8_t* const codes_b = p.b.codes + n0 * p.b.ld;
+    uint32_t off_s[8 / W];
+    const uint8_t* base_s[8 / W];
+#pragma unroll
+    for (int k = 0; k < 8 / W; ++k) {
+        const int part = wave * (8 / W) + k;  // of 64 rows; 4 of a, 4 of b
+        const F8Operand& x = part < 4 ? p.a : p.b;
+        const int64_t first = part < 4 ? m0 : n0, last = part < 4 ? last_a : last_b;
+        const int64_t r = 64 * (part & 3) + lane;
+        base_s[k] = x.scales + (first >> x.shift) * x.lds;
+        off_s[k] = uint32_t(((r < last ? r : last) >> x.shift) * x.lds);
+    }
+    const uint32_t lds0 = lds_address(big);
+    const auto fetch = [&](int block, int half, int slot, int k) {
+        const bool is_a = k < kLoads / 2;
+        load_to_lds((is_a ? codes_a : codes_b) + int64_t(block) * kB + half * kHalfRow, off[k],
+                    lds0 + slot * kHalf + (is_a ? 0 : kOperand) +
+                        ((is_a ? k : k - kLoads / 2) * W + wave) * 1024);
+    };
+    const auto fetch_scales = [&](int word) {
+#pragma unroll
+        for (int k = 0; k < 8 / W; ++k)
+            load4_to_lds(base_s[k] + int64_t(word) * 4, off_s[k],
+                         lds0 + kScales + (word & 1) * kScale + (wave * (8 / W) + k) * 256);
+    };
+    // a lane's 32 codes of a half step, of row `lane % 32` of a 32-row part
+    const int row = lane & 31, g = lane >> 5;
+    const uint8_t* const read_a = big + (wm + row) * kHalfRow;
+    const uint8_t* const read_b = big + kOperand + (wn + row) * kHalfRow;
+    const auto part = [&](const uint8_t* from, int slot, int i) {
+        const uint8_t* x = from + slot * kHalf + i * 32 * kHalfRow;
+        const int swap = (row >> 2) & 3;
+        const i32x4 lo = *reinterpret_cast<const i32x4*>(x + (((2 * g) ^ swap) * 16));
+        const i32x4 hi = *reinterpret_cast<const i32x4*>(x + (((2 * g + 1) ^ swap) * 16));
+        return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+    f32x16 acc[NI][4] = {};
+    uint32_t sa[4], sb[NI];
+    i32x8 a0[4], b0[NI], a1[4], b1[NI];
+    const auto read = [&](int slot, i32x8 (&a)[4], i32x8 (&b)[NI]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = part(read_a, slot, i);
+            if (i < NI) b[i] = part(read_b, slot, i);
+        }
+    };
+    const auto read_scales = [&](int k, uint32_t (&x)[4], uint32_t (&y)[NI]) {
+        const uint8_t* from = big + kScales + ((k >> 2) & 1) * kScale + row * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const uint32_t*>(from + (wm + 32 * i) * 4);
+            if (i < NI) y[i] = *reinterpret_cast<const uint32_t*>(from + (T + wn + 32 * i) * 4);
+        }
+    };
+    const auto multiply = [&](const i32x8 (&a)[4], const i32x8 (&b)[NI]) {
+        if constexpr (!EXACT) {
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        b[j], a[i], acc[j][i], kFormat<TB>, kFormat<TA>, 0, int(sb[j]), 0,
+                        int(sa[i]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                bf16x8 h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    h[i] = widen<TA>(a[i][2 * e], a[i][2 * e + 1], scale_value(sa[i]));
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+                    const bf16x8 y = widen<TB>(b[j][2 * e], b[j][2 * e + 1], scale_value(sb[j]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y, h[i], acc[j][i], 0, 0, 0);
+                }
+            }
+        }
+    };
+    const int blocks = p.blocks, last = blocks - 1;
+    if (blocks > 0) {
+        fetch_scales(0);
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) fetch(min(h >> 1, last), h & 1, h, k);
+        arrived_but<3 * kLoads>();
+        __builtin_amdgcn_s_barrier();
+        read(0, a0, b0);
+        read_scales(0, sa, sb);
+    }
+    // A half step multiplies what was read in the one before, reads the next one's codes and,
+    // into the slot read before, sends for those of four half steps on, so that a load has three
+    // half steps to arrive. Past the last step the last one is loaded and read again: the
+    // loop's body has no branches.
+#pragma unroll 1
+    for (int k = 0; k < blocks; ++k) {
+        if ((k & 3) == 0) fetch_scales(min((k >> 2) + 1, last >> 2));
+        const int two = 2 * (k & 1), then = min(k + 2, last);
+        arrived_but<2 * kLoads>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) fetch(then, 0, two, u);
+        read(two + 1, a1, b1);
+        multiply(a0, b0);
+        __builtin_amdgcn_sched_barrier(0);
+        arrived_but<2 * kLoads>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) fetch(then, 1, two + 1, u);
+        uint32_t ta[4], tb[NI];
+        read(two ^ 2, a0, b0);
+        read_scales(min(k + 1, last), ta, tb);
+        multiply(a1, b1);
+        const int byte = 8 * ((k + 1) & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sa[i] = ta[i] >> byte;
+            if (i < NI) sb[i] = tb[i] >> byte;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    arrived();
+    __builtin_amdgcn_s_barrier();
+    if (DT == ZS_BF16 && p.accumulate) {  // the old value is added before the one rounding
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + wm + 32 * i + row;
+            if (m >= p.a.rows) continue;
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t n = n0 + wn + 32 * j + 8 * e + 4 * g;
+                    if (n < p.b.rows)
+                        put4<DT>(p, m, n, p.b.rows,
+                                 f32x4{acc[j][i][4 * e], acc[j][i][4 * e + 1],
+                                       acc[j][i][4 * e + 2], acc[j][i][4 * e + 3]});
+                }
+        }
+        return;
+    }
+    // Through LDS, so that C is written in whole 128-byte lines: a wavefront's 128 rows of 128
+    // bytes (64 columns in bf16, 32 in fp32) at a time, 16-byte pieces permuted by the row
+    // against bank conflicts.
+    constexpr int kPerPiece = DT == ZS_BF16 ? 8 : 4, kCols = 8 * kPerPiece, kParts = kCols / 32;
+    static_assert(W * 128 * 128 <= sizeof(big) && NI % kParts == 0, "a wavefront's rows fit");
+    uint8_t* const slot = big + wave * 128 * 128;
+#pragma unroll
+    for (int j0 = 0; j0 < NI; j0 += kParts) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 32 * i + row;
+#pragma unroll
+            for (int j = j0; j < j0 + kParts; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v0 = acc[j][i][4 * e], v1 = acc[j][i][4 * e + 1];
+                    const float v2 = acc[j][i][4 * e + 2], v3 = acc[j][i][4 * e + 3];
+                    if constexpr (DT == ZS_BF16) {
+                        const int at = (4 * (j - j0) + e) ^ ((r >> 1) & 7);
+                        *reinterpret_cast<u32x2*>(slot + r * 128 + at * 16 + g * 8) =
+                            u32x2{pack_bf16(v0, v1), pack_bf16(v2, v3)};
+                    } else {
+                        const int at = (2 * e + g) ^ ((r >> 1) & 7);
+                        *reinterpret_cast<f32x4*>(slot + r * 128 + at * 16) = f32x4{v0, v1, v2, v3};
+                    }
+                }
+        }
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+            const int r = 8 * k + (lane >> 3), piece = lane & 7;
+            const int64_t m = m0 + wm + r, n = n0 + wn + 32 * j0 + kPerPiece * piece;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(slot + r * 128 +
+                                                            (piece ^ ((r >> 1) & 7)) * 16);
+            if (m >= p.a.rows || n >= p.b.rows) continue;
+            if constexpr (DT == ZS_BF16) {
+                g_u16* c = global<g_u16>(p.c) + m * p.ldc + n;
+                if (n + 8 <= p.b.rows) {
+                    *reinterpret_cast<g_u32x4*>(c) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (n + e < p.b.rows) c[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
+                }
+            } else {
+                put4<DT>(p, m, n, p.b.rows, __builtin_bit_cast(f32x4, v));
+            }
+        }
+    }
+}
+
+#ifndef ZS_WN
+#define ZS_WN 4
+#endif
+template <int TA, int TB>
+void launch_256(const F8Product& p, int dtype, hipStream_t stream) {
+    const dim3 grid(unsigned(int64_t(p.tiles_m) * p.tiles_n));
+    if (dtype == ZS_BF16)
+        hipLaunchKernelGGL((matmul256_kernel<ZS_WN, TA, TB, ZS_BF16>), grid, dim3(128 * ZS_WN), 0, stream, p);
+    else
+        hipLaunchKernelGGL((matmul256_kernel<ZS_WN, TA, TB, ZS_F32>), grid, dim3(128 * ZS_WN), 0, stream, p);
+}
+
 template <int TM, int TN, int TA, int TB>
 void launch_tile(const F8Product& p, int dtype, hipStream_t stream) {
     const dim3 grid(unsigned(int64_t(p.tiles_m) * p.tiles_n * p.splits));
@@ -292,7 +566,8 @@ void launch_tile(const F8Product& p, int dtype, hipStream_t stream) {
 
 template <int TA, int TB>
 void launch_types(const F8Product& p, const F8Plan& plan, int dtype, hipStream_t stream) {
-    if (plan.tm == 128) launch_tile<128, 128, TA, TB>(p, dtype, stream);
+    if (plan.tm == 256) launch_256<TA, TB>(p, dtype, stream);
+    else if (plan.tm == 128) launch_tile<128, 128, TA, TB>(p, dtype, stream);
     else launch_tile<64, 64, TA, TB>(p, dtype, stream);
 }
 

@@ -38,6 +38,8 @@ constexpr int64_t kF8CountBytes = 2 * kF8Counts * 4;
 
 inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K, bool exact) {
     (void)exact;
+    if (f8_ceil(M, 256) * f8_ceil(N, 256) >= 200)
+        return F8Plan{256, 256, 1, f8_ceil(M, 256), f8_ceil(N, 256)};
     F8Plan p{128, 128, 1, f8_ceil(M, 128), f8_ceil(N, 128)};
     const int64_t blocks = f8_ceil(K, kF8Block);
     if (p.tiles_m * p.tiles_n < 256) {

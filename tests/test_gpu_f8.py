@@ -240,6 +240,23 @@ def test_exact_products(M, N, K, dtype):
         check_beside(store, full, N, lead, f"{i} accumulated")
 
 
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("M,N,K", [(3333, 4200, 300), (3841, 3585, 1), (4096, 4096, 128), (5000, 2561, 1700),
+                                   (2600, 5003, 640), (1000, 13_000, 257)])
+def test_exact_large_products(M, N, K, dtype):
+    """Sizes that fill the chip with the largest tiles; the sum by torch in fp32, which holds
+    these whole numbers exactly."""
+    for i, (ka, kb, br_a, br_b, pad) in enumerate([(F.E4M3, F.E4M3, 1, 128, 0), (F.E5M2, F.E4M3, 1, 1, 5)]):
+        a, va = f8(whole(M, K, i), ka, br_a)
+        b, vb = f8(whole(N, K, 90 + i), kb, br_b)
+        va, vb = (torch.from_numpy(v.astype(np.float32)).to(device()) for v in (va, vb))
+        want = torch.mm(va, vb.t().contiguous()).to(DTYPES[dtype])
+        store, full, c = out_matrix(M, N, dtype, pad, 3 * (pad > 0))
+        zs.zs_matmul_f8(a, b, c, workspace=workspace(M, N, K))
+        assert torch.equal(c, want)
+        check_beside(store, full, N, 3 * (pad > 0), f"{i}")
+
+
 def tolerance(a, b, dtype):
     exact, mags, tops = F.product(a, b)
     n = F.ceil(a.shape[1], 32)
