@@ -146,7 +146,7 @@ F8Operand operand(const zs_f8_matrix& x) {
 // A checked product.
 hipError_t product(const zs_f8_matrix& a, const zs_f8_matrix& b, int dtype, void* c, int64_t ldc,
                    int accumulate, uint32_t* counts, void* partial, hipStream_t stream) {
-    const F8Plan plan = f8_plan(a.rows, b.rows, a.cols, dtype == ZS_F32);
+    const F8Plan plan = f8_plan(a.rows, b.rows, a.cols);
     F8Product p{};
     p.a = operand(a);
     p.b = operand(b);

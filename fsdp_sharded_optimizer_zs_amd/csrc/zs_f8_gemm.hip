@@ -24,7 +24,6 @@
 namespace zs {
 namespace {
 
-constexpr int kThreads = kBlockThreads;
 constexpr int kB = kF8Block;
 
 #define ZS_GLOBAL __attribute__((address_space(1)))
@@ -42,48 +41,12 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef ZS_GLOBAL u32x2_u g_u32x2;
 typedef ZS_GLOBAL u32x4_u g_u32x4;
-typedef ZS_GLOBAL uint8_t g_u8;
 typedef ZS_GLOBAL uint16_t g_u16;
-typedef ZS_GLOBAL uint32_t g_u32;
-typedef ZS_GLOBAL uint64_t g_u64;
 typedef ZS_GLOBAL float g_f32;
 
 template <typename G, typename P>
 __device__ __forceinline__ G* global(P* p) {
     return reinterpret_cast<G*>(reinterpret_cast<uintptr_t>(p));
-}
-
-// Codes of one step of ROWS rows from row `first` on, to LDS. Rows past the operand's last
-// are its last again: what they give is not stored.
-template <int ROWS>
-__device__ __forceinline__ void stage(const F8Operand& x, int64_t first, int block, uint8_t* lds) {
-    const int lane = int(threadIdx.x) & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    const int piece = (lane & 7) ^ (lane >> 3);
-#pragma unroll
-    for (int k = 0; k < ROWS / 32; ++k) {
-        const int part = k * 4 + wave;  // of 8 rows
-        int64_t r = first + part * 8 + (lane >> 3);
-        r = r < x.rows ? r : x.rows - 1;
-        const uint8_t* p = x.codes + r * x.ld + int64_t(block) * kB + piece * 16;
-        __builtin_amdgcn_global_load_lds(global<ZS_GLOBAL void>(const_cast<uint8_t*>(p)),
-                                         (ZS_LDS void*)(lds + part * 1024), 16, 0, 0);
-    }
-}
-
-// A lane's 32 codes of one row of a step.
-__device__ __forceinline__ i32x8 fragment(const uint8_t* lds, int row0) {
-    const int lane = int(threadIdx.x) & 63;
-    const int row = row0 + (lane & 15), g = lane >> 4;
-    const i32x4 a = *reinterpret_cast<const i32x4*>(lds + row * kB + (((2 * g) ^ (row & 7)) * 16));
-    const i32x4 b = *reinterpret_cast<const i32x4*>(lds + row * kB + (((2 * g + 1) ^ (row & 7)) * 16));
-    return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-}
-
-// The word with a lane's row's scale bytes of 4 steps.
-__device__ __forceinline__ uint32_t scale_word(const F8Operand& x, int64_t row, int block) {
-    row = row < x.rows ? row : x.rows - 1;
-    return *global<const g_u32>(x.scales + (row >> x.shift) * x.lds + (block & ~3));
 }
 
 __device__ __forceinline__ float scale_value(uint32_t s) {
@@ -149,143 +112,6 @@ __device__ __forceinline__ void put4(const F8Product& p, int64_t m, int64_t n, i
     }
 }
 
-// TM x TN of C by 4 wavefronts, 2 x 2.
-template <int TM, int TN, int TA, int TB, int DT>
-__global__ __launch_bounds__(kThreads) void matmul_kernel(F8Product p) {
-    constexpr bool EXACT = DT == ZS_F32;
-    constexpr int PM = TM / 2, PN = TN / 2, MI = PM / 16, NI = PN / 16;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][(TM + TN) * kB];
-    __shared__ bool last;
-    const int lane = int(threadIdx.x) & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    const int split = int(blockIdx.x % unsigned(p.splits));
-    const int tile = int(blockIdx.x / unsigned(p.splits));
-    const int64_t m0 = int64_t(tile / p.tiles_n) * TM, n0 = int64_t(tile % p.tiles_n) * TN;
-    const int wm = (wave & 1) * PM, wn = (wave >> 1) * PN;
-    const int k0 = int(int64_t(p.blocks) * split / p.splits);
-    const int k1 = int(int64_t(p.blocks) * (split + 1) / p.splits);
-
-    f32x4 acc[NI][MI] = {};
-    uint32_t sa[MI], sb[NI];
-    if (k0 < k1) {
-        stage<TM>(p.a, m0, k0, lds[0]);
-        stage<TN>(p.b, n0, k0, lds[0] + TM * kB);
-    }
-    for (int k = k0; k < k1; ++k) {
-        uint8_t* const now = lds[(k - k0) & 1];
-        uint8_t* const next = lds[(k - k0 + 1) & 1];
-        if (k == k0 || (k & 3) == 0) {
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-                sa[i] = scale_word(p.a, m0 + wm + 16 * i + (lane & 15), k) >> (8 * (k & 3));
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                sb[i] = scale_word(p.b, n0 + wn + 16 * i + (lane & 15), k) >> (8 * (k & 3));
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();  // this step's codes are there, and the other buffer is read out
-        if (k + 1 < k1) {
-            stage<TM>(p.a, m0, k + 1, next);
-            stage<TN>(p.b, n0, k + 1, next + TM * kB);
-        }
-        i32x8 a[MI];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) a[i] = fragment(now, wm + 16 * i);
-        if constexpr (!EXACT) {
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                const i32x8 b = fragment(now + TM * kB, wn + 16 * j);
-#pragma unroll
-                for (int i = 0; i < MI; ++i)
-                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        b, a[i], acc[j][i], kFormat<TB>, kFormat<TA>, 0, int(sb[j]), 0, int(sa[i]));
-            }
-        } else {
-            i32x8 b[NI];
-#pragma unroll
-            for (int j = 0; j < NI; ++j) b[j] = fragment(now + TM * kB, wn + 16 * j);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                bf16x8 h[MI];
-#pragma unroll
-                for (int i = 0; i < MI; ++i)
-                    h[i] = widen<TA>(a[i][2 * q], a[i][2 * q + 1], scale_value(sa[i]));
-#pragma unroll
-                for (int j = 0; j < NI; ++j) {
-                    const bf16x8 g = widen<TB>(b[j][2 * q], b[j][2 * q + 1], scale_value(sb[j]));
-#pragma unroll
-                    for (int i = 0; i < MI; ++i)
-                        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(g, h[i], acc[j][i], 0, 0, 0);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < MI; ++i) sa[i] >>= 8;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) sb[i] >>= 8;
-    }
-
-    if (p.splits > 1) {
-        // partial sums as the lanes hold them, written through to memory that all XCDs share;
-        // the workgroup that counts in last adds them in their order
-        typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
-        uint64_t* const mine = reinterpret_cast<uint64_t*>(p.partial) +
-                               (int64_t(tile) * p.splits + split) * (TM * TN / 2) +
-                               (wave * NI * MI * 64 + lane) * 2;
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                const u64x2 v = __builtin_bit_cast(u64x2, acc[j][i]);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    __hip_atomic_store(&mine[(j * MI + i) * 128 + e], v[e], __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-            }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            uint32_t* const n = p.counts + tile;
-            last = __hip_atomic_fetch_add(n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
-                   uint32_t(p.splits);
-            if (last) __hip_atomic_store(n, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        __syncthreads();
-        if (!last) return;
-        const uint64_t* from = reinterpret_cast<const uint64_t*>(p.partial) +
-                               int64_t(tile) * p.splits * (TM * TN / 2) +
-                               (wave * NI * MI * 64 + lane) * 2;
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-#pragma unroll
-            for (int i = 0; i < MI; ++i) acc[j][i] = f32x4{0, 0, 0, 0};
-        for (int s = 0; s < p.splits; ++s, from += TM * TN / 2) {
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-#pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    u64x2 v;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        v[e] = __hip_atomic_load(&from[(j * MI + i) * 128 + e], __ATOMIC_RELAXED,
-                                                 __HIP_MEMORY_SCOPE_AGENT);
-                    acc[j][i] += __builtin_bit_cast(f32x4, v);
-                }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int64_t m = m0 + wm + 16 * i + (lane & 15);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
-            if (m < p.a.rows && n < p.b.rows) put4<DT>(p, m, n, p.b.rows, acc[j][i]);
-        }
-    }
-}
-
-// ------------------------------------------------------------ the large product
-
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // 16 bytes a lane from base + offset to LDS, lane l's at lds + 16 l. Written as assembly so
@@ -313,65 +139,86 @@ __device__ __forceinline__ void arrived_but() {  // all but the last N loads
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-// 256 x 256 of C by 2 x WN wavefronts, 128 x 256 / WN each.
-template <int WN, int TA, int TB, int DT>
-__global__ __launch_bounds__(128 * WN, 1) void matmul256_kernel(F8Product p) {
-    constexpr bool EXACT = DT == ZS_F32;
-    constexpr int T = 256, W = 2 * WN, NI = T / WN / 32;
+// TM x TN of C by WM x WN wavefronts, in 32 x 32 parts.
+template <int TM_, int TN_, int WM_, int WN_>
+struct Shape {
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, W = WM * WN, kThreads = 64 * W;
+    static constexpr int PM = TM / WM, PN = TN / WN, MI = PM / 32, NI = PN / 32;
     // LDS: a ring of 4 half steps (64 codes of each row of both operands), and twice the
     // scale bytes of 4 steps
-    constexpr int kHalfRow = 64, kOperand = T * kHalfRow, kHalf = 2 * kOperand;
-    constexpr int kScales = 4 * kHalf, kScale = 2 * T * 4;
-    constexpr int kLoads = T * 2 / 16 / W;  // of a half step, a wavefront
-    __shared__ __attribute__((aligned(16))) uint8_t big[kScales + 2 * kScale];
+    static constexpr int kHalfRow = 64, kHalf = (TM + TN) * kHalfRow, kRing = 4 * kHalf;
+    static constexpr int kScale = (TM + TN) * 4, kLds = kRing + 2 * kScale;
+    // loads of a half step, a wavefront: of a, of b; and all wavefronts' loads of scales
+    static constexpr int kLoadsA = TM / 16 / W, kLoadsB = TN / 16 / W, kLoads = kLoadsA + kLoadsB;
+    static constexpr int kScaleLoads = (TM + TN) / 64;
+    static_assert(TM % (16 * W) == 0 && TN % (16 * W) == 0 && TM % 64 == 0 && TN % 64 == 0 &&
+                      PM % 32 == 0 && PN % 32 == 0,
+                  "whole loads and parts");
+};
+
+template <class S, int TA, int TB, int DT>
+__global__ __launch_bounds__(S::kThreads, 1) void matmul_kernel(F8Product p) {
+    constexpr bool EXACT = DT == ZS_F32;
+    constexpr int TM = S::TM, TN = S::TN, W = S::W, MI = S::MI, NI = S::NI;
+    constexpr int kHalfRow = S::kHalfRow, kHalf = S::kHalf, kOperand = TM * kHalfRow;
+    constexpr int kScales = S::kRing, kScale = S::kScale, kLoads = S::kLoads;
+    __shared__ __attribute__((aligned(16))) uint8_t big[S::kLds];
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    // each XCD takes a run of tiles, 8 rows of tiles deep
-    const unsigned total = unsigned(p.tiles_m) * unsigned(p.tiles_n);
+    // Each XCD takes a run of tiles, 8 rows of tiles deep; a tile's splits are neighbours.
+    const unsigned total = unsigned(p.tiles_m) * unsigned(p.tiles_n) * unsigned(p.splits);
     const unsigned xcd = blockIdx.x & 7u, q = total >> 3, rest = total & 7u;
-    const unsigned t = xcd * q + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
+    const unsigned w = xcd * q + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
+    const unsigned t = w / unsigned(p.splits), split = w - t * unsigned(p.splits);
     const unsigned deep = 8, band = t / (deep * p.tiles_n);
     const unsigned rows = min(deep, unsigned(p.tiles_m) - band * deep);
     const unsigned in = t - band * deep * p.tiles_n;
-    const int64_t m0 = int64_t(band * deep + in % rows) * T, n0 = int64_t(in / rows) * T;
-    const int wm = (wave & 1) * 128, wn = (wave >> 1) * (T / WN);
+    const int64_t m0 = int64_t(band * deep + in % rows) * TM, n0 = int64_t(in / rows) * TN;
+    const int wm = (wave % S::WM) * S::PM, wn = (wave / S::WM) * S::PN;
+    const int first = int(int64_t(p.blocks) * split / p.splits);
+    const int last = int(int64_t(p.blocks) * (split + 1) / p.splits) - 1;
 
-    // What this lane loads: of each half step 16 bytes of kLoads rows, 16 * W apart, the first
-    // half of them of a and the others of b; and the scale bytes of a row.
+    // What this lane loads: of each half step 16 bytes of kLoads rows, 16 * W apart, first of a,
+    // then of b; and the scale bytes of a row. Rows past an operand's last are its last again:
+    // what they give is not stored.
     const int64_t last_a = p.a.rows - 1 - m0, last_b = p.b.rows - 1 - n0;
     uint32_t off[kLoads];
     const int piece = ((lane & 3) ^ ((lane >> 4) & 3)) * 16;
 #pragma unroll
-    for (int k = 0; k < kLoads / 2; ++k) {
-        const int64_t r = 16 * (k * W + wave) + (lane >> 2);
-        off[k] = uint32_t((r < last_a ? r : last_a) * p.a.ld) + piece;
-        off[k + kLoads / 2] = uint32_t((r < last_b ? r : last_b) * p.b.ld) + piece;
+    for (int k = 0; k < kLoads; ++k) {
+        const bool is_a = k < S::kLoadsA;
+        const int64_t r = 16 * ((is_a ? k : k - S::kLoadsA) * W + wave) + (lane >> 2);
+        off[k] = is_a ? uint32_t((r < last_a ? r : last_a) * p.a.ld) + piece
+                      : uint32_t((r < last_b ? r : last_b) * p.b.ld) + piece;
     }
     const uint8_t* const codes_a = p.a.codes + m0 * p.a.ld;
     const uint8_t* const codes_b = p.b.codes + n0 * p.b.ld;
-    uint32_t off_s[8 / W];
-    const uint8_t* base_s[8 / W];
+    constexpr int kMine = (S::kScaleLoads + W - 1) / W;
+    uint32_t off_s[kMine];
+    const uint8_t* base_s[kMine];
 #pragma unroll
-    for (int k = 0; k < 8 / W; ++k) {
-        const int part = wave * (8 / W) + k;  // of 64 rows; 4 of a, 4 of b
-        const F8Operand& x = part < 4 ? p.a : p.b;
-        const int64_t first = part < 4 ? m0 : n0, last = part < 4 ? last_a : last_b;
-        const int64_t r = 64 * (part & 3) + lane;
-        base_s[k] = x.scales + (first >> x.shift) * x.lds;
-        off_s[k] = uint32_t(((r < last ? r : last) >> x.shift) * x.lds);
+    for (int k = 0; k < kMine; ++k) {
+        const int part = wave * kMine + k;  // of 64 rows: of a, then of b
+        const bool is_a = part < TM / 64;
+        const F8Operand& x = is_a ? p.a : p.b;
+        const int64_t from = is_a ? m0 : n0, end = is_a ? last_a : last_b;
+        const int64_t r = 64 * (is_a ? part : part - TM / 64) + lane;
+        base_s[k] = x.scales + (from >> x.shift) * x.lds;
+        off_s[k] = uint32_t((((r < end ? r : end) + (from & ((1 << x.shift) - 1))) >> x.shift) * x.lds);
     }
     const uint32_t lds0 = lds_address(big);
     const auto fetch = [&](int block, int half, int slot, int k) {
-        const bool is_a = k < kLoads / 2;
+        const bool is_a = k < S::kLoadsA;
         load_to_lds((is_a ? codes_a : codes_b) + int64_t(block) * kB + half * kHalfRow, off[k],
                     lds0 + slot * kHalf + (is_a ? 0 : kOperand) +
-                        ((is_a ? k : k - kLoads / 2) * W + wave) * 1024);
+                        ((is_a ? k : k - S::kLoadsA) * W + wave) * 1024);
     };
     const auto fetch_scales = [&](int word) {
 #pragma unroll
-        for (int k = 0; k < 8 / W; ++k)
-            load4_to_lds(base_s[k] + int64_t(word) * 4, off_s[k],
-                         lds0 + kScales + (word & 1) * kScale + (wave * (8 / W) + k) * 256);
+        for (int k = 0; k < kMine; ++k)
+            if (wave * kMine + k < S::kScaleLoads)
+                load4_to_lds(base_s[k] + int64_t(word) * 4, off_s[k],
+                             lds0 + kScales + (word & 1) * kScale + (wave * kMine + k) * 256);
     };
     // a lane's 32 codes of a half step, of row `lane % 32` of a 32-row part
     const int row = lane & 31, g = lane >> 5;
@@ -384,70 +231,72 @@ __global__ __launch_bounds__(128 * WN, 1) void matmul256_kernel(F8Product p) {
         const i32x4 hi = *reinterpret_cast<const i32x4*>(x + (((2 * g + 1) ^ swap) * 16));
         return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
-    f32x16 acc[NI][4] = {};
-    uint32_t sa[4], sb[NI];
-    i32x8 a0[4], b0[NI], a1[4], b1[NI];
-    const auto read = [&](int slot, i32x8 (&a)[4], i32x8 (&b)[NI]) {
+    f32x16 acc[NI][MI] = {};
+    uint32_t sa[MI], sb[NI];
+    i32x8 a0[MI], b0[NI], a1[MI], b1[NI];
+    const auto read = [&](int slot, i32x8 (&a)[MI], i32x8 (&b)[NI]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = part(read_a, slot, i);
+        for (int i = 0; i < (MI > NI ? MI : NI); ++i) {
+            if (i < MI) a[i] = part(read_a, slot, i);
             if (i < NI) b[i] = part(read_b, slot, i);
         }
     };
-    const auto read_scales = [&](int k, uint32_t (&x)[4], uint32_t (&y)[NI]) {
+    const auto read_scales = [&](int k, uint32_t (&x)[MI], uint32_t (&y)[NI]) {
         const uint8_t* from = big + kScales + ((k >> 2) & 1) * kScale + row * 4;
+        const int byte = 8 * (k & 3);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = *reinterpret_cast<const uint32_t*>(from + (wm + 32 * i) * 4);
-            if (i < NI) y[i] = *reinterpret_cast<const uint32_t*>(from + (T + wn + 32 * i) * 4);
-        }
+        for (int i = 0; i < MI; ++i)
+            x[i] = *reinterpret_cast<const uint32_t*>(from + (wm + 32 * i) * 4) >> byte;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            y[i] = *reinterpret_cast<const uint32_t*>(from + (TM + wn + 32 * i) * 4) >> byte;
     };
-    const auto multiply = [&](const i32x8 (&a)[4], const i32x8 (&b)[NI]) {
+    const auto multiply = [&](const i32x8 (&a)[MI], const i32x8 (&b)[NI]) {
         if constexpr (!EXACT) {
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < MI; ++i)
                     acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                         b[j], a[i], acc[j][i], kFormat<TB>, kFormat<TA>, 0, int(sb[j]), 0,
                         int(sa[i]));
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                bf16x8 h[4];
+                bf16x8 h[MI];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < MI; ++i)
                     h[i] = widen<TA>(a[i][2 * e], a[i][2 * e + 1], scale_value(sa[i]));
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {
                     const bf16x8 y = widen<TB>(b[j][2 * e], b[j][2 * e + 1], scale_value(sb[j]));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < MI; ++i)
                         acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y, h[i], acc[j][i], 0, 0, 0);
                 }
             }
         }
     };
-    const int blocks = p.blocks, last = blocks - 1;
-    if (blocks > 0) {
-        fetch_scales(0);
+    if (first <= last) {
+        fetch_scales(first >> 2);
+        fetch_scales(min((first >> 2) + 1, last >> 2));
 #pragma unroll
         for (int h = 0; h < 4; ++h)
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) fetch(min(h >> 1, last), h & 1, h, k);
+            for (int k = 0; k < kLoads; ++k) fetch(min(first + (h >> 1), last), h & 1, h, k);
         arrived_but<3 * kLoads>();
         __builtin_amdgcn_s_barrier();
         read(0, a0, b0);
-        read_scales(0, sa, sb);
+        read_scales(first, sa, sb);
     }
     // A half step multiplies what was read in the one before, reads the next one's codes and,
     // into the slot read before, sends for those of four half steps on, so that a load has three
     // half steps to arrive. Past the last step the last one is loaded and read again: the
     // loop's body has no branches.
 #pragma unroll 1
-    for (int k = 0; k < blocks; ++k) {
+    for (int k = first; k <= last; ++k) {
         if ((k & 3) == 0) fetch_scales(min((k >> 2) + 1, last >> 2));
-        const int two = 2 * (k & 1), then = min(k + 2, last);
+        const int two = 2 * ((k - first) & 1), then = min(k + 2, last);
         arrived_but<2 * kLoads>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -461,23 +310,73 @@ __global__ __launch_bounds__(128 * WN, 1) void matmul256_kernel(F8Product p) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) fetch(then, 1, two + 1, u);
-        uint32_t ta[4], tb[NI];
+        uint32_t ta[MI], tb[NI];
         read(two ^ 2, a0, b0);
         read_scales(min(k + 1, last), ta, tb);
         multiply(a1, b1);
-        const int byte = 8 * ((k + 1) & 3);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sa[i] = ta[i] >> byte;
-            if (i < NI) sb[i] = tb[i] >> byte;
-        }
+        for (int i = 0; i < MI; ++i) sa[i] = ta[i];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) sb[i] = tb[i];
         __builtin_amdgcn_sched_barrier(0);
     }
     arrived();
     __builtin_amdgcn_s_barrier();
+
+    if (p.splits > 1) {
+        // partial sums as the lanes hold them, written through to memory that all XCDs share;
+        // the workgroup that counts in last adds them in their order
+        typedef uint64_t u64x8 __attribute__((ext_vector_type(8)));
+        const int64_t size = TM * TN / 2;  // of a partial sum, in 8 bytes
+        uint64_t* const all = reinterpret_cast<uint64_t*>(p.partial) +
+                              int64_t(t) * p.splits * size + wave * (MI * NI * 512) + lane;
+        uint64_t* const mine = all + split * size;
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const u64x8 v = __builtin_bit_cast(u64x8, acc[j][i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    __hip_atomic_store(&mine[((j * MI + i) * 8 + e) * 64], v[e], __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+            }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        // LDS is free here: the loads of codes are over and read
+        volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(big);
+        if (threadIdx.x == 0) {
+            uint32_t* const n = p.counts + t;
+            const bool last_one = __hip_atomic_fetch_add(n, 1u, __ATOMIC_RELAXED,
+                                                         __HIP_MEMORY_SCOPE_AGENT) + 1 ==
+                                  uint32_t(p.splits);
+            if (last_one) __hip_atomic_store(n, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            *flag = last_one;
+        }
+        __syncthreads();
+        if (*flag == 0) return;
+        __syncthreads();  // the flag is read before its place is written again
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) acc[j][i] = f32x16{};
+        const uint64_t* from = all;
+        for (int s = 0; s < p.splits; ++s, from += size)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    u64x8 v;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = __hip_atomic_load(&from[((j * MI + i) * 8 + e) * 64],
+                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    acc[j][i] += __builtin_bit_cast(f32x16, v);
+                }
+    }
     if (DT == ZS_BF16 && p.accumulate) {  // the old value is added before the one rounding
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < MI; ++i) {
             const int64_t m = m0 + wm + 32 * i + row;
             if (m >= p.a.rows) continue;
 #pragma unroll
@@ -493,16 +392,21 @@ __global__ __launch_bounds__(128 * WN, 1) void matmul256_kernel(F8Product p) {
         }
         return;
     }
-    // Through LDS, so that C is written in whole 128-byte lines: a wavefront's 128 rows of 128
-    // bytes (64 columns in bf16, 32 in fp32) at a time, 16-byte pieces permuted by the row
-    // against bank conflicts.
-    constexpr int kPerPiece = DT == ZS_BF16 ? 8 : 4, kCols = 8 * kPerPiece, kParts = kCols / 32;
-    static_assert(W * 128 * 128 <= sizeof(big) && NI % kParts == 0, "a wavefront's rows fit");
-    uint8_t* const slot = big + wave * 128 * 128;
+    // Through LDS, so that C is written in whole lines: a wavefront's PM rows of up to 128 bytes
+    // (64 columns in bf16, 32 in fp32) at a time, 16-byte pieces permuted by the row against
+    // bank conflicts.
+    constexpr int kPerPiece = DT == ZS_BF16 ? 8 : 4;
+    constexpr int kCols = 8 * kPerPiece < S::PN ? 8 * kPerPiece : S::PN, kParts = kCols / 32;
+    constexpr int kPieces = kCols / kPerPiece, kRows = 64 / kPieces, kRowBytes = 16 * kPieces;
+    static_assert(W * S::PM * kRowBytes <= S::kLds && NI % kParts == 0, "a wavefront's rows fit");
+    uint8_t* const slot = big + wave * S::PM * kRowBytes;
+    const auto place = [&](int r, int at) {
+        return slot + r * kRowBytes + (at ^ ((r / (16 / kPieces)) & (kPieces - 1))) * 16;
+    };
 #pragma unroll
     for (int j0 = 0; j0 < NI; j0 += kParts) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < MI; ++i) {
             const int r = 32 * i + row;
 #pragma unroll
             for (int j = j0; j < j0 + kParts; ++j)
@@ -510,22 +414,18 @@ __global__ __launch_bounds__(128 * WN, 1) void matmul256_kernel(F8Product p) {
                 for (int e = 0; e < 4; ++e) {
                     const float v0 = acc[j][i][4 * e], v1 = acc[j][i][4 * e + 1];
                     const float v2 = acc[j][i][4 * e + 2], v3 = acc[j][i][4 * e + 3];
-                    if constexpr (DT == ZS_BF16) {
-                        const int at = (4 * (j - j0) + e) ^ ((r >> 1) & 7);
-                        *reinterpret_cast<u32x2*>(slot + r * 128 + at * 16 + g * 8) =
+                    if constexpr (DT == ZS_BF16)
+                        *reinterpret_cast<u32x2*>(place(r, 4 * (j - j0) + e) + g * 8) =
                             u32x2{pack_bf16(v0, v1), pack_bf16(v2, v3)};
-                    } else {
-                        const int at = (2 * e + g) ^ ((r >> 1) & 7);
-                        *reinterpret_cast<f32x4*>(slot + r * 128 + at * 16) = f32x4{v0, v1, v2, v3};
-                    }
+                    else
+                        *reinterpret_cast<f32x4*>(place(r, 2 * e + g)) = f32x4{v0, v1, v2, v3};
                 }
         }
 #pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-            const int r = 8 * k + (lane >> 3), piece = lane & 7;
+        for (int k = 0; k < S::PM / kRows; ++k) {
+            const int r = kRows * k + lane / kPieces, piece = lane % kPieces;
             const int64_t m = m0 + wm + r, n = n0 + wn + 32 * j0 + kPerPiece * piece;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(slot + r * 128 +
-                                                            (piece ^ ((r >> 1) & 7)) * 16);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(place(r, piece));
             if (m >= p.a.rows || n >= p.b.rows) continue;
             if constexpr (DT == ZS_BF16) {
                 g_u16* c = global<g_u16>(p.c) + m * p.ldc + n;
@@ -543,32 +443,20 @@ __global__ __launch_bounds__(128 * WN, 1) void matmul256_kernel(F8Product p) {
     }
 }
 
-#ifndef ZS_WN
-#define ZS_WN 4
-#endif
-template <int TA, int TB>
-void launch_256(const F8Product& p, int dtype, hipStream_t stream) {
-    const dim3 grid(unsigned(int64_t(p.tiles_m) * p.tiles_n));
+template <class S, int TA, int TB>
+void launch_shape(const F8Product& p, int dtype, hipStream_t stream) {
+    const dim3 grid(unsigned(int64_t(p.tiles_m) * p.tiles_n * p.splits)), block(S::kThreads);
     if (dtype == ZS_BF16)
-        hipLaunchKernelGGL((matmul256_kernel<ZS_WN, TA, TB, ZS_BF16>), grid, dim3(128 * ZS_WN), 0, stream, p);
+        hipLaunchKernelGGL((matmul_kernel<S, TA, TB, ZS_BF16>), grid, block, 0, stream, p);
     else
-        hipLaunchKernelGGL((matmul256_kernel<ZS_WN, TA, TB, ZS_F32>), grid, dim3(128 * ZS_WN), 0, stream, p);
-}
-
-template <int TM, int TN, int TA, int TB>
-void launch_tile(const F8Product& p, int dtype, hipStream_t stream) {
-    const dim3 grid(unsigned(int64_t(p.tiles_m) * p.tiles_n * p.splits));
-    if (dtype == ZS_BF16)
-        hipLaunchKernelGGL((matmul_kernel<TM, TN, TA, TB, ZS_BF16>), grid, dim3(kThreads), 0, stream, p);
-    else
-        hipLaunchKernelGGL((matmul_kernel<TM, TN, TA, TB, ZS_F32>), grid, dim3(kThreads), 0, stream, p);
+        hipLaunchKernelGGL((matmul_kernel<S, TA, TB, ZS_F32>), grid, block, 0, stream, p);
 }
 
 template <int TA, int TB>
 void launch_types(const F8Product& p, const F8Plan& plan, int dtype, hipStream_t stream) {
-    if (plan.tm == 256) launch_256<TA, TB>(p, dtype, stream);
-    else if (plan.tm == 128) launch_tile<128, 128, TA, TB>(p, dtype, stream);
-    else launch_tile<64, 64, TA, TB>(p, dtype, stream);
+    if (plan.tm == 256) launch_shape<Shape<256, 256, 2, 4>, TA, TB>(p, dtype, stream);
+    else if (plan.tm == 128) launch_shape<Shape<128, 128, 2, 2>, TA, TB>(p, dtype, stream);
+    else launch_shape<Shape<64, 64, 2, 2>, TA, TB>(p, dtype, stream);
 }
 
 }  // namespace

@@ -36,31 +36,39 @@ struct F8Plan {
 constexpr int64_t kF8Counts = 1024;
 constexpr int64_t kF8CountBytes = 2 * kF8Counts * 4;
 
-inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K, bool exact) {
-    (void)exact;
-    if (f8_ceil(M, 256) * f8_ceil(N, 256) >= 200)
-        return F8Plan{256, 256, 1, f8_ceil(M, 256), f8_ceil(N, 256)};
-    F8Plan p{128, 128, 1, f8_ceil(M, 128), f8_ceil(N, 128)};
-    const int64_t blocks = f8_ceil(K, kF8Block);
-    if (p.tiles_m * p.tiles_n < 256) {
-        p = F8Plan{64, 64, 1, f8_ceil(M, 64), f8_ceil(N, 64)};
-        const int64_t t = p.tiles_m * p.tiles_n;
-        if (t > 0 && t < 256) {
-            int64_t s = 512 / t;
-            if (s > blocks / 4) s = blocks / 4;
-            p.splits = int(s < 1 ? 1 : (s > 16 ? 16 : s));
-        }
+// Tiles of 256, 128 or 64 squared: the larger one moves less through LDS for each product,
+// the smaller ones fill 256 CUs with less. The costs of a step of 128 along K for each tile
+// that a CU takes are measured, in hundredths of a microsecond (C in fp32: 290, 93 and 33, in
+// much the same ratios). With them, in us, M x N x K and C in bf16: 3000 x 3000 x 3000
+// 256: 39, 128: 46, 64: 58; 2048 x 4096 x 4096 47, 42, 66; 512 x 4096 x 4096 46, 19, 17.
+// What is left idle by tiles of 64 is filled by splitting K, into parts of 16 steps at
+// least, below which joining them costs more than it gains (128 x 4096 x 4096 in 1, 2, 4 parts
+// 11.0, 10.0, 10.8; 1024 x 256 x 2048 8.1, 8.4, 8.5; 256 x 256 x 8192 19.0, 13.5, 10.6).
+inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
+    constexpr int kCus = 256;
+    const int side[3] = {256, 128, 64}, cost[3] = {150, 55, 22};
+    F8Plan best{};
+    int64_t least = -1;
+    for (int i = 0; i < 3; ++i) {
+        const F8Plan p{side[i], side[i], 1, f8_ceil(M, side[i]), f8_ceil(N, side[i])};
+        const int64_t c = f8_ceil(p.tiles_m * p.tiles_n, kCus) * cost[i];
+        if (least < 0 || c < least) best = p, least = c;
     }
-    return p;
+    const int64_t tiles = best.tiles_m * best.tiles_n;
+    if (best.tm == 64 && tiles > 0) {
+        int64_t s = kCus / tiles;
+        const int64_t parts = f8_ceil(K, kF8Block) / 16;
+        s = s < parts ? s : parts;
+        best.splits = int(s < 1 ? 1 : (s < 32 ? s : 32));
+    }
+    return best;
 }
 inline int64_t f8_partial_bytes(const F8Plan& p) {
     return p.splits > 1 ? p.tiles_m * p.tiles_n * p.splits * p.tm * p.tn * 4 : 0;
 }
 inline int64_t f8_matmul_workspace(int64_t M, int64_t N, int64_t K) {
-    const int64_t a = f8_partial_bytes(f8_plan(M, N, K, false)),
-                  b = f8_partial_bytes(f8_plan(M, N, K, true));
-    const int64_t most = a > b ? a : b;
-    return most > 0 ? kF8CountBytes + most : 0;
+    const int64_t n = f8_partial_bytes(f8_plan(M, N, K));
+    return n > 0 ? kF8CountBytes + n : 0;
 }
 
 }  // namespace zs

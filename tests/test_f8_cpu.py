@@ -286,11 +286,9 @@ using namespace zs;
 int main() {
     long long M, N, K;
     while (std::scanf("%lld %lld %lld", &M, &N, &K) == 3) {
-        for (int exact = 0; exact < 2; ++exact) {
-            const F8Plan p = f8_plan(M, N, K, exact);
-            std::printf("%d %d %d %lld %lld %lld ", p.tm, p.tn, p.splits, (long long)p.tiles_m,
-                        (long long)p.tiles_n, (long long)f8_partial_bytes(p));
-        }
+        const F8Plan p = f8_plan(M, N, K);
+        std::printf("%d %d %d %lld %lld %lld ", p.tm, p.tn, p.splits, (long long)p.tiles_m,
+                    (long long)p.tiles_n, (long long)f8_partial_bytes(p));
         std::printf("%lld %lld %lld %lld %lld\n", (long long)f8_matmul_workspace(M, N, K), (long long)kF8Counts,
                     (long long)kF8CountBytes, (long long)reduce_norm_grid(M * K, 2, true),
                     (long long)reduce_norm_grid(M * K, 2, false));
@@ -314,12 +312,11 @@ def test_plans_cover_the_work_and_fit_the_workspace(tmp_path):
                          capture_output=True, text=True, check=True).stdout.split("\n")
     for (M, N, K), line in zip(cases, out):
         v = [int(x) for x in line.split()]
-        need, counts, count_bytes, aligned, scalar = v[12:]
-        for tm, tn, splits, tiles_m, tiles_n, partial in (v[:6], v[6:12]):
-            assert tiles_m * tm >= M and tiles_n * tn >= N and (tiles_m - 1) * tm < max(M, 1)
-            assert 1 <= splits <= max(1, -(-K // 128))
-            if splits > 1:
-                assert tiles_m * tiles_n <= counts
-                assert partial == tiles_m * tiles_n * splits * tm * tn * 4 and need >= count_bytes + partial
+        tm, tn, splits, tiles_m, tiles_n, partial, need, counts, count_bytes, aligned, scalar = v
+        assert tiles_m * tm >= M and tiles_n * tn >= N and (tiles_m - 1) * tm < max(M, 1)
+        assert 1 <= splits <= max(1, -(-K // 128))
+        if splits > 1:
+            assert tiles_m * tiles_n <= counts
+            assert partial == tiles_m * tiles_n * splits * tm * tn * 4 and need >= count_bytes + partial
         assert count_bytes >= 2 * counts * 4 and need < 2**31
         assert 1 <= aligned <= 512 and 1 <= scalar <= 512
