@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 from typing import List, Sequence, Tuple
@@ -237,7 +238,13 @@ def _ptr_array(ts: Sequence) -> ctypes.Array:
 
 def _hp(hp) -> zs_adamw_hp:
     if isinstance(hp, dict):
-        hp = AdamWHP(**hp)
+        try:
+            if len(hp) == 6:  # straight to the structure: a dataclass in between takes 2 us
+                return zs_adamw_hp(float(hp["lr"]), float(hp["beta1"]), float(hp["beta2"]),
+                                   float(hp["eps"]), float(hp["weight_decay"]), int(hp["step"]))
+        except KeyError:
+            pass
+        hp = AdamWHP(**hp)  # says which name is missing or unknown
     return zs_adamw_hp(float(hp.lr), float(hp.beta1), float(hp.beta2), float(hp.eps),
                        float(hp.weight_decay), int(hp.step))
 
@@ -993,10 +1000,10 @@ def zs_reduce_shard_norm(contribs: Sequence, grad_out, max_norm: float, sumsq, n
     if norm_coef is not None:
         _typed(norm_coef, "norm_coef", torch.float32, 2)
         side.append(norm_coef)
-    _same_device(contribs + side, "zs_reduce_shard_norm")
-    opts = zs_reduce_opts(int(replicas), 1 if round_to_reduce_dtype else 0, float(scale))
-    _enqueue(load().zs_reduce_shard_norm, grad_out, stream, _ptr_array(contribs),
-             _groups(contribs, replicas), ctypes.byref(opts), code, S, grad_out.data_ptr(),
+    _one_device(contribs + side, "zs_reduce_shard_norm")
+    _enqueue(load().zs_reduce_shard_norm, grad_out, stream, _addresses(contribs),
+             _groups(contribs, replicas), _opts(replicas, round_to_reduce_dtype, scale), code, S,
+             grad_out.data_ptr(),
              float(max_norm), sumsq.data_ptr(),
              None if norm_coef is None else norm_coef.data_ptr(), 1 if accumulate else 0,
              workspace.data_ptr())
@@ -1018,24 +1025,44 @@ def zs_adamw_step_clip(p, m, v, w_out, contribs: Sequence, hp, grad_scale, repli
         raise ValueError("w_out must be bf16 bits with S elements")
     code = _contributions(contribs, S)
     _typed(grad_scale, "grad_scale", torch.float32, 1)
-    _same_device([p, m, v, w_out, grad_scale] + contribs, "zs_adamw_step_clip")
-    opts = zs_reduce_opts(int(replicas), 1 if round_to_reduce_dtype else 0, float(scale),
-                          ZS_W_KEEP if keep_working_shard else ZS_W_STREAM, 0)
+    _one_device([p, m, v, w_out, grad_scale] + contribs, "zs_adamw_step_clip")
     _enqueue(load().zs_adamw_step_clip, p, stream, p.data_ptr(), m.data_ptr(), v.data_ptr(),
-             w_out.data_ptr(), S, _ptr_array(contribs), _groups(contribs, replicas),
-             ctypes.byref(opts), code, ctypes.byref(_hp(hp)), grad_scale.data_ptr())
+             w_out.data_ptr(), S, _addresses(contribs), _groups(contribs, replicas),
+             _opts(replicas, round_to_reduce_dtype, scale, keep_working_shard), code,
+             ctypes.byref(_hp(hp)), grad_scale.data_ptr())
 
 
 def _contributions(contribs, S) -> int:
     """The element type of contributions of S elements each."""
     if not contribs:
         return ZS_F32
-    code = _dtype_code(contribs[0])
-    for i, c in enumerate(contribs):
-        _dev(c, f"contribs[{i}]")
-        if c.numel() != S or _dtype_code(c) != code:
-            raise ValueError("contributions must share one dtype and hold S elements")
+    code, dtype = _dtype_code(contribs[0]), contribs[0].dtype
+    # one pass over all of them, then the failing one for the message
+    if not all([t.is_cuda and t.dtype == dtype and t.numel() == S and t.is_contiguous()
+                for t in contribs]):
+        for i, c in enumerate(contribs):
+            _dev(c, f"contribs[{i}]")
+            if c.numel() != S or _dtype_code(c) != code:
+                raise ValueError("contributions must share one dtype and hold S elements")
     return code
+
+
+def _one_device(ts: Sequence, what: str):
+    """_same_device for tensors that are known to be on devices."""
+    if len({t.get_device() for t in ts}) > 1:
+        _same_device(ts, what)
+
+
+def _opts(replicas, round_to_reduce_dtype, scale, keep_working_shard=False):
+    """zs_reduce_opts, or None for the flat reduce."""
+    if replicas == 1 and not round_to_reduce_dtype and scale == 0 and not keep_working_shard:
+        return None
+    return ctypes.byref(zs_reduce_opts(int(replicas), 1 if round_to_reduce_dtype else 0, float(scale),
+                                       ZS_W_KEEP if keep_working_shard else ZS_W_STREAM, 0))
+
+
+def _addresses(ts: Sequence):
+    return (ctypes.c_void_p * max(1, len(ts)))(*[t.data_ptr() for t in ts])
 
 
 # ---------------------------------------------------------- 8-bit matrices
@@ -1064,8 +1091,11 @@ class F8Matrix:
         self.codes, self.scales = codes, scales
         self.rows, self.cols, self.type, self.block_rows = int(rows), int(cols), int(type), int(block_rows)
         self.device = codes.device
-        self._as_parameter_ = ctypes.pointer(zs_f8_matrix(
-            codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, self.type, self.block_rows))
+        self._c = ctypes.byref(zs_f8_matrix(codes.data_ptr(), scales.data_ptr(), self.rows, self.cols,
+                                            self.type, self.block_rows))
+
+    def get_device(self) -> int:
+        return self.codes.get_device()
 
     @classmethod
     def empty(cls, rows: int, cols: int, type: int = ZS_E4M3, block_rows: int = 1,
@@ -1081,12 +1111,21 @@ def _matrix(t, what: str, rows: int = None, cols: int = None):
     """A device matrix whose rows are contiguous: (its element type, row stride)."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a device (cuda/HIP) tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} must be a matrix with contiguous rows")
-    if rows is not None and tuple(t.shape) != (rows, cols):
+    r, c = shape
+    if rows is not None and (r != rows or c != cols):
         raise ValueError(f"{what} must be {rows} x {cols}")
+    ld, one = t.stride()
+    if c > 1 and one != 1:
+        raise ValueError(f"{what} must be a matrix with contiguous rows")
     # a matrix of one row has any stride, and may have one below its columns
-    return _dtype_code(t), t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return _dtype_code(t), ld if r > 1 else max(c, 1)
+
+
+def _c(x):
+    return None if x is None else x._c
 
 
 def _quantized_shape(out, out_t):
@@ -1099,8 +1138,8 @@ def zs_quantize_f8(x, out: F8Matrix = None, out_t: F8Matrix = None, stream=None)
     """x (a bf16 or float32 matrix, its rows contiguous) to 8 bits: as it is (out),
     transposed (out_t, whose blocks run along x's columns) or both from one read."""
     code, ld = _matrix(x, "x", *_quantized_shape(out, out_t))
-    _same_device([x] + [o for o in (out, out_t) if o is not None], "zs_quantize_f8")
-    _enqueue(load().zs_quantize_f8, x, stream, x.data_ptr(), code, ld, out, out_t)
+    _one_device([x] + [o for o in (out, out_t) if o is not None], "zs_quantize_f8")
+    _enqueue(load().zs_quantize_f8, x, stream, x.data_ptr(), code, ld, _c(out), _c(out_t))
 
 
 def zs_gather_matrix_f8(shards: Sequence, offset: int, out: F8Matrix = None, out_t: F8Matrix = None,
@@ -1114,37 +1153,38 @@ def zs_gather_matrix_f8(shards: Sequence, offset: int, out: F8Matrix = None, out
     _quantized_shape(out, out_t)
     S = shards[0].numel()
     code = _contributions(shards, S)
-    _same_device(shards + [o for o in (out, out_t) if o is not None], "zs_gather_matrix_f8")
-    _enqueue(load().zs_gather_matrix_f8, shards[0], stream, _ptr_array(shards), len(shards), S, code,
-             int(offset), out, out_t)
+    _one_device(shards + [o for o in (out, out_t) if o is not None], "zs_gather_matrix_f8")
+    _enqueue(load().zs_gather_matrix_f8, shards[0], stream, _addresses(shards), len(shards), S, code,
+             int(offset), _c(out), _c(out_t))
 
 
 def zs_dequantize_f8(x: F8Matrix, out, stream=None) -> None:
     """out (a bf16 or float32 matrix, its rows contiguous) = the values of x."""
     code, ld = _matrix(out, "out", x.rows, x.cols)
-    _same_device((x, out), "zs_dequantize_f8")
-    _enqueue(load().zs_dequantize_f8, out, stream, x, code, out.data_ptr(), ld)
+    _one_device((x, out), "zs_dequantize_f8")
+    _enqueue(load().zs_dequantize_f8, out, stream, x._c, code, out.data_ptr(), ld)
 
 
-def _f8_workspace(f, M, N, K) -> int:
+@functools.lru_cache(maxsize=None)
+def _f8_workspace(name: str, M: int, N: int, K: int) -> int:
     n = ctypes.c_int64()
-    _check(f(int(M), int(N), int(K), ctypes.byref(n)))
+    _check(getattr(load(), name)(M, N, K, ctypes.byref(n)))
     return n.value
 
 
 def zs_matmul_f8_workspace(M: int, N: int, K: int) -> int:
     """Bytes of workspace of zs_matmul_f8 for a of M x K and b of N x K (may be 0)."""
-    return _f8_workspace(load().zs_matmul_f8_workspace, M, N, K)
+    return _f8_workspace("zs_matmul_f8_workspace", int(M), int(N), int(K))
 
 
 def zs_linear_f8_workspace(M: int, N: int, K: int) -> int:
     """Bytes of workspace of zs_linear_f8 for x of M x K and w of N x K."""
-    return _f8_workspace(load().zs_linear_f8_workspace, M, N, K)
+    return _f8_workspace("zs_linear_f8_workspace", int(M), int(N), int(K))
 
 
 def zs_linear_f8_backward_workspace(M: int, N: int, K: int) -> int:
     """Bytes of workspace of zs_linear_f8_backward for dy of M x N and x of M x K."""
-    return _f8_workspace(load().zs_linear_f8_backward_workspace, M, N, K)
+    return _f8_workspace("zs_linear_f8_backward_workspace", int(M), int(N), int(K))
 
 
 def _workspace(workspace, need: int):
@@ -1170,23 +1210,24 @@ def zs_matmul_f8(a: F8Matrix, b: F8Matrix, c, accumulate: bool = False, workspac
     if a.cols != b.cols:
         raise ValueError("a and b must have the same number of columns")
     ws = _workspace(workspace, zs_matmul_f8_workspace(a.rows, b.rows, a.cols))
-    _same_device([a, b, c] + ([] if workspace is None else [workspace]), "zs_matmul_f8")
-    _enqueue(load().zs_matmul_f8, c, stream, a, b, code, c.data_ptr(), ld, 1 if accumulate else 0, ws)
+    _one_device([a, b, c] + ([] if workspace is None else [workspace]), "zs_matmul_f8")
+    _enqueue(load().zs_matmul_f8, c, stream, a._c, b._c, code, c.data_ptr(), ld, 1 if accumulate else 0, ws)
 
 
-def zs_linear_f8(x, w: F8Matrix, y, workspace, type: int = ZS_E4M3, stream=None) -> None:
+def zs_linear_f8(x, w: F8Matrix, y, workspace=None, type: int = ZS_E4M3, stream=None) -> None:
     """y (M x N, bf16 or float32) = Q(x) w^T: x (M x K, bf16 or float32) quantised to
     8-bit codes of `type` with a scale for each 128 elements of a row, times the 8-bit
     weights w (N x K). workspace: uint8 device tensor of zs_linear_f8_workspace(M, N, K)
-    bytes, zeroed once; one for each of calls that may run at the same time."""
+    bytes (0 for few rows), zeroed once; one for each of calls that may run at the same
+    time."""
     code, ldx = _matrix(x, "x")
     if x.shape[1] != w.cols:
         raise ValueError(f"x must have {w.cols} columns")
     M = x.shape[0]
     y_code, ldy = _matrix(y, "y", M, w.rows)
     ws = _workspace(workspace, zs_linear_f8_workspace(M, w.rows, w.cols))
-    _same_device((x, w, y, workspace), "zs_linear_f8")
-    _enqueue(load().zs_linear_f8, y, stream, x.data_ptr(), code, M, ldx, int(type), w, y_code,
+    _one_device([x, w, y] + ([] if workspace is None else [workspace]), "zs_linear_f8")
+    _enqueue(load().zs_linear_f8, y, stream, x.data_ptr(), code, M, ldx, int(type), w._c, y_code,
              y.data_ptr(), ldy, ws)
 
 
@@ -1218,9 +1259,9 @@ def zs_linear_f8_backward(dy, x, w_t: F8Matrix, dx, dw, workspace, grad_type: in
         args["x"] = (x.data_ptr(), ldx)
         used += [x, dw]
     ws = _workspace(workspace, zs_linear_f8_backward_workspace(M, N, K))
-    _same_device(used, "zs_linear_f8_backward")
+    _one_device(used, "zs_linear_f8_backward")
     _enqueue(load().zs_linear_f8_backward, dy, stream, dy.data_ptr(), lddy, *args["x"], code, M, N, K,
-             int(grad_type), w_t if dx is not None else None, *args["dx"], *args["dw"],
+             int(grad_type), w_t._c if dx is not None else None, *args["dx"], *args["dw"],
              1 if accumulate else 0, ws)
 
 

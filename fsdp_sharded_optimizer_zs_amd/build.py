@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzs.so")
 SOURCES = ("zs_api.cpp", "zs_pipeline.cpp", "zs_ckpt.cpp", "zs_host.cpp", "zs_step.hip",
            "zs_move.hip", "zs_diag.hip", "zs_static.hip", "zs_multi.cpp", "zs_multi.hip",
-           "zs_mx4.hip", "zs_f8.cpp", "zs_f8_quant.hip", "zs_f8_gemm.hip")
+           "zs_mx4.hip", "zs_f8.cpp", "zs_f8_quant.hip", "zs_f8_gemm.hip",
+           "zs_f8_few.hip")
 
 # -ffp-contract=off: no fused multiply-add in the step's arithmetic;
 # correctly rounded fp32 divide and sqrt (the HIP default, stated);

@@ -143,9 +143,16 @@ F8Operand operand(const zs_f8_matrix& x) {
                      x.block_rows == 1 ? 0 : 7};
 }
 
-// A checked product.
+// A checked product. With x, a's codes are still to be made: of rows x cols values of dtype
+// `src`, which only products with few rows take.
+struct Values {
+    const void* x;
+    int64_t ldx;
+    int src;
+};
 hipError_t product(const zs_f8_matrix& a, const zs_f8_matrix& b, int dtype, void* c, int64_t ldc,
-                   int accumulate, uint32_t* counts, void* partial, hipStream_t stream) {
+                   int accumulate, uint32_t* counts, void* partial, hipStream_t stream,
+                   const Values* values = nullptr) {
     const F8Plan plan = f8_plan(a.rows, b.rows, a.cols);
     F8Product p{};
     p.a = operand(a);
@@ -159,7 +166,19 @@ hipError_t product(const zs_f8_matrix& a, const zs_f8_matrix& b, int dtype, void
     p.splits = plan.splits;
     p.counts = counts;
     p.partial = static_cast<float*>(partial);
+    if (plan.tm == kF8Few) {
+        p.tiles_n = plan.tn;
+        if (values != nullptr) p.x = values->x, p.ldx = values->ldx, p.cols = a.cols;
+        return launch_few_f8(p, values != nullptr ? values->src : 0, a.type, b.type, dtype, stream);
+    }
     return launch_matmul_f8(p, plan, a.type, b.type, dtype, stream);
+}
+
+// Whether a linear layer's forward pass makes its codes on the way.
+bool is_few(int64_t M, int64_t N, int64_t K) { return f8_plan(M, N, K).tm == kF8Few; }
+
+int64_t linear_bytes(int64_t M, int64_t N, int64_t K) {
+    return is_few(M, N, K) ? 0 : kF8CountBytes + partial_bytes(M, N, K) + placed_bytes(M, K);
 }
 
 zs_status check_product_size(const char* who, int64_t M, int64_t N, int64_t K) {
@@ -302,7 +321,7 @@ ZS_EXPORT zs_status zs_linear_f8_workspace(int64_t M, int64_t N, int64_t K, int6
     if (st == ZS_OK) st = check_sizes(who, "w", N, K);
     if (st != ZS_OK) return st;
     if (bytes == nullptr) return fail(ZS_EINVAL, "%s: bytes is NULL", who);
-    *bytes = kF8CountBytes + partial_bytes(M, N, K) + placed_bytes(M, K);
+    *bytes = linear_bytes(M, N, K);
     return ok();
 }
 
@@ -322,7 +341,7 @@ ZS_EXPORT zs_status zs_linear_f8(const void* x, int32_t dtype, int64_t M, int64_
     Range rx, ry;
     if (st == ZS_OK) st = check_dense(who, "x", x, es, M, K, ldx, &rx);
     if (st == ZS_OK) st = check_dense(who, "y", y, ys, M, N, ldy, &ry);
-    const int64_t need = kF8CountBytes + partial_bytes(M, N, K) + placed_bytes(M, K);
+    const int64_t need = linear_bytes(M, N, K);
     if (st == ZS_OK) st = check_workspace(who, workspace, need);
     if (st != ZS_OK) return st;
     if (M == 0 || N == 0) return ok();
@@ -331,6 +350,12 @@ ZS_EXPORT zs_status zs_linear_f8(const void* x, int32_t dtype, int64_t M, int64_
         return fail(ZS_EALIAS, "%s: y overlaps x, w or the workspace", who);
     if (overlap(rx, rw) || meets(*w, rw))
         return fail(ZS_EALIAS, "%s: the workspace overlaps x or w", who);
+    if (is_few(M, N, K)) {
+        const zs_f8_matrix a{nullptr, nullptr, M, K, type, 1};
+        const Values values{x, ldx, dtype};
+        return hip_status(product(a, *w, y_dtype, y, ldy, 0, nullptr, nullptr, stream, &values),
+                          who);
+    }
     uint8_t* const partial = static_cast<uint8_t*>(workspace) + kF8CountBytes;
     uint8_t* at = partial + partial_bytes(M, N, K);
     const zs_f8_matrix q = place(at, M, K, type);

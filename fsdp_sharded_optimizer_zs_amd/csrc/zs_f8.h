@@ -49,11 +49,16 @@ struct F8Product {
     int64_t ldc;
     int blocks;  // of 128 along K
     int accumulate;
-    int tiles_m, tiles_n, splits;
+    int tiles_m, tiles_n, splits;  // few rows: tiles_n is the plan's tn
     float* partial;    // splits > 1
     uint32_t* counts;  // likewise, 0 between calls
+    const void* x;     // few rows whose codes are made on the way: a's values, row r from
+    int64_t ldx, cols; // element r * ldx on (of a, only rows is read then)
 };
 hipError_t launch_matmul_f8(const F8Product& p, const F8Plan& plan, int type_a, int type_b,
                             int dtype, hipStream_t stream);
+// Up to kF8Few rows of a; src: 0, a in codes, or the type of the values x.
+hipError_t launch_few_f8(const F8Product& p, int src, int type_a, int type_b, int dtype,
+                         hipStream_t stream);
 
 }  // namespace zs

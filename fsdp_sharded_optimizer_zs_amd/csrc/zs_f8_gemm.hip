@@ -16,8 +16,7 @@
 // The matrix instruction's first operand is b and its second a: a lane then holds 4
 // neighbouring columns n of C.
 
-#include "zs_f8.h"
-#include "zs_math.h"
+#include "zs_f8_dev.h"
 
 #pragma clang fp contract(off)
 
@@ -25,92 +24,6 @@ namespace zs {
 namespace {
 
 constexpr int kB = kF8Block;
-
-#define ZS_GLOBAL __attribute__((address_space(1)))
-#define ZS_LDS __attribute__((address_space(3)))
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
-typedef ZS_GLOBAL f32x4_u g_f32x4;
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
-typedef ZS_GLOBAL u32x2_u g_u32x2;
-typedef ZS_GLOBAL u32x4_u g_u32x4;
-typedef ZS_GLOBAL uint16_t g_u16;
-typedef ZS_GLOBAL float g_f32;
-
-template <typename G, typename P>
-__device__ __forceinline__ G* global(P* p) {
-    return reinterpret_cast<G*>(reinterpret_cast<uintptr_t>(p));
-}
-
-__device__ __forceinline__ float scale_value(uint32_t s) {
-    s &= 255u;
-    return s == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(s == 0 ? 0x400000u : s << 23);
-}
-
-// 8 codes, words w0 and w1, as bf16 times the scale.
-template <int TYPE>
-__device__ __forceinline__ bf16x8 widen(int w0, int w1, float two) {
-    bf16x2 h[4];
-    if constexpr (TYPE == ZS_E4M3) {
-        h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(uint32_t(w0), two, false);
-        h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(uint32_t(w0), two, true);
-        h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(uint32_t(w1), two, false);
-        h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(uint32_t(w1), two, true);
-    } else {
-        h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(uint32_t(w0), two, false);
-        h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(uint32_t(w0), two, true);
-        h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(uint32_t(w1), two, false);
-        h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(uint32_t(w1), two, true);
-    }
-    return bf16x8{h[0][0], h[0][1], h[1][0], h[1][1], h[2][0], h[2][1], h[3][0], h[3][1]};
-}
-
-template <int TYPE>
-constexpr int kFormat = TYPE == ZS_E4M3 ? 0 : 1;
-
-// 4 neighbouring elements of a row of C.
-template <int DT>
-__device__ __forceinline__ void put4(const F8Product& p, int64_t m, int64_t n, int64_t N, f32x4 v) {
-    const int64_t at = m * p.ldc + n;
-    const int live = N - n >= 4 ? 4 : int(N - n);
-    if constexpr (DT == ZS_BF16) {
-        g_u16* c = global<g_u16>(p.c) + at;
-        if (p.accumulate) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < live) v[e] += __uint_as_float(uint32_t(c[e]) << 16);
-        }
-        const u32x2 w{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-        if (live == 4) {
-            *reinterpret_cast<g_u32x2*>(c) = w;
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (e < live) c[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
-    } else {
-        g_f32* c = global<g_f32>(p.c) + at;
-        if (p.accumulate) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < live) v[e] += c[e];
-        }
-        if (live == 4) {
-            *reinterpret_cast<g_f32x4*>(c) = v;
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (e < live) c[e] = v[e];
-    }
-}
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -121,13 +34,13 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                  :
                  : "s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {

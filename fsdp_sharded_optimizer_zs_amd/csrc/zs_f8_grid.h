@@ -36,6 +36,16 @@ struct F8Plan {
 constexpr int64_t kF8Counts = 1024;
 constexpr int64_t kF8CountBytes = 2 * kF8Counts * 4;
 
+// Products with few rows of a: workgroups of 8 wavefronts with an equal share of b's rows
+// each (F8Plan's tn; 4 at least), on every CU one; `splits` of the wavefronts take 16 rows
+// together. All of a is in LDS, in a kernel that takes little of it or nearly all.
+constexpr int kF8Few = 16, kF8FewWaves = 8;
+constexpr int64_t kF8FewSums = 2 * kF8FewWaves * 64 * 16;
+constexpr int64_t kF8FewLdsSmall = 49152, kF8FewLds = 155648;
+constexpr int64_t f8_few_lds(int64_t M, int64_t blocks) {
+    return kF8FewSums + M * (blocks * kF8Block + 16 + blocks);
+}
+
 // Tiles of 256, 128 or 64 squared: the larger one moves less through LDS for each product,
 // the smaller ones fill 256 CUs with less. The costs of a step of 128 along K for each tile
 // that a CU takes are measured, in hundredths of a microsecond (C in fp32: 290, 93 and 33, in
@@ -49,6 +59,13 @@ inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
     const int side[3] = {256, 128, 64}, cost[3] = {150, 55, 22};
     F8Plan best{};
     int64_t least = -1;
+    const int64_t blocks = f8_ceil(K, kF8Block);
+    if (M <= kF8Few && f8_few_lds(M, blocks) <= kF8FewLds) {
+        const int64_t rows = f8_ceil(N, kCus);
+        int s = 1;
+        while (s < kF8FewWaves && s * 8 <= blocks) s *= 2;
+        return F8Plan{kF8Few, int(rows < 4 ? 4 : rows), s, 1, f8_ceil(N, rows < 4 ? 4 : rows)};
+    }
     for (int i = 0; i < 3; ++i) {
         const F8Plan p{side[i], side[i], 1, f8_ceil(M, side[i]), f8_ceil(N, side[i])};
         const int64_t c = f8_ceil(p.tiles_m * p.tiles_n, kCus) * cost[i];
@@ -57,14 +74,14 @@ inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = best.tiles_m * best.tiles_n;
     if (best.tm == 64 && tiles > 0) {
         int64_t s = kCus / tiles;
-        const int64_t parts = f8_ceil(K, kF8Block) / 16;
+        const int64_t parts = blocks / 16;
         s = s < parts ? s : parts;
         best.splits = int(s < 1 ? 1 : (s < 32 ? s : 32));
     }
     return best;
 }
 inline int64_t f8_partial_bytes(const F8Plan& p) {
-    return p.splits > 1 ? p.tiles_m * p.tiles_n * p.splits * p.tm * p.tn * 4 : 0;
+    return p.splits > 1 && p.tm != kF8Few ? p.tiles_m * p.tiles_n * p.splits * p.tm * p.tn * 4 : 0;
 }
 inline int64_t f8_matmul_workspace(int64_t M, int64_t N, int64_t K) {
     const int64_t n = f8_partial_bytes(f8_plan(M, N, K));

@@ -186,7 +186,7 @@ def test_matmul_refusals(lib):
     assert matmul(lib, b=mat(type=9)) == zs.ZS_EUNSUPPORTED
     big = mat(rows=1 << 26), mat(A + 0x40000000, A + 0x50000000, 1 << 26, 256)
     for kw in (dict(a=None), dict(b=mat(cols=128)), dict(c=None), dict(c=X + 1), dict(ldc=31), dict(acc=2),
-               dict(a=mat(codes=A + 1)), dict(ws=A + 0x60000008, a=mat(rows=1, cols=2**20),
+               dict(a=mat(codes=A + 1)), dict(ws=A + 0x60000008, a=mat(rows=20, cols=2**20),
                                               b=mat(A + 0x40000000, A + 0x50000000, 1, 2**20)),
                dict(a=big[0], b=big[1], ldc=1 << 26)):
         assert matmul(lib, **kw) == zs.ZS_EINVAL, kw
@@ -201,7 +201,7 @@ def test_matmul_refusals(lib):
     assert matmul(lib, b=mat(rows=0, codes=None), c=None) == zs.ZS_OK
 
 
-def linear(lib, x=X, dtype=zs.ZS_BF16, M=8, ldx=256, type=zs.ZS_E4M3, w=OUT, yt=zs.ZS_BF16,
+def linear(lib, x=X, dtype=zs.ZS_BF16, M=40, ldx=256, type=zs.ZS_E4M3, w=OUT, yt=zs.ZS_BF16,
            y=A + 0x40000000, ldy=64, ws=A + 0x60000000):
     return lib.zs_linear_f8(x, dtype, M, ldx, type, ref(w), yt, y, ldy, ws, None)
 
@@ -216,6 +216,12 @@ def test_linear_refusals(lib):
     for kw in (dict(y=X), dict(y=A), dict(ws=X), dict(ws=A + 0x40000000), dict(ws=A + 0x10000000)):
         assert linear(lib, **kw) == zs.ZS_EALIAS, kw
     assert linear(lib, M=0, x=None, y=None) == zs.ZS_OK
+    # few rows need no workspace, and are refused what others are
+    assert zs.zs_linear_f8_workspace(16, 64, 256) == 0 < zs.zs_linear_f8_workspace(17, 64, 256)
+    for kw in (dict(x=None), dict(ldx=255), dict(y=None), dict(w=None)):
+        assert linear(lib, M=16, ws=None, **kw) == zs.ZS_EINVAL, kw
+    for y in (X, A, A + 0x10000000):
+        assert linear(lib, M=16, ws=None, y=y) == zs.ZS_EALIAS
 
 
 WT = mat(rows=256, cols=64)       # K x N of dy 8 x 64, x 8 x 256
@@ -315,7 +321,9 @@ def test_plans_cover_the_work_and_fit_the_workspace(tmp_path):
         tm, tn, splits, tiles_m, tiles_n, partial, need, counts, count_bytes, aligned, scalar = v
         assert tiles_m * tm >= M and tiles_n * tn >= N and (tiles_m - 1) * tm < max(M, 1)
         assert 1 <= splits <= max(1, -(-K // 128))
-        if splits > 1:
+        if tm == 16:
+            assert M <= 16 and need == partial == 0 and splits in (1, 2, 4, 8) and tiles_n <= 256
+        elif splits > 1:
             assert tiles_m * tiles_n <= counts
             assert partial == tiles_m * tiles_n * splits * tm * tn * 4 and need >= count_bytes + partial
         assert count_bytes >= 2 * counts * 4 and need < 2**31
