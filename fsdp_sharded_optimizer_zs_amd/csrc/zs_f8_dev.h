@@ -224,5 +224,30 @@ __device__ __forceinline__ void put4(const F8Product& p, int64_t m, int64_t n, i
     }
 }
 
+// 16 bytes a lane from base + offset to LDS, lane l's at lds + 16 l. Written as assembly so
+// that the compiler's own LDS reads do not wait for it; `arrived` and a barrier do. (The
+// instruction takes the LDS address from m0, one wait state after it is written.)
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((ZS_LDS const void*)(p)));
+}
+
+template <int N>
+__device__ __forceinline__ void arrived_but() {  // all but the last N loads
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
 }  // namespace
 }  // namespace zs

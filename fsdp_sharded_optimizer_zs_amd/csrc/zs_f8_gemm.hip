@@ -27,31 +27,6 @@ constexpr int kB = kF8Block;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// 16 bytes a lane from base + offset to LDS, lane l's at lds + 16 l. Written as assembly so
-// that the compiler's own LDS reads do not wait for it; `arrived` and a barrier do. (The
-// instruction takes the LDS address from m0, one wait state after it is written.)
-__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(lds), "v"(offset), "s"(base)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-                 :
-                 : "s"(lds), "v"(offset), "s"(base)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return uint32_t(reinterpret_cast<uintptr_t>((ZS_LDS const void*)(p)));
-}
-
-template <int N>
-__device__ __forceinline__ void arrived_but() {  // all but the last N loads
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
-
 // TM x TN of C by WM x WN wavefronts, in 32 x 32 parts.
 template <int TM_, int TN_, int WM_, int WN_>
 struct Shape {

@@ -36,14 +36,14 @@ struct F8Plan {
 constexpr int64_t kF8Counts = 1024;
 constexpr int64_t kF8CountBytes = 2 * kF8Counts * 4;
 
-// Products with few rows of a: workgroups of 8 wavefronts with an equal share of b's rows
-// each (F8Plan's tn; 4 at least), on every CU one; `splits` of the wavefronts take 16 rows
-// together. All of a is in LDS, in a kernel that takes little of it or nearly all.
+// Products with few rows of a: workgroups of 8 reading wavefronts with an equal share of b's
+// rows each (F8Plan's tn; 4 at least), on every CU one; `splits` of the wavefronts take 16
+// rows together. LDS holds one or two groups of b for each wavefront, and all of a.
 constexpr int kF8Few = 16, kF8FewWaves = 8;
-constexpr int64_t kF8FewSums = 2 * kF8FewWaves * 64 * 16;
-constexpr int64_t kF8FewLdsSmall = 49152, kF8FewLds = 155648;
-constexpr int64_t f8_few_lds(int64_t M, int64_t blocks) {
-    return kF8FewSums + M * (blocks * kF8Block + 16 + blocks);
+constexpr int64_t kF8FewSums = 2 * kF8FewWaves * 64 * 16, kF8FewGroup = 16 * 512 + 256;
+constexpr int64_t kF8FewLds = 163840;
+constexpr int64_t f8_few_lds(int depth, int64_t M, int64_t blocks) {
+    return kF8FewWaves * depth * kF8FewGroup + kF8FewSums + M * (blocks * kF8Block + 16 + blocks);
 }
 
 // Tiles of 256, 128 or 64 squared: the larger one moves less through LDS for each product,
@@ -60,7 +60,7 @@ inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
     F8Plan best{};
     int64_t least = -1;
     const int64_t blocks = f8_ceil(K, kF8Block);
-    if (M <= kF8Few && f8_few_lds(M, blocks) <= kF8FewLds) {
+    if (M <= kF8Few && f8_few_lds(1, M, blocks) <= kF8FewLds) {
         const int64_t rows = f8_ceil(N, kCus);
         int s = 1;
         while (s < kF8FewWaves && s * 8 <= blocks) s *= 2;
