@@ -143,17 +143,9 @@ F8Operand operand(const zs_f8_matrix& x) {
                      x.block_rows == 1 ? 0 : 7};
 }
 
-// A checked product. With x, a's codes are still to be made: of rows x cols values of dtype
-// `src`, which only products with few rows take.
-struct Values {
-    const void* x;
-    int64_t ldx;
-    int src;
-};
-hipError_t product(const zs_f8_matrix& a, const zs_f8_matrix& b, int dtype, void* c, int64_t ldc,
-                   int accumulate, uint32_t* counts, void* partial, hipStream_t stream,
-                   const Values* values = nullptr) {
-    const F8Plan plan = f8_plan(a.rows, b.rows, a.cols);
+// A checked product as the kernels take it.
+F8Product product_of(const zs_f8_matrix& a, const zs_f8_matrix& b, void* c, int64_t ldc,
+                     int accumulate, const F8Plan& plan, uint32_t* counts, void* partial) {
     F8Product p{};
     p.a = operand(a);
     p.b = operand(b);
@@ -162,16 +154,19 @@ hipError_t product(const zs_f8_matrix& a, const zs_f8_matrix& b, int dtype, void
     p.blocks = int(f8_ceil(a.cols, kF8Block));
     p.accumulate = accumulate;
     p.tiles_m = int(plan.tiles_m);
-    p.tiles_n = int(plan.tiles_n);
+    p.tiles_n = plan.tm == kF8Few ? plan.tn : int(plan.tiles_n);
     p.splits = plan.splits;
     p.counts = counts;
     p.partial = static_cast<float*>(partial);
-    if (plan.tm == kF8Few) {
-        p.tiles_n = plan.tn;
-        if (values != nullptr) p.x = values->x, p.ldx = values->ldx, p.cols = a.cols;
-        return launch_few_f8(p, values != nullptr ? values->src : 0, a.type, b.type, dtype, stream);
-    }
-    return launch_matmul_f8(p, plan, a.type, b.type, dtype, stream);
+    return p;
+}
+
+hipError_t product(const zs_f8_matrix& a, const zs_f8_matrix& b, int dtype, void* c, int64_t ldc,
+                   int accumulate, uint32_t* counts, void* partial, hipStream_t stream) {
+    const F8Plan plan = f8_plan(a.rows, b.rows, a.cols);
+    const F8Product p = product_of(a, b, c, ldc, accumulate, plan, counts, partial);
+    if (plan.tm == kF8Few) return launch_few_f8(p, 0, a.type, b.type, dtype, stream);
+    return launch_matmul_f8(p, nullptr, plan.tm, a.type, b.type, dtype, stream);
 }
 
 // Whether a linear layer's forward pass makes its codes on the way.
@@ -180,6 +175,8 @@ bool is_few(int64_t M, int64_t N, int64_t K) { return f8_plan(M, N, K).tm == kF8
 int64_t linear_bytes(int64_t M, int64_t N, int64_t K) {
     return is_few(M, N, K) ? 0 : kF8CountBytes + partial_bytes(M, N, K) + placed_bytes(M, K);
 }
+
+int64_t groups_of(const F8Plan& p) { return p.tiles_m * p.tiles_n * p.splits; }
 
 zs_status check_product_size(const char* who, int64_t M, int64_t N, int64_t K) {
     if (f8_ceil(M, 64) * f8_ceil(N, 64) > kMaxGrid)
@@ -352,9 +349,9 @@ ZS_EXPORT zs_status zs_linear_f8(const void* x, int32_t dtype, int64_t M, int64_
         return fail(ZS_EALIAS, "%s: the workspace overlaps x or w", who);
     if (is_few(M, N, K)) {
         const zs_f8_matrix a{nullptr, nullptr, M, K, type, 1};
-        const Values values{x, ldx, dtype};
-        return hip_status(product(a, *w, y_dtype, y, ldy, 0, nullptr, nullptr, stream, &values),
-                          who);
+        F8Product p = product_of(a, *w, y, ldy, 0, f8_plan(M, N, K), nullptr, nullptr);
+        p.x = x, p.ldx = ldx, p.cols = K;
+        return hip_status(launch_few_f8(p, dtype, type, w->type, y_dtype, stream), who);
     }
     uint8_t* const partial = static_cast<uint8_t*>(workspace) + kF8CountBytes;
     uint8_t* at = partial + partial_bytes(M, N, K);
@@ -403,6 +400,8 @@ ZS_EXPORT zs_status zs_linear_f8_backward(const void* dy, int64_t lddy, const vo
     st = zs_linear_f8_backward_workspace(M, N, K, &need);
     if (st == ZS_OK) st = check_product_size(who, M, K, N);
     if (st == ZS_OK) st = check_product_size(who, N, K, M);
+    if (st == ZS_OK && (f8_tiles(M, N) >= (int64_t(1) << 30) || f8_tiles(M, K) >= (int64_t(1) << 30)))
+        st = fail(ZS_EINVAL, "%s: dy or x has too many elements", who);
     if (st != ZS_OK) return st;
     if (dx == nullptr && dw == nullptr && M > 0 && N > 0 && K > 0)
         return fail(ZS_EINVAL, "%s: dx and dw are both NULL", who);
@@ -439,16 +438,30 @@ ZS_EXPORT zs_status zs_linear_f8_backward(const void* dy, int64_t lddy, const vo
     uint8_t* at = partial_dw + partial_bytes(N, K, M);
     const zs_f8_matrix g = place(at, M, N, dy_type), g_t = place(at, N, M, dy_type),
                        x_t = place(at, K, M, ZS_E4M3);
+    if (M > 0 && N > 0) {
+        const F8Quant from_dy{dy, lddy, M, N, dtype, out_of(want_dx ? &g : nullptr),
+                              out_of(want_dw ? &g_t : nullptr)};
+        const F8Quant from_x{x, ldx, M, K, dtype, out_of(nullptr), out_of(&x_t)};
+        const hipError_t e = want_dw ? launch_quantize2_f8(from_dy, from_x, stream)
+                                     : launch_quantize_f8(from_dy, 1, stream);
+        if (e != hipSuccess) return hip_status(e, who);
+    }
+    // both products in one launch if they take the same kernel
+    const F8Plan plan_dx = f8_plan(M, K, N), plan_dw = f8_plan(N, K, M);
+    if (want_dx && want_dw && plan_dx.tm == plan_dw.tm && plan_dx.tm != kF8Few &&
+        dx_dtype == dw_dtype && w_t->type == ZS_E4M3 &&
+        groups_of(plan_dx) + groups_of(plan_dw) <= kMaxGrid) {
+        const F8Product for_dx = product_of(g, *w_t, dx, lddx, 0, plan_dx, counts, partial);
+        const F8Product for_dw = product_of(g_t, x_t, dw, lddw, accumulate, plan_dw,
+                                            counts + kF8Counts, partial_dw);
+        return hip_status(launch_matmul_f8(for_dx, &for_dw, plan_dx.tm, dy_type, ZS_E4M3, dx_dtype,
+                                           stream),
+                          who);
+    }
     hipError_t e = hipSuccess;
-    if (M > 0 && N > 0 && (want_dx || want_dw))
-        e = launch_quantize_f8(F8Quant{dy, lddy, M, N, dtype, out_of(want_dx ? &g : nullptr),
-                                       out_of(want_dw ? &g_t : nullptr)},
-                               1, stream);
-    if (e == hipSuccess && want_dw && M > 0)
-        e = launch_quantize_f8(F8Quant{x, ldx, M, K, dtype, out_of(nullptr), out_of(&x_t)}, 1,
-                               stream);
-    if (e == hipSuccess && want_dx) e = product(g, *w_t, dx_dtype, dx, lddx, 0, counts, partial, stream);
+    if (want_dx) e = product(g, *w_t, dx_dtype, dx, lddx, 0, counts, partial, stream);
     if (e == hipSuccess && want_dw)
-        e = product(g_t, x_t, dw_dtype, dw, lddw, accumulate, counts + kF8Counts, partial_dw, stream);
+        e = product(g_t, x_t, dw_dtype, dw, lddw, accumulate, counts + kF8Counts, partial_dw,
+                    stream);
     return hip_status(e, who);
 }

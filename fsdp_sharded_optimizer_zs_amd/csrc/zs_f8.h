@@ -29,6 +29,8 @@ struct F8Shards {
     double inv_s;  // 1 / S
 };
 hipError_t launch_quantize_f8(const F8Quant& q, int block_rows, hipStream_t stream);
+// Two matrices in 1 x 128 blocks, in one launch.
+hipError_t launch_quantize2_f8(const F8Quant& one, const F8Quant& two, hipStream_t stream);
 hipError_t launch_gather_f8(const F8Quant& q, const F8Shards& src, int block_rows,
                             hipStream_t stream);
 hipError_t launch_dequantize_f8(const uint8_t* codes, const uint8_t* scales, int block_rows,
@@ -55,8 +57,10 @@ struct F8Product {
     const void* x;     // few rows whose codes are made on the way: a's values, row r from
     int64_t ldx, cols; // element r * ldx on (of a, only rows is read then)
 };
-hipError_t launch_matmul_f8(const F8Product& p, const F8Plan& plan, int type_a, int type_b,
-                            int dtype, hipStream_t stream);
+// side: of the tiles, the plan's tm. two: a second product of the same tiles and types in the
+// same launch, or nullptr.
+hipError_t launch_matmul_f8(const F8Product& p, const F8Product* two, int side, int type_a,
+                            int type_b, int dtype, hipStream_t stream);
 // Up to kF8Few rows of a; src: 0, a in codes, or the type of the values x.
 hipError_t launch_few_f8(const F8Product& p, int src, int type_a, int type_b, int dtype,
                          hipStream_t stream);

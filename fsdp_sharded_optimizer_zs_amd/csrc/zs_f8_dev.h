@@ -106,10 +106,24 @@ __device__ __forceinline__ uint32_t row_max(uint32_t u) {
     u = max_with<0x141>(u);    // row_half_mirror
     return max_with<0x140>(u); // row_mirror
 }
-// Over lanes l % 16 = const.
+// Over lanes l % 16 = const: gfx950 swaps halves and rows of 16 lanes of two registers, which
+// for two copies of one leaves both partners in every lane.
+template <typename F>
+__device__ __forceinline__ uint32_t over_rows(uint32_t u, F larger) {
+    const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    u = larger(h[0], h[1]);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return larger(r[0], r[1]);
+}
 __device__ __forceinline__ uint32_t col_max(uint32_t u) {
-    u = max_u(u, __shfl_xor(u, 16, 64));
-    return max_u(u, __shfl_xor(u, 32, 64));
+    return over_rows(u, [](uint32_t a, uint32_t b) { return max_u(a, b); });
+}
+__device__ __forceinline__ uint32_t col_max_pair(uint32_t u) {  // of the halves apart
+    return over_rows(u, [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(uint32_t,
+                                  __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                            __builtin_bit_cast(u16x2, b)));
+    });
 }
 
 __device__ __forceinline__ int scale_of(uint32_t u, int type) {
@@ -141,21 +155,30 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t w, uint32_t pair, float t
                                   __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(old, h, two, HI));
 }
 
-// 4 codes of values given as pairs of bf16 or as floats, under scale byte s.
-template <int TYPE>
+// Whether a block's codes take more than the instruction: it is not finite, or its scale
+// byte is 1, where magnitudes may be subnormal (not a block of zeros).
+__device__ __forceinline__ bool is_special(uint32_t u, int s) {
+    return s == 255 || (s == 1 && u != 0);
+}
+
+// 4 codes of values given as pairs of bf16 or as floats, under scale byte s. ANY: also of
+// special blocks.
+template <int TYPE, bool ANY = true>
 __device__ __forceinline__ uint32_t four_codes(float a, float b, float c, float d, int s) {
-    if (s == 255) return 0;
     float two = __uint_as_float(uint32_t(s) << 23);
-    if (s == 1) {
-        a = __builtin_ldexpf(a, 126), b = __builtin_ldexpf(b, 126);
-        c = __builtin_ldexpf(c, 126), d = __builtin_ldexpf(d, 126);
-        two = 1.0f;
+    if constexpr (ANY) {
+        if (s == 255) return 0;
+        if (s == 1) {
+            a = __builtin_ldexpf(a, 126), b = __builtin_ldexpf(b, 126);
+            c = __builtin_ldexpf(c, 126), d = __builtin_ldexpf(d, 126);
+            two = 1.0f;
+        }
     }
     return two_codes<TYPE, true>(two_codes<TYPE, false>(0u, a, b, two), c, d, two);
 }
-template <int TYPE>
+template <int TYPE, bool ANY = true>
 __device__ __forceinline__ uint32_t four_codes(uint32_t ab, uint32_t cd, int s) {
-    if (s <= 1 || s == 255)
+    if (ANY && (s <= 1 || s == 255))
         return four_codes<TYPE>(bf16_lo(ab), bf16_hi(ab), bf16_lo(cd), bf16_hi(cd), s);
     const float two = __uint_as_float(uint32_t(s) << 23);
     return two_codes<TYPE, true>(two_codes<TYPE, false>(0u, ab, two), cd, two);

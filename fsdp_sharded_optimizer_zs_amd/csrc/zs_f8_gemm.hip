@@ -44,19 +44,19 @@ struct Shape {
                   "whole loads and parts");
 };
 
+// Workgroup `group` of p's tiles * splits.
 template <class S, int TA, int TB, int DT>
-__global__ __launch_bounds__(S::kThreads, 1) void matmul_kernel(F8Product p) {
+__device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, uint8_t* big) {
     constexpr bool EXACT = DT == ZS_F32;
     constexpr int TM = S::TM, TN = S::TN, W = S::W, MI = S::MI, NI = S::NI;
     constexpr int kHalfRow = S::kHalfRow, kHalf = S::kHalf, kOperand = TM * kHalfRow;
     constexpr int kScales = S::kRing, kScale = S::kScale, kLoads = S::kLoads;
-    __shared__ __attribute__((aligned(16))) uint8_t big[S::kLds];
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     // Each XCD takes a run of tiles, 8 rows of tiles deep; a tile's splits are neighbours.
     const unsigned total = unsigned(p.tiles_m) * unsigned(p.tiles_n) * unsigned(p.splits);
-    const unsigned xcd = blockIdx.x & 7u, q = total >> 3, rest = total & 7u;
-    const unsigned w = xcd * q + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
+    const unsigned xcd = group & 7u, q = total >> 3, rest = total & 7u;
+    const unsigned w = xcd * q + (xcd < rest ? xcd : rest) + (group >> 3);
     const unsigned t = w / unsigned(p.splits), split = w - t * unsigned(p.splits);
     const unsigned deep = 8, band = t / (deep * p.tiles_n);
     const unsigned rows = min(deep, unsigned(p.tiles_m) - band * deep);
@@ -331,32 +331,64 @@ __global__ __launch_bounds__(S::kThreads, 1) void matmul_kernel(F8Product p) {
     }
 }
 
+template <class S, int TA, int TB, int DT>
+__global__ __launch_bounds__(S::kThreads, 1) void matmul_kernel(F8Product p) {
+    __shared__ __attribute__((aligned(16))) uint8_t big[S::kLds];
+    matmul_tile<S, TA, TB, DT>(p, blockIdx.x, big);
+}
+// Two products in one launch: the first one's workgroups, then the second one's, which fill
+// what those leave idle at their end.
+template <class S, int TA, int TB, int DT>
+__global__ __launch_bounds__(S::kThreads, 1) void matmul2_kernel(F8Product one, F8Product two,
+                                                                 unsigned groups1) {
+    __shared__ __attribute__((aligned(16))) uint8_t big[S::kLds];
+    const bool is_one = blockIdx.x < groups1;
+    matmul_tile<S, TA, TB, DT>(is_one ? one : two, is_one ? blockIdx.x : blockIdx.x - groups1, big);
+}
+
+unsigned groups_of(const F8Product& p) {
+    return unsigned(int64_t(p.tiles_m) * p.tiles_n * p.splits);
+}
+
+// two: or nullptr
 template <class S, int TA, int TB>
-void launch_shape(const F8Product& p, int dtype, hipStream_t stream) {
-    const dim3 grid(unsigned(int64_t(p.tiles_m) * p.tiles_n * p.splits)), block(S::kThreads);
-    if (dtype == ZS_BF16)
-        hipLaunchKernelGGL((matmul_kernel<S, TA, TB, ZS_BF16>), grid, block, 0, stream, p);
-    else
-        hipLaunchKernelGGL((matmul_kernel<S, TA, TB, ZS_F32>), grid, block, 0, stream, p);
+void launch_shape(const F8Product& p, const F8Product* two, int dtype, hipStream_t stream) {
+    const dim3 block(S::kThreads);
+    const unsigned n = groups_of(p);
+    if (two == nullptr) {
+        if (dtype == ZS_BF16)
+            hipLaunchKernelGGL((matmul_kernel<S, TA, TB, ZS_BF16>), dim3(n), block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((matmul_kernel<S, TA, TB, ZS_F32>), dim3(n), block, 0, stream, p);
+    } else {
+        const dim3 grid(n + groups_of(*two));
+        if (dtype == ZS_BF16)
+            hipLaunchKernelGGL((matmul2_kernel<S, TA, TB, ZS_BF16>), grid, block, 0, stream, p,
+                               *two, n);
+        else
+            hipLaunchKernelGGL((matmul2_kernel<S, TA, TB, ZS_F32>), grid, block, 0, stream, p, *two,
+                               n);
+    }
 }
 
 template <int TA, int TB>
-void launch_types(const F8Product& p, const F8Plan& plan, int dtype, hipStream_t stream) {
-    if (plan.tm == 256) launch_shape<Shape<256, 256, 2, 4>, TA, TB>(p, dtype, stream);
-    else if (plan.tm == 128) launch_shape<Shape<128, 128, 2, 2>, TA, TB>(p, dtype, stream);
-    else launch_shape<Shape<64, 64, 2, 2>, TA, TB>(p, dtype, stream);
+void launch_types(const F8Product& p, const F8Product* two, int side, int dtype,
+                  hipStream_t stream) {
+    if (side == 256) launch_shape<Shape<256, 256, 2, 4>, TA, TB>(p, two, dtype, stream);
+    else if (side == 128) launch_shape<Shape<128, 128, 2, 2>, TA, TB>(p, two, dtype, stream);
+    else launch_shape<Shape<64, 64, 2, 2>, TA, TB>(p, two, dtype, stream);
 }
 
 }  // namespace
 
-hipError_t launch_matmul_f8(const F8Product& p, const F8Plan& plan, int type_a, int type_b,
-                            int dtype, hipStream_t stream) {
+hipError_t launch_matmul_f8(const F8Product& p, const F8Product* two, int side, int type_a,
+                            int type_b, int dtype, hipStream_t stream) {
     if (type_a == ZS_E4M3) {
-        if (type_b == ZS_E4M3) launch_types<ZS_E4M3, ZS_E4M3>(p, plan, dtype, stream);
-        else launch_types<ZS_E4M3, ZS_E5M2>(p, plan, dtype, stream);
+        if (type_b == ZS_E4M3) launch_types<ZS_E4M3, ZS_E4M3>(p, two, side, dtype, stream);
+        else launch_types<ZS_E4M3, ZS_E5M2>(p, two, side, dtype, stream);
     } else {
-        if (type_b == ZS_E4M3) launch_types<ZS_E5M2, ZS_E4M3>(p, plan, dtype, stream);
-        else launch_types<ZS_E5M2, ZS_E5M2>(p, plan, dtype, stream);
+        if (type_b == ZS_E4M3) launch_types<ZS_E5M2, ZS_E4M3>(p, two, side, dtype, stream);
+        else launch_types<ZS_E5M2, ZS_E5M2>(p, two, side, dtype, stream);
     }
     return hipGetLastError();
 }

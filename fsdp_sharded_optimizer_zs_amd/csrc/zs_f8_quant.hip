@@ -80,21 +80,74 @@ struct Shared {
     uint32_t whole[4];
 };
 
+// A lane's elements of a tile, rows 64 h + 16 w + 4 (l / 16) + i.
+template <int DT>
+using Part = Eight<DT>[2][4];
+
+// Codes of 8 elements of a row, and of 4 rows of column e.
+template <int DT, int TYPE, bool ANY>
+__device__ __forceinline__ u32x2 row_codes(const Eight<DT>& v, int s) {
+    if constexpr (DT == ZS_BF16)
+        return u32x2{four_codes<TYPE, ANY>(v.w[0], v.w[1], s),
+                     four_codes<TYPE, ANY>(v.w[2], v.w[3], s)};
+    else
+        return u32x2{four_codes<TYPE, ANY>(v.f[0], v.f[1], v.f[2], v.f[3], s),
+                     four_codes<TYPE, ANY>(v.f[4], v.f[5], v.f[6], v.f[7], s)};
+}
+template <int DT, int TYPE, bool ANY>
+__device__ __forceinline__ uint32_t col_codes(const Eight<DT> (&v)[4], int e, int s) {
+    if constexpr (DT == ZS_BF16) {
+        const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
+        return four_codes<TYPE, ANY>(__builtin_amdgcn_perm(v[1].w[e / 2], v[0].w[e / 2], sel),
+                                     __builtin_amdgcn_perm(v[3].w[e / 2], v[2].w[e / 2], sel), s);
+    } else {
+        return four_codes<TYPE, ANY>(v[0].f[e], v[1].f[e], v[2].f[e], v[3].f[e], s);
+    }
+}
+
+template <int DT, int BR, int TYPE, bool ANY>
+__device__ __forceinline__ void put_rows(const F8Quant& q, const Part<DT>& x, const int (&s)[2][4],
+                                         int64_t row0, int64_t tc, int cg) {
+    const int64_t blocks = f8_ceil(q.cols, kT);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = row0 + 64 * h + i;
+            const u32x2 w = row_codes<DT, TYPE, ANY>(x[h][i], s[h][i]);
+            if (r >= q.rows) continue;
+            *global<g_u32x2a>(q.out.codes + r * q.out.ld + tc * kT + 8 * cg) = w;
+            if (BR == 1 && cg < 4) put_scale(q.out, r, tc, blocks, cg, s[h][i]);
+        }
+}
+template <int DT, int TYPE, bool ANY>
+__device__ __forceinline__ void stage_cols(const Part<DT>& x, const int (&s)[8], int wave, int cg,
+                                           int rq, Shared& sh) {
+    // word (column, 4 rows): the 16-byte pieces of a column's 128 are permuted by its number
+    // over 8, so that the 16 columns that a wavefront writes at once fall on other banks
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            sh.codes[(8 * cg + e) * 32 + 4 * ((4 * h + wave) ^ (cg & 7)) + rq] =
+                col_codes<DT, TYPE, ANY>(x[h], e, s[e]);
+}
+
 // One tile. BR = 1: a block for each row (column, transposed) of the tile, BR = 128: one.
+// Special blocks are rare: a wavefront without one converts by the instruction alone.
 template <int DT, int BR, class Src>
 __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int64_t tr,
                                            int64_t tc, Shared& sh) {
     const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
     const int cg = lane & 15, rq = lane >> 4;
-    const int64_t r0 = tr * kT, c = tc * kT + 8 * cg;
-    const int64_t blocks_c = f8_ceil(q.cols, kT), blocks_r = f8_ceil(q.rows, kT);
+    const int64_t r0 = tr * kT, row0 = r0 + 16 * wave + 4 * rq, c = tc * kT + 8 * cg;
     const int live = q.cols - c >= 8 ? 8 : (q.cols > c ? int(q.cols - c) : 0);
-    Eight<DT> x[2][4];
+    Part<DT> x;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + 64 * h + 16 * wave + 4 * rq + i;
+            const int64_t r = row0 + 64 * h + i;
             if (r < q.rows && live > 0) x[h][i] = src.template get<DT>(r, c, live);
             else x[h][i] = Eight<DT>{};
         }
@@ -111,97 +164,87 @@ __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int
     }
     if (q.out.codes != nullptr) {
         const int type = q.out.type;
+        int s[2][4];
+        bool special = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t r = r0 + 64 * h + 16 * wave + 4 * rq + i;
-                const int s = scale_of(BR == 128 ? whole : row_max(top_bits<DT>(x[h][i])), type);
-                u32x2 w;
-                const Eight<DT>& v = x[h][i];
-                if constexpr (DT == ZS_BF16) {
-                    if (type == ZS_E4M3)
-                        w = u32x2{four_codes<ZS_E4M3>(v.w[0], v.w[1], s),
-                                  four_codes<ZS_E4M3>(v.w[2], v.w[3], s)};
-                    else
-                        w = u32x2{four_codes<ZS_E5M2>(v.w[0], v.w[1], s),
-                                  four_codes<ZS_E5M2>(v.w[2], v.w[3], s)};
-                } else {
-                    if (type == ZS_E4M3)
-                        w = u32x2{four_codes<ZS_E4M3>(v.f[0], v.f[1], v.f[2], v.f[3], s),
-                                  four_codes<ZS_E4M3>(v.f[4], v.f[5], v.f[6], v.f[7], s)};
-                    else
-                        w = u32x2{four_codes<ZS_E5M2>(v.f[0], v.f[1], v.f[2], v.f[3], s),
-                                  four_codes<ZS_E5M2>(v.f[4], v.f[5], v.f[6], v.f[7], s)};
-                }
-                if (r < q.rows) {
-                    *global<g_u32x2a>(q.out.codes + r * q.out.ld + c) = w;
-                    if (BR == 1 && cg < 4) put_scale(q.out, r, tc, blocks_c, cg, s);
-                }
+                const uint32_t u = BR == 128 ? whole : row_max(top_bits<DT>(x[h][i]));
+                s[h][i] = scale_of(u, type);
+                special |= is_special(u, s[h][i]);
             }
+        if (__any(special)) {
+            if (type == ZS_E4M3) put_rows<DT, BR, ZS_E4M3, true>(q, x, s, row0, tc, cg);
+            else put_rows<DT, BR, ZS_E5M2, true>(q, x, s, row0, tc, cg);
+        } else {
+            if (type == ZS_E4M3) put_rows<DT, BR, ZS_E4M3, false>(q, x, s, row0, tc, cg);
+            else put_rows<DT, BR, ZS_E5M2, false>(q, x, s, row0, tc, cg);
+        }
         if (BR == 128 && threadIdx.x < 4)
-            put_scale(q.out, tr, tc, blocks_c, int(threadIdx.x), scale_of(whole, type));
+            put_scale(q.out, tr, tc, f8_ceil(q.cols, kT), int(threadIdx.x), scale_of(whole, type));
     }
     if (q.out_t.codes == nullptr) return;
     const int type = q.out_t.type;
-    int st[8];
+    const int64_t blocks_r = f8_ceil(q.rows, kT);
+    int s[8];
+    bool special = false;
     if constexpr (BR == 1) {
+        // a column's largest magnitude: of the lane's 8 rows, the wavefront's 32, all 128
+        if constexpr (DT == ZS_BF16) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t u = 0;
+            for (int k = 0; k < 4; ++k) {
+                u16x2 u = mags(x[0][0].w[k]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (DT == ZS_BF16)
-                        u = max_u(u, (x[h][i].w[e / 2] << (e & 1 ? 0 : 16)) & 0x7fff0000u);
-                    else
-                        u = max_u(u, __float_as_uint(x[h][i].f[e]) & 0x7fffffffu);
+                for (int i = 1; i < 8; ++i)
+                    u = __builtin_elementwise_max(u, mags(x[i / 4][i % 4].w[k]));
+                const uint32_t two = col_max_pair(__builtin_bit_cast(uint32_t, u));
+                if (rq == 0) {
+                    sh.top[wave][8 * cg + 2 * k] = two << 16;
+                    sh.top[wave][8 * cg + 2 * k + 1] = two & 0xffff0000u;
                 }
-            u = col_max(u);
-            if (rq == 0) sh.top[wave][8 * cg + e] = u;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                uint32_t u = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    u = max_u(u, __float_as_uint(x[i / 4][i % 4].f[e]) & 0x7fffffffu);
+                u = col_max(u);
+                if (rq == 0) sh.top[wave][8 * cg + e] = u;
+            }
         }
         __syncthreads();
+        const auto top = [&](int k) {
+            return max_u(max_u(sh.top[0][k], sh.top[1][k]), max_u(sh.top[2][k], sh.top[3][k]));
+        };
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int k = 8 * cg + e;
-            st[e] = scale_of(max_u(max_u(sh.top[0][k], sh.top[1][k]),
-                                   max_u(sh.top[2][k], sh.top[3][k])), type);
+            const uint32_t u = top(8 * cg + e);
+            s[e] = scale_of(u, type);
+            special |= is_special(u, s[e]);
         }
-        if (wave == 0 && rq == 0) {
+        const int64_t col = tc * kT + int(threadIdx.x);
+        if (threadIdx.x < kT && col < q.cols) {
+            const int mine = scale_of(top(int(threadIdx.x)), type);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (e < live) put_scale(q.out_t, c + e, tr, blocks_r, k, st[e]);
+            for (int k = 0; k < 4; ++k) put_scale(q.out_t, col, tr, blocks_r, k, mine);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) st[e] = scale_of(whole, type);
+        for (int e = 0; e < 8; ++e) s[e] = scale_of(whole, type);
+        special = is_special(whole, s[0]);
         if (threadIdx.x < 4)
             put_scale(q.out_t, tc, tr, blocks_r, int(threadIdx.x), scale_of(whole, type));
     }
-    // word (column, 4 rows): the 16-byte pieces of a column's 128 are permuted by its number
-    // over 8, so that the 16 columns that a wavefront writes at once fall on other banks
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t w;
-            if constexpr (DT == ZS_BF16) {
-                const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
-                const uint32_t ab = __builtin_amdgcn_perm(x[h][1].w[e / 2], x[h][0].w[e / 2], sel);
-                const uint32_t cd = __builtin_amdgcn_perm(x[h][3].w[e / 2], x[h][2].w[e / 2], sel);
-                w = type == ZS_E4M3 ? four_codes<ZS_E4M3>(ab, cd, st[e])
-                                    : four_codes<ZS_E5M2>(ab, cd, st[e]);
-            } else {
-                const float a = x[h][0].f[e], b = x[h][1].f[e], d = x[h][2].f[e], f = x[h][3].f[e];
-                w = type == ZS_E4M3 ? four_codes<ZS_E4M3>(a, b, d, f, st[e])
-                                    : four_codes<ZS_E5M2>(a, b, d, f, st[e]);
-            }
-            const int piece = (4 * h + wave) ^ (cg & 7);
-            sh.codes[(8 * cg + e) * 32 + 4 * piece + rq] = w;
-        }
+    if (__any(special)) {
+        if (type == ZS_E4M3) stage_cols<DT, ZS_E4M3, true>(x, s, wave, cg, rq, sh);
+        else stage_cols<DT, ZS_E5M2, true>(x, s, wave, cg, rq, sh);
+    } else {
+        if (type == ZS_E4M3) stage_cols<DT, ZS_E4M3, false>(x, s, wave, cg, rq, sh);
+        else stage_cols<DT, ZS_E5M2, false>(x, s, wave, cg, rq, sh);
+    }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -214,21 +257,23 @@ __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int
     }
 }
 
-template <int BR>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(F8Quant q) {
+// One matrix, or (tiles2 > 0) two in one launch.
+template <int DT, int BR>
+__global__ __launch_bounds__(kThreads, DT == ZS_F32 ? 3 : 4) void quantize_kernel(
+    F8Quant one, F8Quant two, uint32_t tiles1, uint32_t tiles2) {
     __shared__ Shared sh;
-    const uint32_t tiles_c = uint32_t(f8_ceil(q.cols, kT));
-    const uint32_t tiles = tiles_c * uint32_t(f8_ceil(q.rows, kT));  // checked: below 2^31
-    const Strided src{q.x, q.ldx};
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        if (q.dtype == ZS_BF16) quant_tile<ZS_BF16, BR>(q, src, t / tiles_c, t % tiles_c, sh);
-        else quant_tile<ZS_F32, BR>(q, src, t / tiles_c, t % tiles_c, sh);
+    for (uint32_t t = blockIdx.x; t < tiles1 + tiles2; t += gridDim.x) {
+        const F8Quant& q = t < tiles1 ? one : two;
+        const uint32_t in = t < tiles1 ? t : t - tiles1;
+        const uint32_t tiles_c = uint32_t(f8_ceil(q.cols, kT));
+        const Strided src{q.x, q.ldx};
+        quant_tile<DT, BR>(q, src, in / tiles_c, in % tiles_c, sh);
         __syncthreads();
     }
 }
 
 template <int DT, int BR>
-__global__ __launch_bounds__(kThreads) void gather_kernel(F8Quant q, F8Shards s) {
+__global__ __launch_bounds__(kThreads, DT == ZS_F32 ? 3 : 4) void gather_kernel(F8Quant q, F8Shards s) {
     __shared__ Shared sh;
     const uint32_t tiles_c = uint32_t(f8_ceil(q.cols, kT));
     const uint32_t tiles = tiles_c * uint32_t(f8_ceil(q.rows, kT));  // checked: below 2^31
@@ -317,11 +362,31 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(
 }  // namespace
 
 hipError_t launch_quantize_f8(const F8Quant& q, int block_rows, hipStream_t stream) {
-    const dim3 grid(unsigned(f8_tile_grid(f8_tiles(q.rows, q.cols))));
-    if (block_rows == 1)
-        hipLaunchKernelGGL((quantize_kernel<1>), grid, dim3(kThreads), 0, stream, q);
+    const uint32_t tiles = uint32_t(f8_tiles(q.rows, q.cols));  // checked: below 2^31
+    const dim3 grid(unsigned(f8_tile_grid(tiles)));
+    const auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, q, q, tiles, 0u);
+    };
+    if (q.dtype == ZS_BF16) {
+        if (block_rows == 1) go(quantize_kernel<ZS_BF16, 1>);
+        else go(quantize_kernel<ZS_BF16, 128>);
+    } else {
+        if (block_rows == 1) go(quantize_kernel<ZS_F32, 1>);
+        else go(quantize_kernel<ZS_F32, 128>);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_quantize2_f8(const F8Quant& one, const F8Quant& two, hipStream_t stream) {
+    const uint32_t a = uint32_t(f8_tiles(one.rows, one.cols)),
+                   b = uint32_t(f8_tiles(two.rows, two.cols));  // checked: each below 2^30
+    const dim3 grid(unsigned(f8_tile_grid(int64_t(a) + b)));
+    if (one.dtype == ZS_BF16)
+        hipLaunchKernelGGL((quantize_kernel<ZS_BF16, 1>), grid, dim3(kThreads), 0, stream, one, two,
+                           a, b);
     else
-        hipLaunchKernelGGL((quantize_kernel<128>), grid, dim3(kThreads), 0, stream, q);
+        hipLaunchKernelGGL((quantize_kernel<ZS_F32, 1>), grid, dim3(kThreads), 0, stream, one, two,
+                           a, b);
     return hipGetLastError();
 }
 
