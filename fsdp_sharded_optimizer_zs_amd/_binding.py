@@ -102,6 +102,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Load libzs.so (once). Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -197,18 +199,27 @@ def zs_abi_version() -> int:
 
 
 # ------------------------------------------------------------------ helpers
+_modules = {}     # torch, once it is asked for, and the element types' codes
+
+
 def _torch():
-    import torch
+    torch = _modules.get("torch")
+    if torch is None:
+        import torch
+        codes = {torch.bfloat16: ZS_BF16, torch.int16: ZS_BF16, torch.float32: ZS_F32}
+        if hasattr(torch, "uint16"):
+            codes[torch.uint16] = ZS_BF16
+        _modules["codes"] = codes
+        _modules["torch"] = torch
     return torch
 
 
 def _dtype_code_of(dtype) -> int:
-    torch = _torch()
-    if dtype in (torch.bfloat16, torch.int16) or dtype == getattr(torch, "uint16", None):
-        return ZS_BF16
-    if dtype == torch.float32:
-        return ZS_F32
-    raise TypeError(f"unsupported dtype {dtype}: use bf16 (bfloat16/int16 bits) or float32")
+    _torch()
+    code = _modules["codes"].get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: use bf16 (bfloat16/int16 bits) or float32")
+    return code
 
 
 def _dtype_code(t) -> int:
@@ -1018,8 +1029,11 @@ def zs_adamw_step_clip(p, m, v, w_out, contribs: Sequence, hp, grad_scale, repli
     torch = _torch()
     contribs = list(contribs)
     S = p.numel()
-    for name, t in (("p", p), ("m", m), ("v", v)):
-        _typed(t, name, torch.float32, S)
+    f32 = torch.float32
+    if not all([t.is_cuda and t.dtype == f32 and t.numel() == S and t.is_contiguous()
+                for t in (p, m, v)]):
+        for name, t in (("p", p), ("m", m), ("v", v)):
+            _typed(t, name, f32, S)
     _dev(w_out, "w_out")
     if _dtype_code(w_out) != ZS_BF16 or w_out.numel() != S:
         raise ValueError("w_out must be bf16 bits with S elements")

@@ -23,13 +23,14 @@ inline int64_t norm_grid(int64_t n_chunks) {
     return b < 1 ? 1 : (b < kNormGrid ? b : kNormGrid);
 }
 
-// The reduce with its result's norm: workgroups of 8 wavefronts, one wavefront per group of
-// `tiles` 512-element tiles (not aligned: one lane per element), at most one workgroup for
-// each partial sum of the workspace.
-inline int64_t reduce_norm_grid(int64_t S, int tiles, bool aligned) {
-    const int64_t per = aligned ? int64_t(8) * tiles * 512 : 512;
-    const int64_t b = S / per + (S % per != 0);
-    return b < 1 ? 1 : (b < kNormGrid ? b : kNormGrid);
+// The reduce with its result's norm: workgroups of 4 wavefronts, one wavefront per group of
+// `tiles` 512-element tiles, at most one workgroup on each of 256 CUs; not aligned (tiles = 0),
+// where accesses are narrow and more of them have to be under way, one lane per element and
+// at most two.
+inline int64_t reduce_norm_grid(int64_t S, int tiles) {
+    const int64_t per = tiles > 0 ? int64_t(4) * tiles * 512 : kBlockThreads;
+    const int64_t b = S / per + (S % per != 0), most = tiles > 0 ? kNormGrid / 2 : kNormGrid;
+    return b < 1 ? 1 : (b < most ? b : most);
 }
 
 // 4-bit quantisation of values of es bytes: one workgroup per tile of kMx4Groups 16-byte

@@ -536,29 +536,30 @@ __global__ __launch_bounds__(kThreads) void reduce_scalar_kernel(float* __restri
 
 // The reduce with the sum of the squares of what it writes, in fp64 (exact products): the
 // square costs no read of its own, where a norm over the written gradient would read it
-// again (4 bytes an element beside D * 2 + 4). Workgroups of 8 wavefronts, at most one
-// for each partial sum of the workspace, which is also what fills the chip at 2 wavefronts
-// a SIMD; their sums are joined as the norm over many tensors joins its own. Elements past
-// the last whole tile group go to the last workgroup; with buffers that are not 16-byte
-// aligned (TP = 0) every workgroup takes elements, one a lane.
-constexpr int kJoinThreads = 512;
+// again (4 bytes an element beside D * 2 + 4). One workgroup a CU, whose sums are joined as
+// the norm over many tensors joins its own, in the one launch. Loops over a shard cost the
+// memory more than the arithmetic does: 25.3M elements of 8 bf16 contributions take 85 us,
+// by 512 workgroups 87, by as many as there are tiles with a launch that joins them 88, by
+// workgroups of 8 wavefronts 92, in each case as long without the squares; the reduce
+// alone, which does not loop, 80. Elements past the last whole tile group go to the last
+// workgroup; with buffers that are not 16-byte aligned (TP = 0) every workgroup takes
+// elements, one a lane.
 template <int DT, class Sum, int TP>
-__global__ __launch_bounds__(kJoinThreads) ZS_WAVES void reduce_norm_kernel(
-    float* __restrict__ out, int64_t S, PtrPack c, Sum sum, double max_norm, int accumulate,
-    NormWorkspace* ws, double* sumsq, float* norm_coef) {
-    constexpr int W = kJoinThreads / kWave, kTP = TP > 0 ? TP : 1;
-    __shared__ f32x4 xpose[W][kTile / 4];
-    __shared__ double slot[W];
+__global__ __launch_bounds__(kThreads) ZS_WAVES void reduce_norm_kernel(
+    float* __restrict__ out, int64_t S, PtrPack c, Sum sum, NormJob job) {
+    constexpr int kTP = TP > 0 ? TP : 1;
+    __shared__ f32x4 xpose[kWaves][kTile / 4];
+    __shared__ double slot[kWaves];
     __shared__ bool last;
     const int lane = int(threadIdx.x) % kWave;
     const int wave = int(threadIdx.x) / kWave;
     double s[2] = {0.0, 0.0};
-    int64_t first = int64_t(blockIdx.x) * kJoinThreads;
-    int64_t step = int64_t(gridDim.x) * kJoinThreads;
+    int64_t first = int64_t(blockIdx.x) * kThreads;
+    int64_t step = int64_t(gridDim.x) * kThreads;
     if constexpr (TP > 0) {
         f32x4* o4 = reinterpret_cast<f32x4*>(out);
-        const int64_t ngroups = S / (TP * kTile);
-        for (int64_t q = int64_t(blockIdx.x) * W + wave; q < ngroups; q += int64_t(gridDim.x) * W) {
+        const int64_t ngroups = S / (TP * kTile), stride = int64_t(gridDim.x) * kWaves;
+        for (int64_t q = int64_t(blockIdx.x) * kWaves + wave; q < ngroups; q += stride) {
             float g[kTP][kVec];
             reduce_tiles<DT, kTP>(o4, c, sum, q * TP, lane, xpose[wave], g);
 #pragma unroll
@@ -568,14 +569,15 @@ __global__ __launch_bounds__(kJoinThreads) ZS_WAVES void reduce_norm_kernel(
                     s[e & 1] = __builtin_fma(double(g[u][e]), double(g[u][e]), s[e & 1]);
         }
         first = blockIdx.x == gridDim.x - 1 ? ngroups * TP * kTile : S;
-        step = kJoinThreads;
+        step = kThreads;
     }
     for (int64_t t = first + threadIdx.x; t < S; t += step) {
         const float g = sum.one(c, t);
         out[t] = g;
         s[0] = __builtin_fma(double(g), double(g), s[0]);
     }
-    const double mine = block_sum<W>(s[0] + s[1], slot);
+    NormWorkspace* const ws = job.ws;
+    const double mine = block_sum<kWaves>(s[0] + s[1], slot);
     if (threadIdx.x == 0) {
         __hip_atomic_store(&ws->partial[blockIdx.x], mine, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
@@ -585,13 +587,13 @@ __global__ __launch_bounds__(kJoinThreads) ZS_WAVES void reduce_norm_kernel(
     __syncthreads();
     if (!last) return;
     double total = 0.0;
-    for (unsigned k = threadIdx.x; k < gridDim.x; k += kJoinThreads)
+    for (unsigned k = threadIdx.x; k < gridDim.x; k += kThreads)
         total += __hip_atomic_load(&ws->partial[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    total = block_sum<W>(total, slot);
+    total = block_sum<kWaves>(total, slot);
     if (threadIdx.x == 0) {
-        if (accumulate) total = *sumsq + total;
-        *sumsq = total;
-        if (norm_coef != nullptr) write_clip(total, max_norm, norm_coef);
+        if (job.accumulate) total = *job.sumsq + total;
+        *job.sumsq = total;
+        if (job.norm_coef != nullptr) write_clip(total, job.max_norm, job.norm_coef);
     }
 }
 
@@ -620,16 +622,14 @@ hipError_t launch_job(const Job& j, const PtrPack& c, const Sum& sum, hipStream_
     const unsigned tiled = unsigned(step_tiled_grid(j.S, TP));
     const unsigned scalar = unsigned(step_scalar_grid(j.S));
     if (j.norm != nullptr) {
-        const NormJob& n = *j.norm;
-        const unsigned grid = unsigned(reduce_norm_grid(j.S, TP, j.aligned));
         if (j.aligned)
-            hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, TP>), dim3(grid), dim3(kJoinThreads),
-                               0, stream, j.out, j.S, c, sum, n.max_norm, n.accumulate, n.ws,
-                               n.sumsq, n.norm_coef);
+            hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, TP>),
+                               dim3(unsigned(reduce_norm_grid(j.S, TP))), dim3(kThreads), 0, stream,
+                               j.out, j.S, c, sum, *j.norm);
         else
-            hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, 0>), dim3(grid), dim3(kJoinThreads),
-                               0, stream, j.out, j.S, c, sum, n.max_norm, n.accumulate, n.ws,
-                               n.sumsq, n.norm_coef);
+            hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, 0>),
+                               dim3(unsigned(reduce_norm_grid(j.S, 0))), dim3(kThreads), 0, stream,
+                               j.out, j.S, c, sum, *j.norm);
     } else if (j.out == nullptr && j.ev_start != nullptr) {
         // timed: the runtime ties the two events to this dispatch's start and
         // end timestamps, with no marker packets around it

@@ -296,8 +296,8 @@ int main() {
         std::printf("%d %d %d %lld %lld %lld ", p.tm, p.tn, p.splits, (long long)p.tiles_m,
                     (long long)p.tiles_n, (long long)f8_partial_bytes(p));
         std::printf("%lld %lld %lld %lld %lld\n", (long long)f8_matmul_workspace(M, N, K), (long long)kF8Counts,
-                    (long long)kF8CountBytes, (long long)reduce_norm_grid(M * K, 2, true),
-                    (long long)reduce_norm_grid(M * K, 2, false));
+                    (long long)kF8CountBytes, (long long)reduce_norm_grid(M * K, 2),
+                    (long long)reduce_norm_grid(M * K, 0));
     }
     return 0;
 }
@@ -327,4 +327,5 @@ def test_plans_cover_the_work_and_fit_the_workspace(tmp_path):
             assert tiles_m * tiles_n <= counts
             assert partial == tiles_m * tiles_n * splits * tm * tn * 4 and need >= count_bytes + partial
         assert count_bytes >= 2 * counts * 4 and need < 2**31
-        assert 1 <= aligned <= 512 and 1 <= scalar <= 512
+        for grid in (aligned, scalar):
+            assert 1 <= grid <= 512
