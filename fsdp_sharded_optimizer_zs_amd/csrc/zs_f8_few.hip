@@ -10,8 +10,11 @@
 // puts all of a into LDS as codes, while the first codes of b are under way: it copies them,
 // or quantises a's values (8 elements a lane, a block in the 16 lanes of a DPP row), which
 // spares a launch. a is the second operand, its rows past M zeros. The sums of a group's
-// wavefronts are added through LDS in their order. C in bf16 and fp32 (EXACT) as in the
-// large products.
+// wavefronts are added through LDS in their order. C in bf16 and fp32 as in the large products.
+//
+// Measured from memory, us (TB/s of codes): 1 x 4096 x 4096 7.4 (2.3), 1 x 4096 x 11008 11.2
+// (4.0), 16 x 11008 x 4096 17.4 (2.6), 1 x 32000 x 8192 50 (5.2); a plain read of 45 MB takes
+// 8.3. What is left is the start: the launch and the first loads' way, some 4 us.
 
 #include "zs_f8_dev.h"
 

@@ -1,20 +1,36 @@
 // Products of block-scaled 8-bit matrices, C[m, n] = sum_k a[m, k] b[n, k], for gfx950.
 //
-// A workgroup sums a TM x TN tile of C over its part of K in steps of 128, one block of
-// both operands: their codes go from memory straight to LDS (16 bytes a lane, two buffers,
-// the next step's under way while this one is multiplied), and every wavefront multiplies
-// its PM x PN part from there. Both operands lie along K, so that all accesses are 16-byte
-// pieces of 128-byte rows; piece j of row r stands at j ^ (r mod 8) of its row in LDS, so
-// that the 16 rows that a wavefront reads at once fall on all banks.
+// What bounds it: the matrix cores. One product of two codes costs them half of what one in
+// bf16 does, and 256 x 256 of C take 64 KiB of codes a step of 128 along K from L2 for
+// 8.4 million products, so that memory stays behind.
 //
-// C in bf16: v_mfma_scale_f32_16x16x128_f8f6f4 multiplies a whole block with both scale
-// bytes. Of 8 neighbouring products it drops what is below 2^-13 of the largest one's power
-// of two (measured; the sums of the eights are added in fp32): on normal data 2^-16 of the
-// result, 2^7 below the rounding to bf16. C in fp32 (EXACT): the codes, times their scales, become bf16
-// exactly and v_mfma_f32_16x16x32_bf16 sums them in fp32, at a quarter of the rate.
+// A workgroup sums a TM x TN tile of C (256, 128 or 64 squared, by 8 or 4 wavefronts) over its
+// part of K. Codes go from memory straight to LDS, 16 bytes a lane, into a ring of 4 half steps
+// of 64 along K: a half step multiplies what the one before read into registers, reads its
+// successor's codes and sends for those of the fourth half step on, so that a load has three to
+// arrive and the wait for it leaves the younger ones under way (whole steps in two buffers
+// reached 2,472 TFLOP/s where this reaches 2,530; registers and LDS hold no more). The
+// accumulators take 256 x 256 / 512 = 128 registers of each lane. Rows lie in LDS in pieces of
+// 16 bytes, piece j of row r at j ^ (r / 4 mod 4), so that the reads of 32 rows spread over the
+// banks (conflicts take 0.6 % of the CUs' cycles at 8192 x 8192 x 8192).
+//
+// C in bf16: v_mfma_scale_f32_32x32x64_f8f6f4 multiplies with both scale bytes. Of 8
+// neighbouring products it drops what is below 2^-13 of the largest one's power of two
+// (measured; the sums of the eights are added in fp32): on normal data 2^-16 of the result, 2^7
+// below the rounding to bf16. C in fp32 (EXACT): the codes, times their scales, become bf16
+// exactly and v_mfma_f32_32x32x16_bf16 sums them in fp32, at half of the rate.
+//
+// Measured on normal data (C in bf16 / fp32): 8192 x 8192 x 8192 434 us, 2,530 TFLOP/s / 785 us,
+// 1,400; 11008 x 4096 x 4096 169 us, 2,190 / 287 us, 1,290; 512 x 11008 x 4096 36 us; the same
+// card's library in bf16 takes 664 and 393 us for the first two. On zeros the first takes 340 us
+// (3,230 TFLOP/s; 621 us in fp32): what bounds the rest is the power that the matrix cores draw,
+// the clock falls to about 1.75 GHz. Wavefronts of 128 x 128 (4 a workgroup) had the same rate
+// and a longer epilogue.
 //
 // The matrix instruction's first operand is b and its second a: a lane then holds 4
-// neighbouring columns n of C.
+// neighbouring columns n of C, which reach memory through LDS in whole lines. Tiles that leave
+// CUs idle split K: each workgroup writes its partial sum, and the one that counts in last adds
+// all of them in their order, so that results do not depend on who that is.
 
 #include "zs_f8_dev.h"
 
@@ -39,6 +55,7 @@ struct Shape {
     // loads of a half step, a wavefront: of a, of b; and all wavefronts' loads of scales
     static constexpr int kLoadsA = TM / 16 / W, kLoadsB = TN / 16 / W, kLoads = kLoadsA + kLoadsB;
     static constexpr int kScaleLoads = (TM + TN) / 64;
+    static constexpr bool kSplits = TM == 64;  // only these split K
     static_assert(TM % (16 * W) == 0 && TN % (16 * W) == 0 && TM % 64 == 0 && TN % 64 == 0 &&
                       PM % 32 == 0 && PN % 32 == 0,
                   "whole loads and parts");
@@ -211,7 +228,7 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
     arrived();
     __builtin_amdgcn_s_barrier();
 
-    if (p.splits > 1) {
+    if (S::kSplits && p.splits > 1) {
         // partial sums as the lanes hold them, written through to memory that all XCDs share;
         // the workgroup that counts in last adds them in their order
         typedef uint64_t u64x8 __attribute__((ext_vector_type(8)));
@@ -232,7 +249,7 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         // LDS is free here: the loads of codes are over and read
-        volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(big);
+        const auto flag = (ZS_LDS volatile uint32_t*)(big);
         if (threadIdx.x == 0) {
             uint32_t* const n = p.counts + t;
             const bool last_one = __hip_atomic_fetch_add(n, 1u, __ATOMIC_RELAXED,

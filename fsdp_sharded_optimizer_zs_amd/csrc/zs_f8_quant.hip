@@ -8,6 +8,15 @@
 // 256 bytes of a bf16 row, a row's block of 128 is the 16 lanes of a DPP row, and the 4
 // rows i of a column are one word of transposed codes. Those words are exchanged through
 // LDS (16 KiB) so that the transpose leaves in 16-byte pieces of whole 128-byte runs too.
+//
+// Memory bounds them: 2 or 4 bytes read and 1 written for each element and form. Blocks of one
+// row cost a maximum, a scale and its checks for each of 128 rows and columns of a tile on top,
+// which shows. Measured from memory, 4096 x 11008 in us (TB/s), as it is / transposed / both:
+//   bf16, blocks of 1 x 128      28.9 (4.7) / 30.0 (4.5) / 41.4 (4.4)
+//   bf16, 128 x 128              25.7 (5.3) / 26.7 (5.1) / 34.2 (5.3)
+//   fp32, 1 x 128                53.8 (4.2) / 55.2 (4.1) / 67.2 (4.0)
+//   fp32, 128 x 128              46.7 (4.8) / 53.1 (4.2) / 57.7 (4.7)
+// and both forms from shards in bf16 39.5 (4.6) in blocks of 128 x 128; back to bf16 22.9 (5.9).
 
 #include "zs_f8_dev.h"
 
@@ -257,9 +266,14 @@ __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int
     }
 }
 
+// Wavefronts to a SIMD: what the registers of a tile's elements allow without spilling (fp32 in
+// blocks of one row, 3 wavefronts and 22 registers spilled: 59.6 / 75.8 / 86.8 us above).
+template <int DT, int BR>
+constexpr int kDepth = DT == ZS_BF16 || BR == 128 ? 4 : 2;
+
 // One matrix, or (tiles2 > 0) two in one launch.
 template <int DT, int BR>
-__global__ __launch_bounds__(kThreads, DT == ZS_F32 ? 3 : 4) void quantize_kernel(
+__global__ __launch_bounds__(kThreads, (kDepth<DT, BR>)) void quantize_kernel(
     F8Quant one, F8Quant two, uint32_t tiles1, uint32_t tiles2) {
     __shared__ Shared sh;
     for (uint32_t t = blockIdx.x; t < tiles1 + tiles2; t += gridDim.x) {
@@ -273,7 +287,7 @@ __global__ __launch_bounds__(kThreads, DT == ZS_F32 ? 3 : 4) void quantize_kerne
 }
 
 template <int DT, int BR>
-__global__ __launch_bounds__(kThreads, DT == ZS_F32 ? 3 : 4) void gather_kernel(F8Quant q, F8Shards s) {
+__global__ __launch_bounds__(kThreads, (kDepth<DT, BR>)) void gather_kernel(F8Quant q, F8Shards s) {
     __shared__ Shared sh;
     const uint32_t tiles_c = uint32_t(f8_ceil(q.cols, kT));
     const uint32_t tiles = tiles_c * uint32_t(f8_ceil(q.rows, kT));  // checked: below 2^31

@@ -312,6 +312,41 @@ def test_scales_at_the_ends(dtype):
         assert np.array_equal(c.float().cpu().numpy(), want), e
 
 
+@pytest.mark.parametrize("M,N", [(4, 20), (40, 50)])
+def test_subnormal_values_and_codes(M, N):
+    """Values down to 2^-135 under products in the middle: the 8-bit instructions take every
+    code and scale byte; for C in fp32 operands pass through bf16, exact down to 2^-133."""
+    x, y = whole(M, 256, 1).astype(np.float64), whole(N, 256, 2).astype(np.float64)
+    for ex, ey in ((-124, 120), (-128, 120), (-131, 120), (-135, 124), (125, -125)):
+        for kind in KINDS:
+            a, va = f8((x * 2.0**ex).astype(np.float32), kind)
+            b, vb = f8((y * 2.0**ey).astype(np.float32), F.E4M3, 128)
+            for dtype in DTYPES:
+                if dtype == "f32" and ex == -135:
+                    continue
+                _, _, c = out_matrix(M, N, dtype)
+                zs.zs_matmul_f8(a, b, c, workspace=workspace(M, N, 256))
+                assert np.array_equal(c.float().cpu().numpy(), rounded(va @ vb.T, dtype)), (ex, kind, dtype)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("M,N", [(4, 20), (40, 50)])
+def test_codes_that_are_not_finite(M, N, dtype):
+    """Codes of infinity and NaN that a caller wrote go through products as such."""
+    a, b = zs.F8Matrix.empty(M, 128, zs.ZS_E5M2), zs.F8Matrix.empty(N, 128)
+    a.codes.zero_()
+    b.codes.fill_(0x38)                               # 1
+    for m in (a, b):
+        m.scales.fill_(127)
+    for r, code in enumerate((0x3C, 0x7C, 0xFC, 0x7F)):
+        a.codes.view(M, 128)[r, 5 + r] = code
+    _, _, c = out_matrix(M, N, dtype)
+    zs.zs_matmul_f8(a, b, c, workspace=workspace(M, N, 128))
+    want = np.zeros((M, N), np.float32)
+    want[:4] = np.array([1, np.inf, -np.inf, np.nan])[:, None]
+    assert np.array_equal(c.float().cpu().numpy(), want, equal_nan=True)
+
+
 def test_empty_products():
     ws = workspace(64, 64, 0)
     for M, N, K in ((0, 8, 256), (8, 0, 256), (70, 80, 0), (1, 5, 0)):
@@ -413,6 +448,32 @@ def test_backward(M, N, K, kind):
         assert torch.equal(dx2, dx.contiguous()) and torch.equal(dw2, dw)
         zs.zs_linear_f8_backward(dy, x, None, None, dw2, ws, grad_type=kind, accumulate=True)
         assert (np.abs(dw2.double().cpu().numpy() - 2 * e) <= 2 * t + 2.0**-7 * np.abs(e)).all()
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("M,N,K", [(3900, 4000, 3850), (2000, 1900, 2000), (4200, 300, 300), (700, 5000, 40)])
+def test_exact_large_backward(M, N, K, dtype):
+    """Both products in one launch by every tile, and by other tiles and types in two: whole
+    numbers under small powers of two, which 8 bits and every order of the sum hold exactly
+    (below 2^24 of their steps)."""
+    dev = device()
+    dy, x, w = (torch.from_numpy(whole(a, b, i)).to(dev) for i, (a, b) in enumerate(((M, N), (M, K), (N, K))))
+    want = [torch.mm(dy, w), torch.mm(dy.t().contiguous(), x)]
+    ws = workspace(M, N, K, zs.zs_linear_f8_backward_workspace)
+    for kind_w, kind, other, pad in ((F.E4M3, F.E4M3, False, 0), (F.E4M3, F.E5M2, False, 3), (F.E5M2, F.E4M3, False, 0),
+                                     (F.E4M3, F.E4M3, True, 1)):
+        w_t = zs.F8Matrix.empty(K, N, kind_w)
+        zs.zs_quantize_f8(w, None, w_t)
+        dw_dtype = {"bf16": "f32", "f32": "bf16"}[dtype] if other else dtype
+        s1, f1, dx = out_matrix(M, K, dtype, pad, pad)
+        s2, f2, dw = out_matrix(N, K, dw_dtype, pad, pad)
+        zs.zs_linear_f8_backward(dy, x, w_t, dx, dw, ws, grad_type=kind)
+        assert torch.equal(dx, want[0].to(DTYPES[dtype])) and torch.equal(dw, want[1].to(DTYPES[dw_dtype]))
+        check_beside(s1, f1, K, pad, "dx")
+        check_beside(s2, f2, K, pad, "dw")
+        old = dw.to(torch.float32, copy=True)     # dw itself is added to
+        zs.zs_linear_f8_backward(dy, x, w_t, dx, dw, ws, grad_type=kind, accumulate=True)
+        assert torch.equal(dx, want[0].to(DTYPES[dtype])) and torch.equal(dw, (old + want[1]).to(DTYPES[dw_dtype]))
 
 
 def test_gradients_against_differences():
