@@ -55,7 +55,7 @@ struct Shape {
     // loads of a half step, a wavefront: of a, of b; and all wavefronts' loads of scales
     static constexpr int kLoadsA = TM / 16 / W, kLoadsB = TN / 16 / W, kLoads = kLoadsA + kLoadsB;
     static constexpr int kScaleLoads = (TM + TN) / 64;
-    static constexpr bool kSplits = TM == 64;  // only these split K
+    static constexpr bool kSplits = TM < 256;  // these may split K
     static_assert(TM % (16 * W) == 0 && TN % (16 * W) == 0 && TM % 64 == 0 && TN % 64 == 0 &&
                       PM % 32 == 0 && PN % 32 == 0,
                   "whole loads and parts");

@@ -50,13 +50,15 @@ constexpr int64_t f8_few_lds(int depth, int64_t M, int64_t blocks) {
 // the smaller ones fill 256 CUs with less. The costs of a step of 128 along K for each tile
 // that a CU takes are measured, in hundredths of a microsecond (C in fp32: 290, 93 and 33, in
 // much the same ratios). With them, in us, M x N x K and C in bf16: 3000 x 3000 x 3000
-// 256: 39, 128: 46, 64: 58; 2048 x 4096 x 4096 47, 42, 66; 512 x 4096 x 4096 46, 19, 17.
-// What is left idle by tiles of 64 is filled by splitting K, into parts of 16 steps at
-// least, below which joining them costs more than it gains (128 x 4096 x 4096 in 1, 2, 4 parts
-// 11.0, 10.0, 10.8; 1024 x 256 x 2048 8.1, 8.4, 8.5; 256 x 256 x 8192 19.0, 13.5, 10.6).
+// 256: 39, 128: 46, 64: 58; 2048 x 4096 x 4096 47, 43, 67; 512 x 4096 x 4096 46, 19, 17.
+// CUs that tiles of 128 or 64 leave idle take parts of K, of 16 steps at least, if joining them
+// (writing the partial sums, and one workgroup a tile reading its own again) costs less than
+// the steps it saves: 512 x 4096 x 11008 64: 47, 128: 51, 128 in 2 parts: 37; 256 x 256 x 8192
+// 64 in 1, 2, 4 parts 19, 13, 10; 1024 x 1024 x 4096 64 in 1 and 2 parts 11, 13. (256 in 2 parts
+// would gain where K is past 10,000 alone, 2048 x 4096 x 11008 99 for 114, and take 64 MiB.)
 inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
     constexpr int kCus = 256;
-    const int side[3] = {256, 128, 64}, cost[3] = {150, 55, 22};
+    const int side[3] = {256, 128, 64}, cost[3] = {150, 58, 25};
     F8Plan best{};
     int64_t least = -1;
     const int64_t blocks = f8_ceil(K, kF8Block);
@@ -67,16 +69,19 @@ inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
         return F8Plan{kF8Few, int(rows < 4 ? 4 : rows), s, 1, f8_ceil(N, rows < 4 ? 4 : rows)};
     }
     for (int i = 0; i < 3; ++i) {
-        const F8Plan p{side[i], side[i], 1, f8_ceil(M, side[i]), f8_ceil(N, side[i])};
-        const int64_t c = f8_ceil(p.tiles_m * p.tiles_n, kCus) * cost[i];
+        F8Plan p{side[i], side[i], 1, f8_ceil(M, side[i]), f8_ceil(N, side[i])};
+        const int64_t tiles = p.tiles_m * p.tiles_n;
+        int64_t c = f8_ceil(tiles, kCus) * cost[i] * (blocks > 0 ? blocks : 1);
+        int64_t s = tiles > 0 ? kCus / tiles : 0;
+        s = s < blocks / 16 ? s : blocks / 16;
+        s = s < 32 ? s : 32;
+        if (i > 0 && s > 1) {
+            // 2 us, 0.35 us a MB of all partial sums and 10 us a MB of one tile's
+            const int64_t kb = s * side[i] * side[i] * 4 / 1000;
+            const int64_t joined = cost[i] * f8_ceil(blocks, s) + 200 + tiles * kb * 35 / 1000 + kb;
+            if (joined < c) c = joined, p.splits = int(s);
+        }
         if (least < 0 || c < least) best = p, least = c;
-    }
-    const int64_t tiles = best.tiles_m * best.tiles_n;
-    if (best.tm == 64 && tiles > 0) {
-        int64_t s = kCus / tiles;
-        const int64_t parts = blocks / 16;
-        s = s < parts ? s : parts;
-        best.splits = int(s < 1 ? 1 : (s < 32 ? s : 32));
     }
     return best;
 }

@@ -242,7 +242,7 @@ def test_exact_products(M, N, K, dtype):
 
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
 @pytest.mark.parametrize("M,N,K", [(3333, 4200, 300), (3841, 3585, 1), (4096, 4096, 128), (5000, 2561, 1700),
-                                   (2600, 5003, 640), (1000, 13_000, 257)])
+                                   (2600, 5003, 640), (1000, 13_000, 257), (500, 4001, 11_000)])
 def test_exact_large_products(M, N, K, dtype):
     """Sizes that fill the chip with the largest tiles; the sum by torch in fp32, which holds
     these whole numbers exactly."""
@@ -451,7 +451,7 @@ def test_backward(M, N, K, kind):
 
 
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
-@pytest.mark.parametrize("M,N,K", [(3900, 4000, 3850), (2000, 1900, 2000), (4200, 300, 300), (700, 5000, 40)])
+@pytest.mark.parametrize("M,N,K", [(3900, 4000, 3850), (2000, 1900, 2000), (4200, 300, 300), (700, 5000, 40), (11_000, 4000, 512)])
 def test_exact_large_backward(M, N, K, dtype):
     """Both products in one launch by every tile, and by other tiles and types in two: whole
     numbers under small powers of two, which 8 bits and every order of the sum hold exactly
