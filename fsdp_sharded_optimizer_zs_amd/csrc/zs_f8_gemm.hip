@@ -12,7 +12,7 @@
 // reached 2,472 TFLOP/s where this reaches 2,530; registers and LDS hold no more). The
 // accumulators take 256 x 256 / 512 = 128 registers of each lane. Rows lie in LDS in pieces of
 // 16 bytes, piece j of row r at j ^ (r / 4 mod 4), so that the reads of 32 rows spread over the
-// banks (conflicts take 0.6 % of the CUs' cycles at 8192 x 8192 x 8192).
+// banks (conflicts take 0.5 % of the CUs' cycles at 8192 x 8192 x 8192).
 //
 // C in bf16: v_mfma_scale_f32_32x32x64_f8f6f4 multiplies with both scale bytes. Of 8
 // neighbouring products it drops what is below 2^-13 of the largest one's power of two
