@@ -1102,11 +1102,14 @@ class F8Matrix:
         _typed(codes, "codes", uint8, n_codes)
         _typed(scales, "scales", uint8, n_scales)
         _same_device((codes, scales), "F8Matrix")
-        self.codes, self.scales = codes, scales
-        self.rows, self.cols, self.type, self.block_rows = int(rows), int(cols), int(type), int(block_rows)
-        self.device = codes.device
-        self._c = ctypes.byref(zs_f8_matrix(codes.data_ptr(), scales.data_ptr(), self.rows, self.cols,
-                                            self.type, self.block_rows))
+        rows, cols, type, block_rows = int(rows), int(cols), int(type), int(block_rows)
+        self.__dict__.update(
+            codes=codes, scales=scales, rows=rows, cols=cols, type=type, block_rows=block_rows,
+            device=codes.device,
+            _c=ctypes.byref(zs_f8_matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, type, block_rows)))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"F8Matrix.{name} is fixed when the matrix is made")
 
     def get_device(self) -> int:
         return self.codes.get_device()
@@ -1179,7 +1182,7 @@ def zs_dequantize_f8(x: F8Matrix, out, stream=None) -> None:
     _enqueue(load().zs_dequantize_f8, out, stream, x._c, code, out.data_ptr(), ld)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _f8_workspace(name: str, M: int, N: int, K: int) -> int:
     n = ctypes.c_int64()
     _check(getattr(load(), name)(M, N, K, ctypes.byref(n)))
@@ -1265,6 +1268,8 @@ def zs_linear_f8_backward(dy, x, w_t: F8Matrix, dx, dw, workspace, grad_type: in
         args["dx"] = (dx_code, dx.data_ptr(), ld)
         used += [dx, w_t]
     if dw is not None:
+        if x is None:
+            raise ValueError("dw needs x")
         dw_code, ld = _matrix(dw, "dw", N, K)
         x_code, ldx = _matrix(x, "x", M, K)
         if x_code != code:

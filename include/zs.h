@@ -988,8 +988,9 @@ zs_status zs_dequantize_f8(const zs_f8_matrix* x, int32_t dtype, void* out, int6
  *              that is 0), zeroed by the caller before its first use; each call leaves it
  *              ready for the next one, of any size it is large enough for. Calls that may
  *              run at the same time (other streams, graphs) need one each
- * With K = 0 the sum is 0. Errors: ZS_EINVAL, ZS_EALIAS (C or the workspace overlap an
- * operand or each other), ZS_EUNSUPPORTED.
+ * With K = 0 the sum is 0. Errors: ZS_EINVAL (also when C has more than (2^32 - 1) / 256
+ * tiles of 64 x 64), ZS_EALIAS (C or the workspace overlap an operand or each other),
+ * ZS_EUNSUPPORTED.
  */
 zs_status zs_matmul_f8(const zs_f8_matrix* a, const zs_f8_matrix* b, int32_t dtype, void* c,
                        int64_t ldc, int32_t accumulate, void* workspace, hipStream_t stream);

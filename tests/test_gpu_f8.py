@@ -637,6 +637,73 @@ def test_two_streams_at_once():
         assert all(torch.equal(s, t) for s, t in zip(L.state(), alone.state()))
 
 
+class Products:
+    """Calls that split K, take few rows and make their codes on the way, on one workspace."""
+    SIZES = [(70, 100, 4200), (3, 300, 1000), (1, 40, 20_000), (500, 700, 9000), (16, 260, 512)]
+
+    def __init__(self, seed=1):
+        dev = device()
+        gen = torch.Generator(device=dev).manual_seed(seed)
+        rand = lambda *n: torch.randn(*n, generator=gen, device=dev)
+        self.x, self.w, self.y, self.c = [], [], [], []
+        for M, N, K in self.SIZES:
+            self.x.append(rand(M, K))
+            self.w.append(zs.F8Matrix.empty(N, K, block_rows=128))
+            zs.zs_quantize_f8(rand(N, K), self.w[-1])
+            self.y.append(torch.zeros(M, N, dtype=torch.bfloat16, device=dev))
+            self.c.append(torch.zeros(M, N, device=dev))
+        need = max(f(*n) for n in self.SIZES for f in (zs.zs_matmul_f8_workspace, zs.zs_linear_f8_workspace))
+        assert need > zs.zs_linear_f8_workspace(70, 100, 4200) > 70 * 4200
+        self.ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+        self.a = [zs.F8Matrix.empty(M, K, zs.ZS_E5M2) for M, _, K in self.SIZES]
+
+    def run(self):
+        for x, w, y, c, a in zip(self.x, self.w, self.y, self.c, self.a):
+            zs.zs_linear_f8(x, w, y, self.ws)
+            zs.zs_quantize_f8(x, a)
+            zs.zs_matmul_f8(a, w, c, accumulate=True, workspace=self.ws)
+
+    def same(self, other):
+        return all(torch.equal(a, b) for a, b in zip(self.y + self.c, other.y + other.c))
+
+
+def test_products_from_a_graph():
+    run, eager = Products(), Products()
+    Products(2).run()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        run.run()
+    torch.cuda.synchronize()
+    for rep in range(4):
+        for r in (run, eager):
+            for x in r.x:
+                x.mul_(-1.5)
+        graph.replay()
+        eager.run()
+        torch.cuda.synchronize()
+        assert run.same(eager), rep
+
+
+def test_products_on_two_streams():
+    """At the same time, each with a workspace of its own, behind work of the stream."""
+    one, two, alone = Products(), Products(), Products()
+    for _ in range(3):
+        alone.run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for r, s in zip((one, two), streams):
+            with torch.cuda.stream(s):
+                r.run()
+    torch.cuda.synchronize()
+    assert one.same(alone) and two.same(alone)
+    zs.zs_linear_f8(one.x[0], one.w[0], one.y[0], one.ws, stream=streams[0])
+    streams[0].synchronize()
+    assert one.same(alone)
+
+
 def test_refusals_on_the_device():
     dev = device()
     x = torch.zeros(64, 256, device=dev)
@@ -657,6 +724,16 @@ def test_refusals_on_the_device():
         with pytest.raises((ValueError, TypeError)):
             call()
             print("call", i, "was not refused")
+    ws = workspace(64, 64, 256, zs.zs_linear_f8_backward_workspace)
+    dy, dw = torch.zeros(64, 64, device=dev), torch.zeros(64, 256, device=dev)
+    for call in (lambda: zs.zs_linear_f8_backward(dy, None, None, None, dw, ws),
+                 lambda: zs.zs_linear_f8_backward(dy, x, None, x.clone(), dw, ws),
+                 lambda: zs.zs_linear_f8_backward(dy, x.bfloat16(), None, None, dw, ws)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    for name, value in (("codes", out_t.codes), ("scales", out_t.scales), ("rows", 3), ("type", zs.ZS_E5M2)):
+        with pytest.raises(AttributeError):
+            setattr(out, name, value)
     for call in (lambda: zs.zs_quantize_f8(x, zs.F8Matrix(out.codes, out.scales, 64, 256, 9)),
                  lambda: zs.zs_gather_matrix_f8([x.view(-1)], 1, out)):
         with pytest.raises(zs.ZsError):
