@@ -721,11 +721,14 @@ def _same_device(ts: Sequence, what: str):
             raise ValueError(f"{what}: every tensor must be on one device")
 
 
-def _typed(t, what: str, dtype, numel=None):
-    if (t.is_cuda and t.dtype == dtype and t.is_contiguous()
-            and (numel is None or t.numel() == numel)):
+def _typed(t, what: str, dtype, numel=None, dev=None):
+    """Checks a contiguous device tensor, on device dev (an index) if that is given."""
+    if ((t.is_cuda if dev is None else t.get_device() == dev) and t.dtype is dtype
+            and t.is_contiguous() and (numel is None or t.numel() == numel)):
         return
     _dev(t, what)
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{what}: every tensor must be on one device")
     size = "" if numel is None else f" with {numel} elements"
     raise ValueError(f"{what} must be {str(dtype).replace('torch.', '')}{size}")
 
@@ -1002,16 +1005,14 @@ def zs_reduce_shard_norm(contribs: Sequence, grad_out, max_norm: float, sumsq, n
     contribs = list(contribs)
     S = grad_out.numel()
     _typed(grad_out, "grad_out", torch.float32)
-    code = _contributions(contribs, S)
-    _typed(sumsq, "sumsq", torch.float64, 1)
-    _typed(workspace, "workspace", torch.uint8)
+    dev = grad_out.get_device()
+    code = _contributions(contribs, S, dev)
+    _typed(sumsq, "sumsq", torch.float64, 1, dev)
+    _typed(workspace, "workspace", torch.uint8, None, dev)
     if workspace.numel() < ZS_NORM_WORKSPACE:
         raise ValueError(f"workspace must hold {ZS_NORM_WORKSPACE} bytes")
-    side = [grad_out, sumsq, workspace]
     if norm_coef is not None:
-        _typed(norm_coef, "norm_coef", torch.float32, 2)
-        side.append(norm_coef)
-    _one_device(contribs + side, "zs_reduce_shard_norm")
+        _typed(norm_coef, "norm_coef", torch.float32, 2, dev)
     _enqueue(load().zs_reduce_shard_norm, grad_out, stream, _addresses(contribs),
              _groups(contribs, replicas), _opts(replicas, round_to_reduce_dtype, scale), code, S,
              grad_out.data_ptr(),
@@ -1030,32 +1031,34 @@ def zs_adamw_step_clip(p, m, v, w_out, contribs: Sequence, hp, grad_scale, repli
     contribs = list(contribs)
     S = p.numel()
     f32 = torch.float32
-    if not all([t.is_cuda and t.dtype == f32 and t.numel() == S and t.is_contiguous()
-                for t in (p, m, v)]):
-        for name, t in (("p", p), ("m", m), ("v", v)):
-            _typed(t, name, f32, S)
-    _dev(w_out, "w_out")
+    _typed(p, "p", f32)
+    dev = p.get_device()
+    _typed(m, "m", f32, S, dev)
+    _typed(v, "v", f32, S, dev)
+    _typed(grad_scale, "grad_scale", f32, 1, dev)
+    if w_out.get_device() != dev or not w_out.is_contiguous():
+        _same_device((p, _dev(w_out, "w_out")), "zs_adamw_step_clip")
     if _dtype_code(w_out) != ZS_BF16 or w_out.numel() != S:
         raise ValueError("w_out must be bf16 bits with S elements")
-    code = _contributions(contribs, S)
-    _typed(grad_scale, "grad_scale", torch.float32, 1)
-    _one_device([p, m, v, w_out, grad_scale] + contribs, "zs_adamw_step_clip")
+    code = _contributions(contribs, S, dev)
     _enqueue(load().zs_adamw_step_clip, p, stream, p.data_ptr(), m.data_ptr(), v.data_ptr(),
              w_out.data_ptr(), S, _addresses(contribs), _groups(contribs, replicas),
              _opts(replicas, round_to_reduce_dtype, scale, keep_working_shard), code,
              ctypes.byref(_hp(hp)), grad_scale.data_ptr())
 
 
-def _contributions(contribs, S) -> int:
-    """The element type of contributions of S elements each."""
+def _contributions(contribs, S, dev) -> int:
+    """The element type of contributions of S elements each, on device dev."""
     if not contribs:
         return ZS_F32
     code, dtype = _dtype_code(contribs[0]), contribs[0].dtype
     # one pass over all of them, then the failing one for the message
-    if not all([t.is_cuda and t.dtype == dtype and t.numel() == S and t.is_contiguous()
+    if not all([t.get_device() == dev and t.dtype is dtype and t.numel() == S and t.is_contiguous()
                 for t in contribs]):
         for i, c in enumerate(contribs):
             _dev(c, f"contribs[{i}]")
+            if c.get_device() != dev:
+                raise ValueError(f"contribs[{i}]: every tensor must be on one device")
             if c.numel() != S or _dtype_code(c) != code:
                 raise ValueError("contributions must share one dtype and hold S elements")
     return code
@@ -1168,9 +1171,11 @@ def zs_gather_matrix_f8(shards: Sequence, offset: int, out: F8Matrix = None, out
     if not shards:
         raise ValueError("need at least one shard")
     _quantized_shape(out, out_t)
-    S = shards[0].numel()
-    code = _contributions(shards, S)
-    _one_device(shards + [o for o in (out, out_t) if o is not None], "zs_gather_matrix_f8")
+    S, dev = shards[0].numel(), _dev(shards[0], "shards[0]").get_device()
+    code = _contributions(shards, S, dev)
+    for o in (out, out_t):
+        if o is not None and o.get_device() != dev:
+            raise ValueError("zs_gather_matrix_f8: every tensor must be on one device")
     _enqueue(load().zs_gather_matrix_f8, shards[0], stream, _addresses(shards), len(shards), S, code,
              int(offset), _c(out), _c(out_t))
 
