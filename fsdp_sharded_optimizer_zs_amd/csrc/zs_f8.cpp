@@ -347,11 +347,15 @@ ZS_EXPORT zs_status zs_linear_f8(const void* x, int32_t dtype, int64_t M, int64_
         return fail(ZS_EALIAS, "%s: y overlaps x, w or the workspace", who);
     if (overlap(rx, rw) || meets(*w, rw))
         return fail(ZS_EALIAS, "%s: the workspace overlaps x or w", who);
-    if (is_few(M, N, K)) {
+    const F8Plan plan = f8_plan(M, N, K);
+    if (plan.tm == kF8Few || f8_made(plan, K)) {
         const zs_f8_matrix a{nullptr, nullptr, M, K, type, 1};
-        F8Product p = product_of(a, *w, y, ldy, 0, f8_plan(M, N, K), nullptr, nullptr);
+        F8Product p = product_of(a, *w, y, ldy, 0, plan, nullptr, nullptr);
         p.x = x, p.ldx = ldx, p.cols = K;
-        return hip_status(launch_few_f8(p, dtype, type, w->type, y_dtype, stream), who);
+        return hip_status(plan.tm == kF8Few
+                              ? launch_few_f8(p, dtype, type, w->type, y_dtype, stream)
+                              : launch_linear_f8(p, dtype, type, w->type, y_dtype, stream),
+                          who);
     }
     uint8_t* const partial = static_cast<uint8_t*>(workspace) + kF8CountBytes;
     uint8_t* at = partial + partial_bytes(M, N, K);

@@ -54,7 +54,7 @@ struct F8Product {
     int tiles_m, tiles_n, splits;  // few rows: tiles_n is the plan's tn
     float* partial;    // splits > 1
     uint32_t* counts;  // likewise, 0 between calls
-    const void* x;     // few rows whose codes are made on the way: a's values, row r from
+    const void* x;     // where a's codes are made on the way: its values, row r from
     int64_t ldx, cols; // element r * ldx on (of a, only rows is read then)
 };
 // side: of the tiles, the plan's tm. two: a second product of the same tiles and types in the
@@ -64,5 +64,8 @@ hipError_t launch_matmul_f8(const F8Product& p, const F8Product* two, int side, 
 // Up to kF8Few rows of a; src: 0, a in codes, or the type of the values x.
 hipError_t launch_few_f8(const F8Product& p, int src, int type_a, int type_b, int dtype,
                          hipStream_t stream);
+// f8_made's products, of values x of type src.
+hipError_t launch_linear_f8(const F8Product& p, int src, int type_a, int type_b, int dtype,
+                            hipStream_t stream);
 
 }  // namespace zs

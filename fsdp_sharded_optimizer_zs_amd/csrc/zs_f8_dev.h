@@ -210,6 +210,41 @@ __device__ __forceinline__ bf16x8 widen(int w0, int w1, float two) {
 template <int TYPE>
 constexpr int kFormat = TYPE == ZS_E4M3 ? 0 : 1;
 
+// Elements [k, k + 8) of row m of p's values x, those past the last column +0.
+template <int DT>
+__device__ __forceinline__ Eight<DT> eight_of(const F8Product& p, int64_t m, int64_t k) {
+    Eight<DT> x{};
+    const int64_t at = m * p.ldx + k;
+    if (k + 8 <= p.cols) {
+        if constexpr (DT == ZS_BF16) {
+            const u32x4 h = *reinterpret_cast<const g_u32x4*>(global<const g_u16>(p.x) + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x.w[e] = h[e];
+        } else {
+            const g_f32x4* from = reinterpret_cast<const g_f32x4*>(global<const g_f32>(p.x) + at);
+            const f32x4 a = from[0], b = from[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x.f[e] = a[e], x.f[4 + e] = b[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < p.cols) load1<DT>(p.x, at + e, e, x);
+    }
+    return x;
+}
+
+// Codes of 8 elements of a row under scale byte s.
+template <int DT, int TYPE, bool ANY = true>
+__device__ __forceinline__ u32x2 eight_codes(const Eight<DT>& v, int s) {
+    if constexpr (DT == ZS_BF16)
+        return u32x2{four_codes<TYPE, ANY>(v.w[0], v.w[1], s),
+                     four_codes<TYPE, ANY>(v.w[2], v.w[3], s)};
+    else
+        return u32x2{four_codes<TYPE, ANY>(v.f[0], v.f[1], v.f[2], v.f[3], s),
+                     four_codes<TYPE, ANY>(v.f[4], v.f[5], v.f[6], v.f[7], s)};
+}
+
 // 4 neighbouring elements of a row of C.
 template <int DT>
 __device__ __forceinline__ void put4(const F8Product& p, int64_t m, int64_t n, int64_t N, f32x4 v) {

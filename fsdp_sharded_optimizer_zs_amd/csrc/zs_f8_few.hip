@@ -26,30 +26,6 @@ namespace {
 constexpr int kWaves = kF8FewWaves, kThreads = 2 * 64 * kWaves;
 constexpr int kB = kF8Block;
 
-// Elements [k, k + 8) of row m, those past the last column +0.
-template <int DT>
-__device__ __forceinline__ Eight<DT> eight_of(const F8Product& p, int64_t m, int64_t k) {
-    Eight<DT> x{};
-    const int64_t at = m * p.ldx + k;
-    if (k + 8 <= p.cols) {
-        if constexpr (DT == ZS_BF16) {
-            const u32x4 h = *reinterpret_cast<const g_u32x4*>(global<const g_u16>(p.x) + at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x.w[e] = h[e];
-        } else {
-            const g_f32x4* from = reinterpret_cast<const g_f32x4*>(global<const g_f32>(p.x) + at);
-            const f32x4 a = from[0], b = from[1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x.f[e] = a[e], x.f[4 + e] = b[e];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (k + e < p.cols) load1<DT>(p.x, at + e, e, x);
-    }
-    return x;
-}
-
 // All of a into LDS, by the threads of the workgroup's second half: 8 elements each, 4 such at
 // a time so that their loads are under way together; the 16 lanes of a block make the same
 // trips.
@@ -80,13 +56,7 @@ __device__ __forceinline__ void put_a(const F8Product& p, uint8_t* codes, uint8_
             if (u0 + v * kHalf >= units) continue;
             if constexpr (SRC != 0) {
                 s[v] = uint8_t(scale_of(row_max(top_bits<SRC>(x[v])), TA));
-                if constexpr (SRC == ZS_BF16)
-                    w[v] = u32x2{four_codes<TA>(x[v].w[0], x[v].w[1], s[v]),
-                                 four_codes<TA>(x[v].w[2], x[v].w[3], s[v])};
-                else
-                    w[v] = u32x2{
-                        four_codes<TA>(x[v].f[0], x[v].f[1], x[v].f[2], x[v].f[3], s[v]),
-                        four_codes<TA>(x[v].f[4], x[v].f[5], x[v].f[6], x[v].f[7], s[v])};
+                w[v] = eight_codes<SRC, TA>(x[v], s[v]);
             }
             *reinterpret_cast<u32x2*>(codes + m[v] * ld + 8 * k[v]) = w[v];
             if ((k[v] & 15) == 0) scales[m[v] * p.blocks + k[v] / 16] = s[v];

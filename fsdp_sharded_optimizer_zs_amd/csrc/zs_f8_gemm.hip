@@ -40,6 +40,7 @@ namespace zs {
 namespace {
 
 constexpr int kB = kF8Block;
+constexpr int kMakers = 1024;  // threads of a workgroup that makes a's codes
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -50,24 +51,62 @@ struct Shape {
     static constexpr int PM = TM / WM, PN = TN / WN, MI = PM / 32, NI = PN / 32;
     // LDS: a ring of 4 half steps (64 codes of each row of both operands), and twice the
     // scale bytes of 4 steps
-    static constexpr int kHalfRow = 64, kHalf = (TM + TN) * kHalfRow, kRing = 4 * kHalf;
-    static constexpr int kScale = (TM + TN) * 4, kLds = kRing + 2 * kScale;
-    // loads of a half step, a wavefront: of a, of b; and all wavefronts' loads of scales
-    static constexpr int kLoadsA = TM / 16 / W, kLoadsB = TN / 16 / W, kLoads = kLoadsA + kLoadsB;
-    static constexpr int kScaleLoads = (TM + TN) / 64;
+    static constexpr int kHalfRow = 64, kLds = 4 * (TM + TN) * kHalfRow + 2 * (TM + TN) * 4;
+    // where a's codes are made on the way: the ring is b's, all of a's codes stand behind it, by
+    // half steps too, and its scale bytes, by 4 steps
+    static constexpr int kMadeCodes = 4 * TN * kHalfRow + 2 * TN * 4;
+    static constexpr int kMadeScales = kMadeCodes + kF8MadeBlocks * 2 * TM * kHalfRow;
+    static constexpr int kMadeLds = kMadeScales + kF8MadeBlocks * TM;
     static constexpr bool kSplits = TM < 256;  // these may split K
     static_assert(TM % (16 * W) == 0 && TN % (16 * W) == 0 && TM % 64 == 0 && TN % 64 == 0 &&
                       PM % 32 == 0 && PN % 32 == 0,
                   "whole loads and parts");
 };
 
-// Workgroup `group` of p's tiles * splits.
-template <class S, int TA, int TB, int DT>
+// a's codes of a tile into LDS from its values x, by all kThreads threads of the workgroup: a
+// wavefront takes 512 elements at a time of each of its rows.
+template <class S, int SRC, int TA, int kThreads>
+__device__ __forceinline__ void make_a(const F8Product& p, int64_t m0, uint8_t* codes,
+                                       uint8_t* scales) {
+    constexpr int kWaves = kThreads / 64, kRows = S::TM / kWaves;
+    const int lane = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int64_t left = p.a.rows - m0;
+    const int rows = left < S::TM ? int(left) : S::TM;
+    for (int k = lane; k < 16 * p.blocks; k += 64) {
+        Eight<SRC> x[kRows];
+#pragma unroll
+        for (int v = 0; v < kRows; ++v)
+            if (wave + v * kWaves < rows) x[v] = eight_of<SRC>(p, m0 + wave + v * kWaves, 8 * k);
+#pragma unroll
+        for (int v = 0; v < kRows; ++v) {
+            const int row = wave + v * kWaves;
+            if (row >= rows) break;
+            const uint32_t u = row_max(top_bits<SRC>(x[v]));
+            const int s = scale_of(u, TA);
+            const u32x2 w = __any(is_special(u, s)) ? eight_codes<SRC, TA, true>(x[v], s)
+                                                    : eight_codes<SRC, TA, false>(x[v], s);
+            const int piece = ((k >> 1) & 3) ^ ((row >> 2) & 3);
+            *reinterpret_cast<u32x2*>(codes + ((k >> 3) * S::TM + row) * S::kHalfRow + piece * 16 +
+                                      (k & 1) * 8) = w;
+            if ((k & 15) == 0) scales[((k >> 6) * S::TM + row) * 4 + ((k >> 4) & 3)] = uint8_t(s);
+        }
+    }
+}
+
+// Workgroup `group` of p's tiles * splits. SRC: 0, a in codes, or the type of its values, whose
+// codes are made first, by kThreads threads.
+template <class S, int TA, int TB, int DT, int SRC = 0, int kThreads = S::kThreads>
 __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, uint8_t* big) {
     constexpr bool EXACT = DT == ZS_F32;
+    constexpr bool MADE = SRC != 0;
     constexpr int TM = S::TM, TN = S::TN, W = S::W, MI = S::MI, NI = S::NI;
-    constexpr int kHalfRow = S::kHalfRow, kHalf = S::kHalf, kOperand = TM * kHalfRow;
-    constexpr int kScales = S::kRing, kScale = S::kScale, kLoads = S::kLoads;
+    constexpr int kRowsA = MADE ? 0 : TM, kHalfRow = S::kHalfRow, kOperand = kRowsA * kHalfRow;
+    constexpr int kHalf = (kRowsA + TN) * kHalfRow, kScales = 4 * kHalf;
+    constexpr int kScale = (kRowsA + TN) * 4;
+    // loads of a half step, a wavefront: of a, of b; and all wavefronts' loads of scales
+    constexpr int kLoadsA = kRowsA / 16 / W, kLoads = kLoadsA + TN / 16 / W;
+    constexpr int kScaleLoads = (kRowsA + TN) / 64;
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     // Each XCD takes a run of tiles, 8 rows of tiles deep; a tile's splits are neighbours.
@@ -83,6 +122,15 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
     const int first = int(int64_t(p.blocks) * split / p.splits);
     const int last = int(int64_t(p.blocks) * (split + 1) / p.splits) - 1;
 
+    if constexpr (MADE) {
+        if (wave >= W) {  // these only help to make a's codes (K > 0: first <= last)
+            make_a<S, SRC, TA, kThreads>(p, m0, big + S::kMadeCodes, big + S::kMadeScales);
+            arrived_but<0>();
+            __builtin_amdgcn_s_barrier();
+            return;
+        }
+    }
+
     // What this lane loads: of each half step 16 bytes of kLoads rows, 16 * W apart, first of a,
     // then of b; and the scale bytes of a row. Rows past an operand's last are its last again:
     // what they give is not stored.
@@ -91,46 +139,46 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
     const int piece = ((lane & 3) ^ ((lane >> 4) & 3)) * 16;
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
-        const bool is_a = k < S::kLoadsA;
-        const int64_t r = 16 * ((is_a ? k : k - S::kLoadsA) * W + wave) + (lane >> 2);
+        const bool is_a = k < kLoadsA;
+        const int64_t r = 16 * ((is_a ? k : k - kLoadsA) * W + wave) + (lane >> 2);
         off[k] = is_a ? uint32_t((r < last_a ? r : last_a) * p.a.ld) + piece
                       : uint32_t((r < last_b ? r : last_b) * p.b.ld) + piece;
     }
     const uint8_t* const codes_a = p.a.codes + m0 * p.a.ld;
     const uint8_t* const codes_b = p.b.codes + n0 * p.b.ld;
-    constexpr int kMine = (S::kScaleLoads + W - 1) / W;
+    constexpr int kMine = (kScaleLoads + W - 1) / W;
     uint32_t off_s[kMine];
     const uint8_t* base_s[kMine];
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
         const int part = wave * kMine + k;  // of 64 rows: of a, then of b
-        const bool is_a = part < TM / 64;
+        const bool is_a = part < kRowsA / 64;
         const F8Operand& x = is_a ? p.a : p.b;
         const int64_t from = is_a ? m0 : n0, end = is_a ? last_a : last_b;
-        const int64_t r = 64 * (is_a ? part : part - TM / 64) + lane;
+        const int64_t r = 64 * (is_a ? part : part - kRowsA / 64) + lane;
         base_s[k] = x.scales + (from >> x.shift) * x.lds;
         off_s[k] = uint32_t((((r < end ? r : end) + (from & ((1 << x.shift) - 1))) >> x.shift) * x.lds);
     }
     const uint32_t lds0 = lds_address(big);
     const auto fetch = [&](int block, int half, int slot, int k) {
-        const bool is_a = k < S::kLoadsA;
+        const bool is_a = k < kLoadsA;
         load_to_lds((is_a ? codes_a : codes_b) + int64_t(block) * kB + half * kHalfRow, off[k],
                     lds0 + slot * kHalf + (is_a ? 0 : kOperand) +
-                        ((is_a ? k : k - S::kLoadsA) * W + wave) * 1024);
+                        ((is_a ? k : k - kLoadsA) * W + wave) * 1024);
     };
     const auto fetch_scales = [&](int word) {
 #pragma unroll
         for (int k = 0; k < kMine; ++k)
-            if (wave * kMine + k < S::kScaleLoads)
+            if (wave * kMine + k < kScaleLoads)
                 load4_to_lds(base_s[k] + int64_t(word) * 4, off_s[k],
                              lds0 + kScales + (word & 1) * kScale + (wave * kMine + k) * 256);
     };
     // a lane's 32 codes of a half step, of row `lane % 32` of a 32-row part
     const int row = lane & 31, g = lane >> 5;
-    const uint8_t* const read_a = big + (wm + row) * kHalfRow;
+    const uint8_t* const read_a = big + (MADE ? S::kMadeCodes : 0) + (wm + row) * kHalfRow;
     const uint8_t* const read_b = big + kOperand + (wn + row) * kHalfRow;
-    const auto part = [&](const uint8_t* from, int slot, int i) {
-        const uint8_t* x = from + slot * kHalf + i * 32 * kHalfRow;
+    const auto part = [&](const uint8_t* from, int i) {
+        const uint8_t* x = from + i * 32 * kHalfRow;
         const int swap = (row >> 2) & 3;
         const i32x4 lo = *reinterpret_cast<const i32x4*>(x + (((2 * g) ^ swap) * 16));
         const i32x4 hi = *reinterpret_cast<const i32x4*>(x + (((2 * g + 1) ^ swap) * 16));
@@ -139,22 +187,26 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
     f32x16 acc[NI][MI] = {};
     uint32_t sa[MI], sb[NI];
     i32x8 a0[MI], b0[NI], a1[MI], b1[NI];
-    const auto read = [&](int slot, i32x8 (&a)[MI], i32x8 (&b)[NI]) {
+    // half: of all half steps, in `slot` of the ring
+    const auto read = [&](int half, int slot, i32x8 (&a)[MI], i32x8 (&b)[NI]) {
+        const uint8_t* const from_a = read_a + (MADE ? half * TM * kHalfRow : slot * kHalf);
+        const uint8_t* const from_b = read_b + slot * kHalf;
 #pragma unroll
         for (int i = 0; i < (MI > NI ? MI : NI); ++i) {
-            if (i < MI) a[i] = part(read_a, slot, i);
-            if (i < NI) b[i] = part(read_b, slot, i);
+            if (i < MI) a[i] = part(from_a, i);
+            if (i < NI) b[i] = part(from_b, i);
         }
     };
     const auto read_scales = [&](int k, uint32_t (&x)[MI], uint32_t (&y)[NI]) {
         const uint8_t* from = big + kScales + ((k >> 2) & 1) * kScale + row * 4;
+        const uint8_t* from_a = MADE ? big + S::kMadeScales + (k >> 2) * TM * 4 + row * 4 : from;
         const int byte = 8 * (k & 3);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
-            x[i] = *reinterpret_cast<const uint32_t*>(from + (wm + 32 * i) * 4) >> byte;
+            x[i] = *reinterpret_cast<const uint32_t*>(from_a + (wm + 32 * i) * 4) >> byte;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-            y[i] = *reinterpret_cast<const uint32_t*>(from + (TM + wn + 32 * i) * 4) >> byte;
+            y[i] = *reinterpret_cast<const uint32_t*>(from + (kRowsA + wn + 32 * i) * 4) >> byte;
     };
     const auto multiply = [&](const i32x8 (&a)[MI], const i32x8 (&b)[NI]) {
         if constexpr (!EXACT) {
@@ -189,9 +241,11 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
         for (int h = 0; h < 4; ++h)
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) fetch(min(first + (h >> 1), last), h & 1, h, k);
+        if constexpr (MADE)
+            make_a<S, SRC, TA, kThreads>(p, m0, big + S::kMadeCodes, big + S::kMadeScales);
         arrived_but<3 * kLoads>();
         __builtin_amdgcn_s_barrier();
-        read(0, a0, b0);
+        read(2 * first, 0, a0, b0);
         read_scales(first, sa, sb);
     }
     // A half step multiplies what was read in the one before, reads the next one's codes and,
@@ -207,7 +261,7 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) fetch(then, 0, two, u);
-        read(two + 1, a1, b1);
+        read(2 * k + 1, two + 1, a1, b1);
         multiply(a0, b0);
         __builtin_amdgcn_sched_barrier(0);
         arrived_but<2 * kLoads>();
@@ -216,7 +270,7 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) fetch(then, 1, two + 1, u);
         uint32_t ta[MI], tb[NI];
-        read(two ^ 2, a0, b0);
+        read(2 * min(k + 1, last), two ^ 2, a0, b0);
         read_scales(min(k + 1, last), ta, tb);
         multiply(a1, b1);
 #pragma unroll
@@ -228,7 +282,7 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
     arrived();
     __builtin_amdgcn_s_barrier();
 
-    if (S::kSplits && p.splits > 1) {
+    if (S::kSplits && !MADE && p.splits > 1) {
         // partial sums as the lanes hold them, written through to memory that all XCDs share;
         // the workgroup that counts in last adds them in their order
         typedef uint64_t u64x8 __attribute__((ext_vector_type(8)));
@@ -279,7 +333,7 @@ __device__ __forceinline__ void matmul_tile(const F8Product& p, unsigned group, 
                     acc[j][i] += __builtin_bit_cast(f32x16, v);
                 }
     }
-    if (DT == ZS_BF16 && p.accumulate) {  // the old value is added before the one rounding
+    if (!MADE && DT == ZS_BF16 && p.accumulate) {  // the old value is added before the one rounding
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int64_t m = m0 + wm + 32 * i + row;
@@ -363,6 +417,16 @@ __global__ __launch_bounds__(S::kThreads, 1) void matmul2_kernel(F8Product one, 
     matmul_tile<S, TA, TB, DT>(is_one ? one : two, is_one ? blockIdx.x : blockIdx.x - groups1, big);
 }
 
+// One whose a is given by values: a linear layer in one launch. All of a's codes stay in LDS,
+// the ring is b's alone; 16 wavefronts make the codes, while the first of b are under way, and
+// the 4 that multiply stay. Making them is bound by VALU instructions, some 2.7 us for K = 1024
+// (f8_made has what that means against two launches).
+template <class S, int SRC, int TA, int TB, int DT>
+__global__ __launch_bounds__(kMakers) void linear_kernel(F8Product p) {
+    __shared__ __attribute__((aligned(16))) uint8_t big[S::kMadeLds];
+    matmul_tile<S, TA, TB, DT, SRC, kMakers>(p, blockIdx.x, big);
+}
+
 unsigned groups_of(const F8Product& p) {
     return unsigned(int64_t(p.tiles_m) * p.tiles_n * p.splits);
 }
@@ -396,7 +460,37 @@ void launch_types(const F8Product& p, const F8Product* two, int side, int dtype,
     else launch_shape<Shape<64, 64, 2, 2>, TA, TB>(p, two, dtype, stream);
 }
 
+using Made = Shape<64, 64, 2, 2>;
+static_assert(kF8MadeSide == 64 && Made::kMadeLds <= 163840, "one workgroup's LDS");
+
+template <int SRC, int TA, int TB>
+void launch_linear(const F8Product& p, int dtype, hipStream_t stream) {
+    const dim3 grid(groups_of(p)), block(kMakers);
+    if (dtype == ZS_BF16)
+        hipLaunchKernelGGL((linear_kernel<Made, SRC, TA, TB, ZS_BF16>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((linear_kernel<Made, SRC, TA, TB, ZS_F32>), grid, block, 0, stream, p);
+}
+template <int SRC>
+void launch_linear_types(const F8Product& p, int type_a, int type_b, int dtype,
+                         hipStream_t stream) {
+    if (type_a == ZS_E4M3) {
+        if (type_b == ZS_E4M3) launch_linear<SRC, ZS_E4M3, ZS_E4M3>(p, dtype, stream);
+        else launch_linear<SRC, ZS_E4M3, ZS_E5M2>(p, dtype, stream);
+    } else {
+        if (type_b == ZS_E4M3) launch_linear<SRC, ZS_E5M2, ZS_E4M3>(p, dtype, stream);
+        else launch_linear<SRC, ZS_E5M2, ZS_E5M2>(p, dtype, stream);
+    }
+}
+
 }  // namespace
+
+hipError_t launch_linear_f8(const F8Product& p, int src, int type_a, int type_b, int dtype,
+                            hipStream_t stream) {
+    if (src == ZS_BF16) launch_linear_types<ZS_BF16>(p, type_a, type_b, dtype, stream);
+    else launch_linear_types<ZS_F32>(p, type_a, type_b, dtype, stream);
+    return hipGetLastError();
+}
 
 hipError_t launch_matmul_f8(const F8Product& p, const F8Product* two, int side, int type_a,
                             int type_b, int dtype, hipStream_t stream) {

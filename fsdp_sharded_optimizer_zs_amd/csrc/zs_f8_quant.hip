@@ -93,16 +93,7 @@ struct Shared {
 template <int DT>
 using Part = Eight<DT>[2][4];
 
-// Codes of 8 elements of a row, and of 4 rows of column e.
-template <int DT, int TYPE, bool ANY>
-__device__ __forceinline__ u32x2 row_codes(const Eight<DT>& v, int s) {
-    if constexpr (DT == ZS_BF16)
-        return u32x2{four_codes<TYPE, ANY>(v.w[0], v.w[1], s),
-                     four_codes<TYPE, ANY>(v.w[2], v.w[3], s)};
-    else
-        return u32x2{four_codes<TYPE, ANY>(v.f[0], v.f[1], v.f[2], v.f[3], s),
-                     four_codes<TYPE, ANY>(v.f[4], v.f[5], v.f[6], v.f[7], s)};
-}
+// Codes of 4 rows of column e.
 template <int DT, int TYPE, bool ANY>
 __device__ __forceinline__ uint32_t col_codes(const Eight<DT> (&v)[4], int e, int s) {
     if constexpr (DT == ZS_BF16) {
@@ -123,7 +114,7 @@ __device__ __forceinline__ void put_rows(const F8Quant& q, const Part<DT>& x, co
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t r = row0 + 64 * h + i;
-            const u32x2 w = row_codes<DT, TYPE, ANY>(x[h][i], s[h][i]);
+            const u32x2 w = eight_codes<DT, TYPE, ANY>(x[h][i], s[h][i]);
             if (r >= q.rows) continue;
             *global<g_u32x2a>(q.out.codes + r * q.out.ld + tc * kT + 8 * cg) = w;
             if (BR == 1 && cg < 4) put_scale(q.out, r, tc, blocks, cg, s[h][i]);

@@ -408,6 +408,31 @@ def test_linear(M, N, K, dtype, y_dtype):
         check_beside(store, full, N, lead, "linear")
 
 
+@pytest.mark.parametrize("y_dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("M,N,K", [(17, 1, 1), (17, 64, 127), (33, 100, 128), (64, 64, 2048), (64, 70, 2049), (65, 1000, 513),
+                                   (100, 65, 640), (1000, 700, 900), (777, 1001, 1500), (2048, 256, 1024), (129, 4000, 2047),
+                                   (16, 300, 2000), (5, 40, 700), (40, 3000, 5000), (300, 20_000, 200)])
+def test_linear_is_its_two_calls(M, N, K, y_dtype):
+    """Codes that are made on the way give the bits of the quantiser's codes, in every form."""
+    for i, (dtype, kind, kind_w, br, pad, lead) in enumerate([
+            ("bf16", F.E4M3, F.E4M3, 128, 0, 0), ("f32", F.E5M2, F.E4M3, 1, 3, 1), ("bf16", F.E5M2, F.E5M2, 128, 5, 3),
+            ("f32", F.E4M3, F.E5M2, 128, 0, 0)]):
+        x, _ = on_device(matrix(M, K, i) * np.exp(matrix(M, 1, i + 9)), dtype, pad, lead)
+        if i == 1:
+            x[M // 2, K // 2] = float("inf")
+            x[M // 3] = 2.0**-140
+        w, _ = f8(matrix(N, K, 50 + i), kind_w, br)
+        _, _, want = out_matrix(M, N, y_dtype)
+        store, full, y = out_matrix(M, N, y_dtype, pad, lead)
+        codes = zs.F8Matrix.empty(M, K, kind)
+        zs.zs_quantize_f8(x, codes)
+        zs.zs_matmul_f8(codes, w, want, workspace=workspace(M, N, K))
+        zs.zs_linear_f8(x, w, y, workspace(M, N, K, zs.zs_linear_f8_workspace), type=kind)
+        assert torch.equal(y.view(torch.int16 if y_dtype == "bf16" else torch.int32),
+                           want.view(torch.int16 if y_dtype == "bf16" else torch.int32)), i
+        check_beside(store, full, N, lead, f"{i}")
+
+
 @pytest.mark.parametrize("M", (1, 2, 5, 16, 40))
 def test_linear_of_not_finite_rows(M):
     x, h = on_device(whole(M, 300, 3), "bf16")
