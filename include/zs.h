@@ -999,7 +999,7 @@ zs_status zs_matmul_f8_workspace(int64_t M, int64_t N, int64_t K, int64_t* bytes
 /*
  * zs_linear_f8 -- a linear layer over 8-bit weights: y = Q(x) w^T with Q the quantiser of
  * zs_quantize_f8 with 1 x 128 blocks, then zs_matmul_f8, with the same results; up to 16
- * rows (serving: one new token) in one launch.
+ * rows (serving: one new token) and small layers in one launch.
  *
  *   x     device, M x K elements of dtype, row stride ldx;  type  of its codes
  *   w     N x K, block_rows 1 or 128 (a gathered matrix)
