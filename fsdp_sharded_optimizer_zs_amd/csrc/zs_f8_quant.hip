@@ -2,21 +2,23 @@
 // and transposed, from one read), the same of a matrix that lies in a unit's shards, and
 // the values that codes stand for.
 //
-// All stream once over their data. A workgroup of 4 wavefronts takes a 128 x 128 tile, so
+// All stream once over their data. A workgroup of 8 wavefronts takes a 128 x 128 tile, so
 // that the blocks of both forms are whole in it. Lane l of wavefront w holds 8 columns
-// (from 8 (l % 16) on) of the rows 64 h + 16 w + 4 (l / 16) + i, h < 2, i < 4: 16 lanes cover
-// 256 bytes of a bf16 row, a row's block of 128 is the 16 lanes of a DPP row, and the 4
-// rows i of a column are one word of transposed codes. Those words are exchanged through
-// LDS (16 KiB) so that the transpose leaves in 16-byte pieces of whole 128-byte runs too.
+// (from 8 (l % 16) on) of the rows 16 w + 4 (l / 16) + i, i < 4: 16 lanes cover 256 bytes of a
+// bf16 row, a row's block of 128 is the 16 lanes of a DPP row, and the 4 rows i of a column
+// are one word of transposed codes. Those words are exchanged through LDS (16 KiB) so that the
+// transpose leaves in 16-byte pieces of whole 128-byte runs too.
 //
-// Memory bounds them: 2 or 4 bytes read and 1 written for each element and form. Blocks of one
-// row cost a maximum, a scale and its checks for each of 128 rows and columns of a tile on top,
-// which shows. Measured from memory, 4096 x 11008 in us (TB/s), as it is / transposed / both:
-//   bf16, blocks of 1 x 128      28.9 (4.7) / 30.0 (4.5) / 41.4 (4.4)
-//   bf16, 128 x 128              25.7 (5.3) / 26.7 (5.1) / 34.2 (5.3)
-//   fp32, 1 x 128                53.8 (4.2) / 55.2 (4.1) / 67.2 (4.0)
-//   fp32, 128 x 128              46.7 (4.8) / 53.1 (4.2) / 57.7 (4.7)
-// and both forms from shards in bf16 39.5 (4.6) in blocks of 128 x 128; back to bf16 22.9 (5.9).
+// Memory bounds them: 2 or 4 bytes read and 1 written for each element and form. Measured from
+// memory, 4096 x 11008 in us (TB/s), as it is / transposed / both / both from 4 shards:
+//   bf16, blocks of 1 x 128      27.9 (4.9) / 28.5 (4.8) / 37.5 (4.8) / 43.6
+//   bf16, 128 x 128              26.6 (5.1) / 27.7 (4.9) / 35.0 (5.2) / 39.4
+//   fp32, 1 x 128                49.9 (4.5) / 53.5 (4.2) / 60.4 (4.5) / 64.6
+//   fp32, 128 x 128              45.5 (5.0) / 49.8 (4.5) / 53.7 (5.0) / 55.8
+// and back to bf16 22.9 (5.9). Tiles by 4 wavefronts of twice the rows: 28.5, 28.0, 39.5 and
+// 49.0 in the first line, 24.5, 25.5, 33.2, 40.0 in the second; a small matrix, whose tiles
+// leave CUs idle, takes longer by them (2048 x 1024, both forms 6.5 us against 5.6, from shards
+// 7.5 against 5.7), and fp32 needs twice the registers.
 
 #include "zs_f8_dev.h"
 
@@ -26,6 +28,7 @@ namespace zs {
 namespace {
 
 constexpr int kThreads = kBlockThreads;
+constexpr int kWaves = 8, kTileThreads = 64 * kWaves;  // of a tile to be quantised
 constexpr int kT = kF8Block;  // side of a tile
 
 // A matrix in memory, row r from element r * ldx on.
@@ -85,13 +88,20 @@ __device__ __forceinline__ void put_scale(const F8Out& o, int64_t row, int64_t b
 
 struct Shared {
     uint32_t codes[kT * kT / 4];
-    uint32_t top[4][kT];
-    uint32_t whole[4];
+    uint32_t top[kWaves][kT];
+    __attribute__((aligned(16))) int scale[kT];
+    uint32_t whole[kWaves];
 };
+__device__ __forceinline__ uint32_t max_of(const uint32_t* x, int step) {
+    uint32_t u = x[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) u = max_u(u, x[w * step]);
+    return u;
+}
 
-// A lane's elements of a tile, rows 64 h + 16 w + 4 (l / 16) + i.
+// A lane's elements of a tile, rows 16 w + 4 (l / 16) + i.
 template <int DT>
-using Part = Eight<DT>[2][4];
+using Part = Eight<DT>[4];
 
 // Codes of 4 rows of column e.
 template <int DT, int TYPE, bool ANY>
@@ -106,19 +116,17 @@ __device__ __forceinline__ uint32_t col_codes(const Eight<DT> (&v)[4], int e, in
 }
 
 template <int DT, int BR, int TYPE, bool ANY>
-__device__ __forceinline__ void put_rows(const F8Quant& q, const Part<DT>& x, const int (&s)[2][4],
+__device__ __forceinline__ void put_rows(const F8Quant& q, const Part<DT>& x, const int (&s)[4],
                                          int64_t row0, int64_t tc, int cg) {
     const int64_t blocks = f8_ceil(q.cols, kT);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = row0 + 64 * h + i;
-            const u32x2 w = eight_codes<DT, TYPE, ANY>(x[h][i], s[h][i]);
-            if (r >= q.rows) continue;
-            *global<g_u32x2a>(q.out.codes + r * q.out.ld + tc * kT + 8 * cg) = w;
-            if (BR == 1 && cg < 4) put_scale(q.out, r, tc, blocks, cg, s[h][i]);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = row0 + i;
+        const u32x2 w = eight_codes<DT, TYPE, ANY>(x[i], s[i]);
+        if (r >= q.rows) continue;
+        *global<g_u32x2a>(q.out.codes + r * q.out.ld + tc * kT + 8 * cg) = w;
+        if (BR == 1 && cg < 4) put_scale(q.out, r, tc, blocks, cg, s[i]);
+    }
 }
 template <int DT, int TYPE, bool ANY>
 __device__ __forceinline__ void stage_cols(const Part<DT>& x, const int (&s)[8], int wave, int cg,
@@ -126,11 +134,9 @@ __device__ __forceinline__ void stage_cols(const Part<DT>& x, const int (&s)[8],
     // word (column, 4 rows): the 16-byte pieces of a column's 128 are permuted by its number
     // over 8, so that the 16 columns that a wavefront writes at once fall on other banks
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sh.codes[(8 * cg + e) * 32 + 4 * ((4 * h + wave) ^ (cg & 7)) + rq] =
-                col_codes<DT, TYPE, ANY>(x[h], e, s[e]);
+    for (int e = 0; e < 8; ++e)
+        sh.codes[(8 * cg + e) * 32 + 4 * (wave ^ (cg & 7)) + rq] =
+            col_codes<DT, TYPE, ANY>(x, e, s[e]);
 }
 
 // One tile. BR = 1: a block for each row (column, transposed) of the tile, BR = 128: one.
@@ -144,36 +150,29 @@ __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int
     const int live = q.cols - c >= 8 ? 8 : (q.cols > c ? int(q.cols - c) : 0);
     Part<DT> x;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = row0 + 64 * h + i;
-            if (r < q.rows && live > 0) x[h][i] = src.template get<DT>(r, c, live);
-            else x[h][i] = Eight<DT>{};
-        }
+    for (int i = 0; i < 4; ++i) {
+        if (row0 + i < q.rows && live > 0) x[i] = src.template get<DT>(row0 + i, c, live);
+        else x[i] = Eight<DT>{};
+    }
     uint32_t whole = 0;
     if constexpr (BR == 128) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) whole = max_u(whole, top_bits<DT>(x[h][i]));
+        for (int i = 0; i < 4; ++i) whole = max_u(whole, top_bits<DT>(x[i]));
         whole = col_max(row_max(whole));
         if (lane == 0) sh.whole[wave] = whole;
         __syncthreads();
-        whole = max_u(max_u(sh.whole[0], sh.whole[1]), max_u(sh.whole[2], sh.whole[3]));
+        whole = max_of(sh.whole, 1);
     }
     if (q.out.codes != nullptr) {
         const int type = q.out.type;
-        int s[2][4];
+        int s[4];
         bool special = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t u = BR == 128 ? whole : row_max(top_bits<DT>(x[h][i]));
-                s[h][i] = scale_of(u, type);
-                special |= is_special(u, s[h][i]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = BR == 128 ? whole : row_max(top_bits<DT>(x[i]));
+            s[i] = scale_of(u, type);
+            special |= is_special(u, s[i]);
+        }
         if (__any(special)) {
             if (type == ZS_E4M3) put_rows<DT, BR, ZS_E4M3, true>(q, x, s, row0, tc, cg);
             else put_rows<DT, BR, ZS_E5M2, true>(q, x, s, row0, tc, cg);
@@ -190,14 +189,14 @@ __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int
     int s[8];
     bool special = false;
     if constexpr (BR == 1) {
-        // a column's largest magnitude: of the lane's 8 rows, the wavefront's 32, all 128
+        // a column's largest magnitude: of the lane's 4 rows, the wavefront's 16, all 128
         if constexpr (DT == ZS_BF16) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                u16x2 u = mags(x[0][0].w[k]);
+                u16x2 u = mags(x[0].w[k]);
 #pragma unroll
-                for (int i = 1; i < 8; ++i)
-                    u = __builtin_elementwise_max(u, mags(x[i / 4][i % 4].w[k]));
+                for (int i = 1; i < 4; ++i)
+                    u = __builtin_elementwise_max(u, mags(x[i].w[k]));
                 const uint32_t two = col_max_pair(__builtin_bit_cast(uint32_t, u));
                 if (rq == 0) {
                     sh.top[wave][8 * cg + 2 * k] = two << 16;
@@ -209,27 +208,30 @@ __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int
             for (int e = 0; e < 8; ++e) {
                 uint32_t u = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    u = max_u(u, __float_as_uint(x[i / 4][i % 4].f[e]) & 0x7fffffffu);
+                for (int i = 0; i < 4; ++i)
+                    u = max_u(u, __float_as_uint(x[i].f[e]) & 0x7fffffffu);
                 u = col_max(u);
                 if (rq == 0) sh.top[wave][8 * cg + e] = u;
             }
         }
         __syncthreads();
-        const auto top = [&](int k) {
-            return max_u(max_u(sh.top[0][k], sh.top[1][k]), max_u(sh.top[2][k], sh.top[3][k]));
-        };
+        // one thread a column joins the wavefronts' maxima; bit 8 of its word: a special block
+        if (threadIdx.x < kT) {
+            const uint32_t u = max_of(&sh.top[0][threadIdx.x], kT);
+            const int mine = scale_of(u, type);
+            sh.scale[threadIdx.x] = mine | (is_special(u, mine) ? 256 : 0);
+            const int64_t col = tc * kT + int(threadIdx.x);
+            if (col < q.cols) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) put_scale(q.out_t, col, tr, blocks_r, k, mine);
+            }
+        }
+        __syncthreads();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint32_t u = top(8 * cg + e);
-            s[e] = scale_of(u, type);
-            special |= is_special(u, s[e]);
-        }
-        const int64_t col = tc * kT + int(threadIdx.x);
-        if (threadIdx.x < kT && col < q.cols) {
-            const int mine = scale_of(top(int(threadIdx.x)), type);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) put_scale(q.out_t, col, tr, blocks_r, k, mine);
+            const int w = sh.scale[8 * cg + e];
+            s[e] = w & 255;
+            special |= w > 255;
         }
     } else {
 #pragma unroll
@@ -247,8 +249,8 @@ __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int col = 32 * k + int(threadIdx.x) / 8, piece = int(threadIdx.x) % 8;
+    for (int k = 0; k < 16 / kWaves; ++k) {
+        const int col = 8 * kWaves * k + int(threadIdx.x) / 8, piece = int(threadIdx.x) % 8;
         if (tc * kT + col < q.cols) {
             const u32x4 w = *reinterpret_cast<const u32x4*>(
                 &sh.codes[col * 32 + 4 * (piece ^ ((col >> 3) & 7))]);
@@ -257,14 +259,9 @@ __device__ __forceinline__ void quant_tile(const F8Quant& q, const Src& src, int
     }
 }
 
-// Wavefronts to a SIMD: what the registers of a tile's elements allow without spilling (fp32 in
-// blocks of one row, 3 wavefronts and 22 registers spilled: 59.6 / 75.8 / 86.8 us above).
-template <int DT, int BR>
-constexpr int kDepth = DT == ZS_BF16 || BR == 128 ? 4 : 2;
-
 // One matrix, or (tiles2 > 0) two in one launch.
 template <int DT, int BR>
-__global__ __launch_bounds__(kThreads, (kDepth<DT, BR>)) void quantize_kernel(
+__global__ __launch_bounds__(kTileThreads, 4) void quantize_kernel(
     F8Quant one, F8Quant two, uint32_t tiles1, uint32_t tiles2) {
     __shared__ Shared sh;
     for (uint32_t t = blockIdx.x; t < tiles1 + tiles2; t += gridDim.x) {
@@ -278,7 +275,7 @@ __global__ __launch_bounds__(kThreads, (kDepth<DT, BR>)) void quantize_kernel(
 }
 
 template <int DT, int BR>
-__global__ __launch_bounds__(kThreads, (kDepth<DT, BR>)) void gather_kernel(F8Quant q, F8Shards s) {
+__global__ __launch_bounds__(kTileThreads, 4) void gather_kernel(F8Quant q, F8Shards s) {
     __shared__ Shared sh;
     const uint32_t tiles_c = uint32_t(f8_ceil(q.cols, kT));
     const uint32_t tiles = tiles_c * uint32_t(f8_ceil(q.rows, kT));  // checked: below 2^31
@@ -370,7 +367,7 @@ hipError_t launch_quantize_f8(const F8Quant& q, int block_rows, hipStream_t stre
     const uint32_t tiles = uint32_t(f8_tiles(q.rows, q.cols));  // checked: below 2^31
     const dim3 grid(unsigned(f8_tile_grid(tiles)));
     const auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, q, q, tiles, 0u);
+        hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), 0, stream, q, q, tiles, 0u);
     };
     if (q.dtype == ZS_BF16) {
         if (block_rows == 1) go(quantize_kernel<ZS_BF16, 1>);
@@ -387,10 +384,10 @@ hipError_t launch_quantize2_f8(const F8Quant& one, const F8Quant& two, hipStream
                    b = uint32_t(f8_tiles(two.rows, two.cols));  // checked: each below 2^30
     const dim3 grid(unsigned(f8_tile_grid(int64_t(a) + b)));
     if (one.dtype == ZS_BF16)
-        hipLaunchKernelGGL((quantize_kernel<ZS_BF16, 1>), grid, dim3(kThreads), 0, stream, one, two,
+        hipLaunchKernelGGL((quantize_kernel<ZS_BF16, 1>), grid, dim3(kTileThreads), 0, stream, one, two,
                            a, b);
     else
-        hipLaunchKernelGGL((quantize_kernel<ZS_F32, 1>), grid, dim3(kThreads), 0, stream, one, two,
+        hipLaunchKernelGGL((quantize_kernel<ZS_F32, 1>), grid, dim3(kTileThreads), 0, stream, one, two,
                            a, b);
     return hipGetLastError();
 }
@@ -400,15 +397,15 @@ hipError_t launch_gather_f8(const F8Quant& q, const F8Shards& src, int block_row
     const dim3 grid(unsigned(f8_tile_grid(f8_tiles(q.rows, q.cols))));
     if (q.dtype == ZS_BF16) {
         if (block_rows == 1)
-            hipLaunchKernelGGL((gather_kernel<ZS_BF16, 1>), grid, dim3(kThreads), 0, stream, q, src);
+            hipLaunchKernelGGL((gather_kernel<ZS_BF16, 1>), grid, dim3(kTileThreads), 0, stream, q, src);
         else
-            hipLaunchKernelGGL((gather_kernel<ZS_BF16, 128>), grid, dim3(kThreads), 0, stream, q,
+            hipLaunchKernelGGL((gather_kernel<ZS_BF16, 128>), grid, dim3(kTileThreads), 0, stream, q,
                                src);
     } else {
         if (block_rows == 1)
-            hipLaunchKernelGGL((gather_kernel<ZS_F32, 1>), grid, dim3(kThreads), 0, stream, q, src);
+            hipLaunchKernelGGL((gather_kernel<ZS_F32, 1>), grid, dim3(kTileThreads), 0, stream, q, src);
         else
-            hipLaunchKernelGGL((gather_kernel<ZS_F32, 128>), grid, dim3(kThreads), 0, stream, q,
+            hipLaunchKernelGGL((gather_kernel<ZS_F32, 128>), grid, dim3(kTileThreads), 0, stream, q,
                                src);
     }
     return hipGetLastError();
