@@ -88,10 +88,10 @@ inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
 // Whether a linear layer's product makes a's codes on the way, in every workgroup those of its
 // own rows: one launch instead of two, where a CU takes one tile at most and K is short enough
 // that making the same codes again for every 64 columns costs less than a launch. Measured, us,
-// one launch against two, bf16: 17 x 64 x 128 4.0, 6.0; 512 x 512 x 256 5.4, 8.3;
-// 1000 x 1000 x 512 6.5, 9.4; 2048 x 256 x 1024 8.7, 11.0; 777 x 1001 x 1500 12.7, 14.5 (fp32
-// 13.0, 13.3); 200 x 300 x 2048 13.5, 12.2.
-constexpr int kF8MadeSide = 64, kF8MadeBlocks = 12;
+// one launch against two, bf16: 17 x 64 x 128 3.9, 5.5; 512 x 512 x 256 5.3, 7.1;
+// 1000 x 1000 x 512 6.5, 8.3; 2048 x 256 x 1024 8.6, 9.9; 256 x 4096 x 1024 9.1, 9.3;
+// 777 x 1001 x 1500 12.6, 12.4; 200 x 300 x 2048 13.5, 11.
+constexpr int kF8MadeSide = 64, kF8MadeBlocks = 8;
 inline bool f8_made(const F8Plan& p, int64_t K) {
     return p.tm == kF8MadeSide && p.splits == 1 && p.tiles_m * p.tiles_n <= 256 && K > 0 &&
            K <= kF8MadeBlocks * kF8Block;
