@@ -18,11 +18,19 @@ inline int64_t f8_scale_bytes(int64_t rows, int64_t cols, int block_rows) {
     return f8_ceil(rows, block_rows) * f8_lds(cols);
 }
 
-// Quantisation and its inverse: one workgroup per 128 x 128 tile.
+// Quantisation: one workgroup of 512 threads per 128 x 128 tile, as many as keep the launch's
+// threads below 2^32 (2^23 - 1). Its inverse: one of 256 threads per 64 x 128.
+constexpr int kF8TileThreads = 512;
 inline int64_t f8_tiles(int64_t rows, int64_t cols) {
     return f8_ceil(rows, kF8Block) * f8_ceil(cols, kF8Block);
 }
-inline int64_t f8_tile_grid(int64_t tiles) { return grid_blocks(tiles, 1); }
+inline int64_t f8_quant_grid(int64_t tiles) {
+    constexpr int64_t most = ((int64_t(1) << 32) - 1) / kF8TileThreads;
+    return tiles < 1 ? 1 : (tiles < most ? tiles : most);
+}
+inline int64_t f8_values_grid(int64_t rows, int64_t cols) {
+    return grid_blocks(f8_ceil(rows, 64) * f8_ceil(cols, kF8Block), 1);
+}
 
 // How a product is cut: tiles of tm x tn of C, each summed by `splits` workgroups.
 struct F8Plan {

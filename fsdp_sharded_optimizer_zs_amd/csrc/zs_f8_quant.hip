@@ -28,7 +28,7 @@ namespace zs {
 namespace {
 
 constexpr int kThreads = kBlockThreads;
-constexpr int kWaves = 8, kTileThreads = 64 * kWaves;  // of a tile to be quantised
+constexpr int kTileThreads = kF8TileThreads, kWaves = kTileThreads / 64;  // of a tile to be quantised
 constexpr int kT = kF8Block;  // side of a tile
 
 // A matrix in memory, row r from element r * ldx on.
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(
 
 hipError_t launch_quantize_f8(const F8Quant& q, int block_rows, hipStream_t stream) {
     const uint32_t tiles = uint32_t(f8_tiles(q.rows, q.cols));  // checked: below 2^31
-    const dim3 grid(unsigned(f8_tile_grid(tiles)));
+    const dim3 grid(unsigned(f8_quant_grid(tiles)));
     const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(kTileThreads), 0, stream, q, q, tiles, 0u);
     };
@@ -382,7 +382,7 @@ hipError_t launch_quantize_f8(const F8Quant& q, int block_rows, hipStream_t stre
 hipError_t launch_quantize2_f8(const F8Quant& one, const F8Quant& two, hipStream_t stream) {
     const uint32_t a = uint32_t(f8_tiles(one.rows, one.cols)),
                    b = uint32_t(f8_tiles(two.rows, two.cols));  // checked: each below 2^30
-    const dim3 grid(unsigned(f8_tile_grid(int64_t(a) + b)));
+    const dim3 grid(unsigned(f8_quant_grid(int64_t(a) + b)));
     if (one.dtype == ZS_BF16)
         hipLaunchKernelGGL((quantize_kernel<ZS_BF16, 1>), grid, dim3(kTileThreads), 0, stream, one, two,
                            a, b);
@@ -394,7 +394,7 @@ hipError_t launch_quantize2_f8(const F8Quant& one, const F8Quant& two, hipStream
 
 hipError_t launch_gather_f8(const F8Quant& q, const F8Shards& src, int block_rows,
                             hipStream_t stream) {
-    const dim3 grid(unsigned(f8_tile_grid(f8_tiles(q.rows, q.cols))));
+    const dim3 grid(unsigned(f8_quant_grid(f8_tiles(q.rows, q.cols))));
     if (q.dtype == ZS_BF16) {
         if (block_rows == 1)
             hipLaunchKernelGGL((gather_kernel<ZS_BF16, 1>), grid, dim3(kTileThreads), 0, stream, q, src);
@@ -416,7 +416,7 @@ hipError_t launch_dequantize_f8(const uint8_t* codes, const uint8_t* scales, int
                                 int64_t ldo, hipStream_t stream) {
     const int64_t ld = f8_ld(cols), lds = f8_lds(cols);
     const int shift = block_rows == 1 ? 0 : 7;
-    const dim3 grid(unsigned(f8_tile_grid(f8_ceil(rows, 64) * f8_ceil(cols, kT))));
+    const dim3 grid(unsigned(f8_values_grid(rows, cols)));
     const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, codes, scales, shift, rows,
                            cols, ld, lds, out, ldo);

@@ -6,14 +6,15 @@
 // than the work is still correct; the cap only keeps the launch legal. A
 // launch's total thread count (workgroups x threads per workgroup) must fit
 // in 32 bits, so with 256-thread workgroups the grid is capped at
-// floor((2^32 - 1) / 256) = 2^24 - 1 workgroups.
+// floor((2^32 - 1) / 256) = 2^24 - 1 workgroups. Kernels with larger workgroups
+// have a cap of their own (zs_f8_grid.h) or a grid of a few hundred.
 #pragma once
 
 #include <stdint.h>
 
 namespace zs {
 
-constexpr int kBlockThreads = 256;  // threads per workgroup, every kernel
+constexpr int kBlockThreads = 256;  // threads per workgroup, where a kernel names no other
 constexpr int64_t kMaxGrid = ((int64_t(1) << 32) - 1) / kBlockThreads;  // 2^24 - 1
 
 // ceil(units / per_block) workgroups, at least 1 and at most kMaxGrid.
