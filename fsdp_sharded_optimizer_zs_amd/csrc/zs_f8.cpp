@@ -335,6 +335,8 @@ ZS_EXPORT zs_status zs_linear_f8(const void* x, int32_t dtype, int64_t M, int64_
     const int64_t N = w->rows, K = w->cols;
     st = check_sizes(who, "x", M, K);
     if (st == ZS_OK) st = check_product_size(who, M, N, K);
+    if (st == ZS_OK && f8_tiles(M, K) > (int64_t(1) << 31) - 1)
+        st = fail(ZS_EINVAL, "%s: x has too many elements", who);
     Range rx, ry;
     if (st == ZS_OK) st = check_dense(who, "x", x, es, M, K, ldx, &rx);
     if (st == ZS_OK) st = check_dense(who, "y", y, ys, M, N, ldy, &ry);
