@@ -1096,20 +1096,38 @@ class F8Matrix:
     scale bytes (contiguous uint8 device tensors, in the layout of zs_f8_layout:
     rows of 128 * ceil(cols / 128) codes and of 4 * ceil(cols / 512) scales, one
     row of scales for each block_rows rows), their type (ZS_E4M3 or ZS_E5M2) and
-    block_rows (1 or 128)."""
+    block_rows (1 or 128). Each call reads and writes the buffers where they are then:
+    their storage may be freed (untyped_storage().resize_(0)) and taken again between
+    calls."""
 
     def __init__(self, codes, scales, rows: int, cols: int, type: int = ZS_E4M3,
                  block_rows: int = 1):
+        self.__dict__.update(codes=codes, scales=scales, rows=int(rows), cols=int(cols),
+                             type=int(type), block_rows=int(block_rows))
+        self._place()
+        self.__dict__["device"] = codes.device
+
+    def _place(self):
+        """Checks the buffers and takes their addresses."""
         uint8 = _torch().uint8
-        n_codes, n_scales = zs_f8_layout(rows, cols, block_rows)
-        _typed(codes, "codes", uint8, n_codes)
-        _typed(scales, "scales", uint8, n_scales)
-        _same_device((codes, scales), "F8Matrix")
-        rows, cols, type, block_rows = int(rows), int(cols), int(type), int(block_rows)
-        self.__dict__.update(
-            codes=codes, scales=scales, rows=rows, cols=cols, type=type, block_rows=block_rows,
-            device=codes.device,
-            _c=ctypes.byref(zs_f8_matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, type, block_rows)))
+        buffers = self.codes, self.scales
+        for t, what, n in zip(buffers, ("codes", "scales"),
+                              zs_f8_layout(self.rows, self.cols, self.block_rows)):
+            _typed(t, what, uint8, n)
+            if t.untyped_storage().nbytes() < t.storage_offset() + n:
+                raise ValueError(f"{what}: the tensor's storage holds less than {n} bytes")
+        _same_device(buffers, "F8Matrix")
+        at = tuple(t.data_ptr() for t in buffers)
+        c = ctypes.byref(zs_f8_matrix(*at, self.rows, self.cols, self.type, self.block_rows))
+        self.__dict__["_placed"] = *at, c
+
+    def _c(self):
+        """The matrix as the library takes it, its buffers where they are now."""
+        codes, scales, c = self._placed
+        if self.codes.data_ptr() != codes or self.scales.data_ptr() != scales:
+            self._place()
+            c = self._placed[2]
+        return c
 
     def __setattr__(self, name, value):
         raise AttributeError(f"F8Matrix.{name} is fixed when the matrix is made")
@@ -1145,7 +1163,7 @@ def _matrix(t, what: str, rows: int = None, cols: int = None):
 
 
 def _c(x):
-    return None if x is None else x._c
+    return None if x is None else x._c()
 
 
 def _quantized_shape(out, out_t):
@@ -1184,7 +1202,7 @@ def zs_dequantize_f8(x: F8Matrix, out, stream=None) -> None:
     """out (a bf16 or float32 matrix, its rows contiguous) = the values of x."""
     code, ld = _matrix(out, "out", x.rows, x.cols)
     _one_device((x, out), "zs_dequantize_f8")
-    _enqueue(load().zs_dequantize_f8, out, stream, x._c, code, out.data_ptr(), ld)
+    _enqueue(load().zs_dequantize_f8, out, stream, x._c(), code, out.data_ptr(), ld)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -1233,7 +1251,7 @@ def zs_matmul_f8(a: F8Matrix, b: F8Matrix, c, accumulate: bool = False, workspac
         raise ValueError("a and b must have the same number of columns")
     ws = _workspace(workspace, zs_matmul_f8_workspace(a.rows, b.rows, a.cols))
     _one_device([a, b, c] + ([] if workspace is None else [workspace]), "zs_matmul_f8")
-    _enqueue(load().zs_matmul_f8, c, stream, a._c, b._c, code, c.data_ptr(), ld, 1 if accumulate else 0, ws)
+    _enqueue(load().zs_matmul_f8, c, stream, a._c(), b._c(), code, c.data_ptr(), ld, 1 if accumulate else 0, ws)
 
 
 def zs_linear_f8(x, w: F8Matrix, y, workspace=None, type: int = ZS_E4M3, stream=None) -> None:
@@ -1249,7 +1267,7 @@ def zs_linear_f8(x, w: F8Matrix, y, workspace=None, type: int = ZS_E4M3, stream=
     y_code, ldy = _matrix(y, "y", M, w.rows)
     ws = _workspace(workspace, zs_linear_f8_workspace(M, w.rows, w.cols))
     _one_device([x, w, y] + ([] if workspace is None else [workspace]), "zs_linear_f8")
-    _enqueue(load().zs_linear_f8, y, stream, x.data_ptr(), code, M, ldx, int(type), w._c, y_code,
+    _enqueue(load().zs_linear_f8, y, stream, x.data_ptr(), code, M, ldx, int(type), w._c(), y_code,
              y.data_ptr(), ldy, ws)
 
 
@@ -1285,7 +1303,7 @@ def zs_linear_f8_backward(dy, x, w_t: F8Matrix, dx, dw, workspace, grad_type: in
     ws = _workspace(workspace, zs_linear_f8_backward_workspace(M, N, K))
     _one_device(used, "zs_linear_f8_backward")
     _enqueue(load().zs_linear_f8_backward, dy, stream, dy.data_ptr(), lddy, *args["x"], code, M, N, K,
-             int(grad_type), w_t._c if dx is not None else None, *args["dx"], *args["dw"],
+             int(grad_type), w_t._c() if dx is not None else None, *args["dx"], *args["dw"],
              1 if accumulate else 0, ws)
 
 
