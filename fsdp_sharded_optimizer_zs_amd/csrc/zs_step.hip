@@ -309,6 +309,10 @@ struct Clipped {
         return sum.one(c, i) * *factor;
     }
 };
+template <class Sum>
+constexpr bool kIsClipped = false;
+template <class Sum>
+constexpr bool kIsClipped<Clipped<Sum>> = true;
 
 // One AdamW element, in the fixed order, every operation rounded on its own.
 __device__ __forceinline__ void adamw1(float& p, float& m, float& v, float g,
@@ -615,46 +619,59 @@ struct Job {
     const NormJob* norm;  // with out: also the sum of squares
 };
 
+// On 16-byte aligned buffers. A clipped reduce is a step's, and not timed: no other kernel of it
+// is compiled.
 template <int DT, class Sum>
-hipError_t launch_job(const Job& j, const PtrPack& c, const Sum& sum, hipStream_t stream) {
+hipError_t launch_tiled(const Job& j, const PtrPack& c, const Sum& sum, hipStream_t stream) {
     constexpr int TP = ZS_STEP_TILES;
     static_assert(kThreads == kBlockThreads, "grid arithmetic assumes 256-thread workgroups");
-    const unsigned tiled = unsigned(step_tiled_grid(j.S, TP));
-    const unsigned scalar = unsigned(step_scalar_grid(j.S));
-    if (j.norm != nullptr) {
-        if (j.aligned)
-            hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, TP>),
-                               dim3(unsigned(reduce_norm_grid(j.S, TP))), dim3(kThreads), 0, stream,
-                               j.out, j.S, c, sum, *j.norm);
-        else
-            hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, 0>),
-                               dim3(unsigned(reduce_norm_grid(j.S, 0))), dim3(kThreads), 0, stream,
-                               j.out, j.S, c, sum, *j.norm);
-    } else if (j.out == nullptr && j.ev_start != nullptr) {
+    const dim3 grid(unsigned(step_tiled_grid(j.S, TP))), block(kThreads);
+    const auto step = [&] {
+        hipLaunchKernelGGL((adamw_vec_kernel<DT, Sum, TP>), grid, block, 0, stream, j.p, j.m, j.v,
+                           j.w, j.S, c, sum, j.k);
+    };
+    if constexpr (kIsClipped<Sum>) {
+        step();
+    } else if (j.norm != nullptr) {
+        hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, TP>),
+                           dim3(unsigned(reduce_norm_grid(j.S, TP))), block, 0, stream, j.out, j.S,
+                           c, sum, *j.norm);
+    } else if (j.out != nullptr) {
+        hipLaunchKernelGGL((reduce_vec_kernel<DT, Sum, TP>), grid, block, 0, stream, j.out, j.S, c,
+                           sum);
+    } else if (j.ev_start != nullptr) {
         // timed: the runtime ties the two events to this dispatch's start and
         // end timestamps, with no marker packets around it
-        if (j.aligned)
-            hipExtLaunchKernelGGL((adamw_vec_kernel<DT, Sum, TP>), dim3(tiled), dim3(kThreads), 0,
-                                  stream, j.ev_start, j.ev_stop, 0, j.p, j.m, j.v, j.w, j.S, c,
-                                  sum, j.k);
-        else
-            hipExtLaunchKernelGGL((adamw_scalar_kernel<DT, Sum>), dim3(scalar), dim3(kThreads), 0,
-                                  stream, j.ev_start, j.ev_stop, 0, j.p, j.m, j.v, j.w, j.S, c,
-                                  sum, j.k);
-    } else if (j.out == nullptr) {
-        if (j.aligned)
-            hipLaunchKernelGGL((adamw_vec_kernel<DT, Sum, TP>), dim3(tiled), dim3(kThreads), 0,
-                               stream, j.p, j.m, j.v, j.w, j.S, c, sum, j.k);
-        else
-            hipLaunchKernelGGL((adamw_scalar_kernel<DT, Sum>), dim3(scalar), dim3(kThreads), 0,
-                               stream, j.p, j.m, j.v, j.w, j.S, c, sum, j.k);
+        hipExtLaunchKernelGGL((adamw_vec_kernel<DT, Sum, TP>), grid, block, 0, stream, j.ev_start,
+                              j.ev_stop, 0, j.p, j.m, j.v, j.w, j.S, c, sum, j.k);
     } else {
-        if (j.aligned)
-            hipLaunchKernelGGL((reduce_vec_kernel<DT, Sum, TP>), dim3(tiled), dim3(kThreads), 0,
-                               stream, j.out, j.S, c, sum);
-        else
-            hipLaunchKernelGGL((reduce_scalar_kernel<DT, Sum>), dim3(scalar), dim3(kThreads), 0,
-                               stream, j.out, j.S, c, sum);
+        step();
+    }
+    return hipGetLastError();
+}
+
+// On buffers of any alignment, an element a lane.
+template <int DT, class Sum>
+hipError_t launch_scalar(const Job& j, const PtrPack& c, const Sum& sum, hipStream_t stream) {
+    const dim3 grid(unsigned(step_scalar_grid(j.S))), block(kThreads);
+    const auto step = [&] {
+        hipLaunchKernelGGL((adamw_scalar_kernel<DT, Sum>), grid, block, 0, stream, j.p, j.m, j.v,
+                           j.w, j.S, c, sum, j.k);
+    };
+    if constexpr (kIsClipped<Sum>) {
+        step();
+    } else if (j.norm != nullptr) {
+        hipLaunchKernelGGL((reduce_norm_kernel<DT, Sum, 0>),
+                           dim3(unsigned(reduce_norm_grid(j.S, 0))), block, 0, stream, j.out, j.S,
+                           c, sum, *j.norm);
+    } else if (j.out != nullptr) {
+        hipLaunchKernelGGL((reduce_scalar_kernel<DT, Sum>), grid, block, 0, stream, j.out, j.S, c,
+                           sum);
+    } else if (j.ev_start != nullptr) {
+        hipExtLaunchKernelGGL((adamw_scalar_kernel<DT, Sum>), grid, block, 0, stream, j.ev_start,
+                              j.ev_stop, 0, j.p, j.m, j.v, j.w, j.S, c, sum, j.k);
+    } else {
+        step();
     }
     return hipGetLastError();
 }
@@ -664,15 +681,15 @@ hipError_t launch_job(const Job& j, const PtrPack& c, const Sum& sum, hipStream_
 // kernels take the runtime form only.
 template <int DT, template <int, int> class SumT, class Make>
 hipError_t dispatch_nc(const Job& j, const PtrPack& c, int nc, Make make, hipStream_t stream) {
-    if (!j.aligned) return launch_job<DT>(j, c, make(SumT<DT, 0>{}), stream);
+    if (!j.aligned) return launch_scalar<DT>(j, c, make(SumT<DT, 0>{}), stream);
     switch (nc) {
-        case 1: return launch_job<DT>(j, c, make(SumT<DT, 1>{}), stream);
-        case 2: return launch_job<DT>(j, c, make(SumT<DT, 2>{}), stream);
-        case 4: return launch_job<DT>(j, c, make(SumT<DT, 4>{}), stream);
-        case 8: return launch_job<DT>(j, c, make(SumT<DT, 8>{}), stream);
-        case 16: return launch_job<DT>(j, c, make(SumT<DT, 16>{}), stream);
-        case 32: return launch_job<DT>(j, c, make(SumT<DT, 32>{}), stream);
-        default: return launch_job<DT>(j, c, make(SumT<DT, 0>{}), stream);
+        case 1: return launch_tiled<DT>(j, c, make(SumT<DT, 1>{}), stream);
+        case 2: return launch_tiled<DT>(j, c, make(SumT<DT, 2>{}), stream);
+        case 4: return launch_tiled<DT>(j, c, make(SumT<DT, 4>{}), stream);
+        case 8: return launch_tiled<DT>(j, c, make(SumT<DT, 8>{}), stream);
+        case 16: return launch_tiled<DT>(j, c, make(SumT<DT, 16>{}), stream);
+        case 32: return launch_tiled<DT>(j, c, make(SumT<DT, 32>{}), stream);
+        default: return launch_tiled<DT>(j, c, make(SumT<DT, 0>{}), stream);
     }
 }
 
@@ -692,14 +709,15 @@ hipError_t dispatch(const Job& j, const PtrPack& c, int nd, int R, bool rnd, hip
 template <int DT>
 hipError_t dispatch_clip(const Job& j, const PtrPack& c, int nd, int R, bool rnd,
                          const float* factor, hipStream_t stream) {
-    const float inv_n = j.k.inv_n;
-    if (R == 1 && !rnd) {
-        if (nd == 1 && j.aligned)
-            return launch_job<DT>(j, c, Clipped<FlatSum<DT, 1>>{{nd, inv_n}, factor}, stream);
-        return launch_job<DT>(j, c, Clipped<FlatSum<DT, 0>>{{nd, inv_n}, factor}, stream);
-    }
-    return launch_job<DT>(j, c, Clipped<HybridSum<DT, 0>>{{nd, R, rnd ? 1 : 0, inv_n}, factor},
-                          stream);
+    const Clipped<FlatSum<DT, 0>> flat{{nd, j.k.inv_n}, factor};
+    const Clipped<HybridSum<DT, 0>> hybrid{{nd, R, rnd ? 1 : 0, j.k.inv_n}, factor};
+    if (R != 1 || rnd)
+        return j.aligned ? launch_tiled<DT>(j, c, hybrid, stream)
+                         : launch_scalar<DT>(j, c, hybrid, stream);
+    if (!j.aligned) return launch_scalar<DT>(j, c, flat, stream);
+    if (nd == 1)
+        return launch_tiled<DT>(j, c, Clipped<FlatSum<DT, 1>>{{nd, j.k.inv_n}, factor}, stream);
+    return launch_tiled<DT>(j, c, flat, stream);
 }
 
 }  // namespace
