@@ -169,11 +169,13 @@ hipError_t product(const zs_f8_matrix& a, const zs_f8_matrix& b, int dtype, void
     return launch_matmul_f8(p, nullptr, plan.tm, a.type, b.type, dtype, stream);
 }
 
-// Whether a linear layer's forward pass makes its codes on the way.
-bool is_few(int64_t M, int64_t N, int64_t K) { return f8_plan(M, N, K).tm == kF8Few; }
-
+// Few rows and small layers make their codes on the way and place none. (Small layers do not
+// count either: theirs is the least that a layer of more than kF8Few rows asks for.)
 int64_t linear_bytes(int64_t M, int64_t N, int64_t K) {
-    return is_few(M, N, K) ? 0 : kF8CountBytes + partial_bytes(M, N, K) + placed_bytes(M, K);
+    const F8Plan plan = f8_plan(M, N, K);
+    if (plan.tm == kF8Few) return 0;
+    if (f8_made(plan, K)) return kF8CountBytes;
+    return kF8CountBytes + partial_bytes(M, N, K) + placed_bytes(M, K);
 }
 
 int64_t groups_of(const F8Plan& p) { return p.tiles_m * p.tiles_n * p.splits; }

@@ -1,6 +1,5 @@
-"""Limits of the 8-bit matrices' entry points on the host: sizes that the kernels do not count."""
-import pytest
-
+"""Sizes at the 8-bit matrices' entry points on the host: what the kernels do not count, and the
+workspaces that layers ask for."""
 import fsdp_sharded_optimizer_zs_amd as zs
 from test_f8_cpu import A, lib, linear, mat, no_gpu  # noqa: F401
 
@@ -16,3 +15,15 @@ def test_linear_refuses_more_tiles_of_x_than_a_launch_counts(lib):  # noqa: F811
     for M in (2**23 + 1, 2**24, 2**30 - 64):
         assert call(M) == zs.ZS_EINVAL, M
         assert "x has too many elements" in zs.zs_last_error()
+
+
+def test_layers_that_place_no_codes_ask_for_none(lib):  # noqa: F811
+    """Layers of one 64 x 64 tile a CU at most and K up to 1,024 (of more than 16 rows) make their codes on
+    the way: their workspace does not grow with M x K. Others place M rows of codes and scales."""
+    least = zs.zs_linear_f8_workspace(17, 64, 256)
+    assert 0 < least <= 1 << 14
+    for M, N, K in ((40, 64, 256), (512, 512, 256), (1000, 1000, 512), (2048, 256, 1024), (777, 1001, 1024),
+                    (16384, 64, 1024)):
+        assert zs.zs_linear_f8_workspace(M, N, K) == least, (M, N, K)
+    for M, N, K in ((777, 1001, 1025), (777, 1001, 1500), (512, 512, 4096), (4096, 4096, 1024)):
+        assert zs.zs_linear_f8_workspace(M, N, K) >= least + M * K, (M, N, K)
