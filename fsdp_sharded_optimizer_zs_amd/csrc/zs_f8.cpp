@@ -180,10 +180,9 @@ int64_t linear_bytes(int64_t M, int64_t N, int64_t K) {
 
 int64_t groups_of(const F8Plan& p) { return p.tiles_m * p.tiles_n * p.splits; }
 
-zs_status check_product_size(const char* who, int64_t M, int64_t N, int64_t K) {
+zs_status check_product_size(const char* who, int64_t M, int64_t N) {
     if (f8_ceil(M, 64) * f8_ceil(N, 64) > kMaxGrid)
         return fail(ZS_EINVAL, "%s: the product has too many elements", who);
-    (void)K;
     return ZS_OK;
 }
 
@@ -295,7 +294,7 @@ ZS_EXPORT zs_status zs_matmul_f8(const zs_f8_matrix* a, const zs_f8_matrix* b, i
                     (long long)b->cols);
     if (accumulate != 0 && accumulate != 1)
         return fail(ZS_EINVAL, "%s: accumulate must be 0 or 1", who);
-    st = check_product_size(who, a->rows, b->rows, a->cols);
+    st = check_product_size(who, a->rows, b->rows);
     if (st != ZS_OK) return st;
     Range rc;
     st = check_dense(who, "c", c, es, a->rows, b->rows, ldc, &rc);
@@ -336,7 +335,7 @@ ZS_EXPORT zs_status zs_linear_f8(const void* x, int32_t dtype, int64_t M, int64_
     if (st != ZS_OK) return st;
     const int64_t N = w->rows, K = w->cols;
     st = check_sizes(who, "x", M, K);
-    if (st == ZS_OK) st = check_product_size(who, M, N, K);
+    if (st == ZS_OK) st = check_product_size(who, M, N);
     if (st == ZS_OK && f8_tiles(M, K) > (int64_t(1) << 31) - 1)
         st = fail(ZS_EINVAL, "%s: x has too many elements", who);
     Range rx, ry;
@@ -406,8 +405,8 @@ ZS_EXPORT zs_status zs_linear_f8_backward(const void* dy, int64_t lddy, const vo
         return fail(ZS_EINVAL, "%s: accumulate must be 0 or 1", who);
     int64_t need = 0;
     st = zs_linear_f8_backward_workspace(M, N, K, &need);
-    if (st == ZS_OK) st = check_product_size(who, M, K, N);
-    if (st == ZS_OK) st = check_product_size(who, N, K, M);
+    if (st == ZS_OK) st = check_product_size(who, M, K);
+    if (st == ZS_OK) st = check_product_size(who, N, K);
     if (st == ZS_OK && (f8_tiles(M, N) >= (int64_t(1) << 30) || f8_tiles(M, K) >= (int64_t(1) << 30)))
         st = fail(ZS_EINVAL, "%s: dy or x has too many elements", who);
     if (st != ZS_OK) return st;
