@@ -1258,8 +1258,8 @@ def zs_linear_f8(x, w: F8Matrix, y, workspace=None, type: int = ZS_E4M3, stream=
     """y (M x N, bf16 or float32) = Q(x) w^T: x (M x K, bf16 or float32) quantised to
     8-bit codes of `type` with a scale for each 128 elements of a row, times the 8-bit
     weights w (N x K). workspace: uint8 device tensor of zs_linear_f8_workspace(M, N, K)
-    bytes (0 for few rows), zeroed once; one for each of calls that may run at the same
-    time."""
+    bytes (0 for few rows: include/zs.h says how many for which K), zeroed once; one for
+    each of calls that may run at the same time."""
     code, ldx = _matrix(x, "x")
     if x.shape[1] != w.cols:
         raise ValueError(f"x must have {w.cols} columns")

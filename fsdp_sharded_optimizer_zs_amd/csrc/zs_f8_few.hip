@@ -1,20 +1,28 @@
 // Products with few rows of a (serving: one new token, a handful at once) for gfx950: the
 // weights b are read once, and that is the time.
 //
+// All of a's codes have to fit LDS beside a group of b for each wavefront: 16 rows up to K = 4,864,
+// 8 up to 9,856, 1 up to 79,232 (f8_plan); past that two launches of the larger products' way.
+//
 // A workgroup takes `rows` rows of b, so many that 256 workgroups, one a CU, share b evenly.
 // Half of its wavefronts read and multiply: its rows go 16 at a time to `splits` of them, each
 // of which takes every splits-th group of 4 blocks along K. A group's 8 KiB of codes go
 // straight to the wavefront's own part of LDS, whole 512-byte pieces of rows at a time (loads
-// of 64 bytes a row into registers reached 3 TB/s), the next group's under way meanwhile, and
-// from there to v_mfma_scale_f32_16x16x128_f8f6f4 as its first operand. The other half first
+// of 64 bytes a row into registers reached 3 TB/s), and from there to
+// v_mfma_scale_f32_16x16x128_f8f6f4 as its first operand. Where LDS has room for two groups
+// (1 row up to K = 12,160, 2 up to 6,016, 4 up to 2,944, 16 up to 640) the next one is under way
+// meanwhile; where it has one, a wavefront sends for the next when it has read the present one
+// out, and its loads rest while it multiplies. The other half of the wavefronts first
 // puts all of a into LDS as codes, while the first codes of b are under way: it copies them,
 // or quantises a's values (8 elements a lane, a block in the 16 lanes of a DPP row), which
 // spares a launch. a is the second operand, its rows past M zeros. The sums of a group's
 // wavefronts are added through LDS in their order. C in bf16 and fp32 as in the large products.
 //
-// Measured from memory, us (TB/s of codes): 1 x 4096 x 4096 7.4 (2.3), 1 x 4096 x 11008 11.2
-// (4.0), 16 x 11008 x 4096 17.4 (2.6), 1 x 32000 x 8192 50 (5.2); a plain read of 45 MB takes
-// 8.3. What is left is the start: the launch and the first loads' way, some 4 us.
+// Measured, us (TB/s of codes), with 1.2 GB of weights in turn, so that they come from HBM / the
+// same weights again, from the caches: 1 x 4096 x 4096 7.4 (2.3) / 6.4, 1 x 4096 x 11008 13.7
+// (3.3) / 10.2, 1 x 11008 x 4096 12.8 (3.5) / 10.4, 16 x 11008 x 4096 20.4 (2.2) / 16.7,
+// 1 x 32000 x 8192 50 (5.2) / 40; a plain read of 45 MB in turn takes 8.3. With one row what is left is
+// the start, the launch and the first loads' way, some 4 us; with more, the loads' rests too.
 
 #include "zs_f8_dev.h"
 

@@ -16,15 +16,22 @@
 //
 // C in bf16: v_mfma_scale_f32_32x32x64_f8f6f4 multiplies with both scale bytes. Of 8
 // neighbouring products it drops what is below 2^-13 of the largest one's power of two
-// (measured; the sums of the eights are added in fp32): on normal data 2^-16 of the result, 2^7
-// below the rounding to bf16. C in fp32 (EXACT): the codes, times their scales, become bf16
+// (measured; the sums of the eights are added in fp32): on normal data 2^-16 of the results'
+// norm, 2^7 below the rounding to bf16, and 2^-14.5 where a few columns are much larger than
+// the others, to either side alike. One result in 40 or fewer is then bf16's other neighbour
+// of the exact sum; the error against 64 bits stays the rounding's (1.6572e-3 of the norm for
+// 1.6568e-3). C in fp32 (EXACT): the codes, times their scales, become bf16
 // exactly and v_mfma_f32_32x32x16_bf16 sums them in fp32, at half of the rate.
 //
-// Measured on normal data (C in bf16 / fp32): 8192 x 8192 x 8192 434 us, 2,530 TFLOP/s / 785 us,
-// 1,400; 11008 x 4096 x 4096 169 us, 2,190 / 287 us, 1,290; 512 x 11008 x 4096 36 us; the same
-// card's library in bf16 takes 664 and 393 us for the first two. On zeros the first takes 340 us
-// (3,230 TFLOP/s; 621 us in fp32): what bounds the rest is the power that the matrix cores draw,
-// the clock falls to about 1.75 GHz. Wavefronts of 128 x 128 (4 a workgroup) had the same rate
+// Measured on normal data, the same operands again (C in bf16 / fp32): 8192 x 8192 x 8192 434 us,
+// 2,530 TFLOP/s / 785 us, 1,400; 11008 x 4096 x 4096 169 us, 2,190 / 287 us, 1,290;
+// 512 x 11008 x 4096 36 us; the same card's library in bf16 takes 664 and 393 us for the first two.
+// Other cards: 478 / 833 us and, with other operands in turn, 185 / 318, the library 818 for the
+// first. On zeros the first takes 340 us (3,230 TFLOP/s; 621 us in fp32): at 8192, where every
+// round of tiles fills the CUs, the power that the matrix cores draw bounds it, the clock falls to
+// about 1.75 GHz. 11008 x 4096 is 688 tiles on 256 CUs, three rounds for 2.69 rounds' work: a step
+// of 128 costs 1.76 us there for 1.70 (on zeros 1.46 for 1.33), and the last round, with 80 CUs
+// idle, up to a tenth of the time. Wavefronts of 128 x 128 (4 a workgroup) had the same rate
 // and a longer epilogue.
 //
 // The matrix instruction's first operand is b and its second a: a lane then holds 4

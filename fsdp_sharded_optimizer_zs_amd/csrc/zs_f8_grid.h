@@ -56,14 +56,20 @@ constexpr int64_t f8_few_lds(int depth, int64_t M, int64_t blocks) {
 
 // Tiles of 256, 128 or 64 squared: the larger one moves less through LDS for each product,
 // the smaller ones fill 256 CUs with less. The costs of a step of 128 along K for each tile
-// that a CU takes are measured, in hundredths of a microsecond (C in fp32: 290, 93 and 33, in
-// much the same ratios). With them, in us, M x N x K and C in bf16: 3000 x 3000 x 3000
+// that a CU takes are measured, in hundredths of a microsecond, for C in bf16. C in fp32 is cut
+// alike, since the workspace is asked for by sizes alone; its own costs, 290, 93 and 33, favour
+// small tiles more, so that it loses where rounds of tiles fall badly (2624 x 11840 x 4096 by
+// 256 293, by 128 241; 3000 x 3000 x 3000 71, 68) and wins as much elsewhere (384 x 10944 x 4096
+// 50 by 128, 58 by the 64 in one part that those costs pick). Measured with the same operands
+// again, in us, M x N x K and C in bf16: 3000 x 3000 x 3000
 // 256: 39, 128: 46, 64: 58; 2048 x 4096 x 4096 47, 43, 67; 512 x 4096 x 4096 46, 19, 17.
 // CUs that tiles of 128 or 64 leave idle take parts of K, of 16 steps at least, if joining them
 // (writing the partial sums, and one workgroup a tile reading its own again) costs less than
 // the steps it saves: 512 x 4096 x 11008 64: 47, 128: 51, 128 in 2 parts: 37; 256 x 256 x 8192
 // 64 in 1, 2, 4 parts 19, 13, 10; 1024 x 1024 x 4096 64 in 1 and 2 parts 11, 13. (256 in 2 parts
 // would gain where K is past 10,000 alone, 2048 x 4096 x 11008 99 for 114, and take 64 MiB.)
+// With other operands in turn, from memory, these products take 5 to 7 us more
+// (512 x 4096 x 11008 46 to 48).
 inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
     constexpr int kCus = 256;
     const int side[3] = {256, 128, 64}, cost[3] = {150, 58, 25};
@@ -96,7 +102,7 @@ inline F8Plan f8_plan(int64_t M, int64_t N, int64_t K) {
 // Whether a linear layer's product makes a's codes on the way, in every workgroup those of its
 // own rows: one launch instead of two, where a CU takes one tile at most and K is short enough
 // that making the same codes again for every 64 columns costs less than a launch. Measured, us,
-// one launch against two, bf16: 17 x 64 x 128 3.9, 5.5; 512 x 512 x 256 5.3, 7.1;
+// one launch against two, bf16, the same operands again: 17 x 64 x 128 3.9, 5.5; 512 x 512 x 256 5.3, 7.1;
 // 1000 x 1000 x 512 6.5, 8.3; 2048 x 256 x 1024 8.6, 9.9; 256 x 4096 x 1024 9.1, 9.3;
 // 777 x 1001 x 1500 12.6, 12.4; 200 x 300 x 2048 13.5, 11.
 constexpr int kF8MadeSide = 64, kF8MadeBlocks = 8;

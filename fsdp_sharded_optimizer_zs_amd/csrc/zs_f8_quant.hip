@@ -9,14 +9,16 @@
 // are one word of transposed codes. Those words are exchanged through LDS (16 KiB) so that the
 // transpose leaves in 16-byte pieces of whole 128-byte runs too.
 //
-// Memory bounds them: 2 or 4 bytes read and 1 written for each element and form. Measured from
-// memory, 4096 x 11008 in us (TB/s), as it is / transposed / both / both from 4 shards:
-//   bf16, blocks of 1 x 128      27.9 (4.9) / 28.5 (4.8) / 37.5 (4.8) / 43.6
-//   bf16, 128 x 128              26.6 (5.1) / 27.7 (4.9) / 35.0 (5.2) / 39.4
-//   fp32, 1 x 128                49.9 (4.5) / 53.5 (4.2) / 60.4 (4.5) / 64.6
-//   fp32, 128 x 128              45.5 (5.0) / 49.8 (4.5) / 53.7 (5.0) / 55.8
-// and back to bf16 22.9 (5.9). Tiles by 4 wavefronts of twice the rows: 28.5, 28.0, 39.5 and
-// 49.0 in the first line, 24.5, 25.5, 33.2, 40.0 in the second; a small matrix, whose tiles
+// Memory bounds them: 2 or 4 bytes read and 1 written for each element and form. Measured with
+// 1.2 GB of matrices in turn, so that they come from HBM, launches in a row, 4096 x 11008 in us
+// (TB/s), as it is / transposed / both / both from 4 shards:
+//   bf16, blocks of 1 x 128      29.4 (4.6) / 29.8 (4.5) / 40.5 (4.5) / 43.4
+//   bf16, 128 x 128              28.4 (4.8) / 29.0 (4.7) / 38.2 (4.7) / 38.5
+//   fp32, 1 x 128                51.8 (4.4) / 53.3 (4.2) / 61.5 (4.4) / 66.3
+//   fp32, 128 x 128              47.5 (4.7) / 50.7 (4.4) / 58.0 (4.7) / 59.7
+// and back to bf16 26.4 (5.1). Tiles by 4 wavefronts of twice the rows, with four matrices in turn,
+// against these: 28.5, 28.0, 39.5 and 49.0 in the first line for 27.9, 28.5, 37.5 and 43.6, in
+// the second 24.5, 25.5, 33.2, 40.0 for 26.6, 27.7, 35.0, 39.4; a small matrix, whose tiles
 // leave CUs idle, takes longer by them (2048 x 1024, both forms 6.5 us against 5.6, from shards
 // 7.5 against 5.7), and fp32 needs twice the registers.
 

@@ -17,6 +17,17 @@ def test_linear_refuses_more_tiles_of_x_than_a_launch_counts(lib):  # noqa: F811
         assert "x has too many elements" in zs.zs_last_error()
 
 
+def test_few_rows_without_a_workspace_are_those_of_the_header(lib):  # noqa: F811
+    """M <= 16 and M * (129 * ceil(K / 128) + 16) <= 79872."""
+    for M in range(0, 19):
+        for K in (0, 1, 128, 640, 4096, 4864, 4865, 9856, 9857, 11_008, 19_712, 19_713, 79_232, 79_233, 2**22):
+            few = M <= 16 and M * (129 * -(-K // 128) + 16) <= 79872
+            for N in (1, 64, 4096):
+                assert (zs.zs_linear_f8_workspace(M, N, K) == 0) == few, (M, N, K)
+    for M, K in ((16, 4864), (8, 9856), (4, 19_712), (1, 79_232)):
+        assert zs.zs_linear_f8_workspace(M, 4096, K) == 0 < zs.zs_linear_f8_workspace(M, 4096, K + 1)
+
+
 def test_layers_that_place_no_codes_ask_for_none(lib):  # noqa: F811
     """Layers of one 64 x 64 tile a CU at most and K up to 1,024 (of more than 16 rows) make their codes on
     the way: their workspace does not grow with M x K. Others place M rows of codes and scales."""
